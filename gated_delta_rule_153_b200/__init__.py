@@ -12,6 +12,7 @@ states [B,H,dv,dk] fp32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -33,13 +34,23 @@ EXPORTS = ("gdn_chunk_fwd_workspace", "gdn_chunk_fwd", "gdn_chunk_bwd_workspace"
            "gdn_product_bwd_workspace", "gdn_product_bwd", "gdn_chunk_fwd_varlen_workspace",
            "gdn_chunk_fwd_varlen", "gdn_chunk_bwd_varlen_workspace", "gdn_chunk_bwd_varlen",
            "gdn_tree_verify", "gdn_tree_commit", "gdn_short_conv_fwd",
-           "gdn_short_conv_bwd_workspace", "gdn_short_conv_bwd")
+           "gdn_short_conv_bwd_workspace", "gdn_short_conv_bwd",
+           "gdn_decay_fwd_workspace", "gdn_decay_fwd", "gdn_decay_bwd_workspace",
+           "gdn_decay_bwd", "gdn_decay_step", "gdn_tree_attn_workspace", "gdn_tree_attn",
+           "gdn_tree_append", "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace",
+           "gdn_gated_norm_bwd")
 
 
 class gdn_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("chunk", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("gate", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class gdn_decay_dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class GdnError(RuntimeError):
@@ -129,6 +140,33 @@ def lib() -> ctypes.CDLL:
             L.gdn_short_conv_bwd_workspace.restype = sz
             L.gdn_short_conv_bwd.argtypes = [i, i, i, i, i, i, i, vp, fp, vp, vp, fp, vp, sz, vp]
             L.gdn_short_conv_bwd.restype = i
+            dd, ll = ctypes.POINTER(gdn_decay_dims), ctypes.c_longlong
+            L.gdn_decay_fwd_workspace.argtypes = [dd, i]
+            L.gdn_decay_fwd_workspace.restype = sz
+            L.gdn_decay_fwd.argtypes = [dd, vp, i, vp, vp, vp, fp, fp, vp, fp, vp, sz, vp]
+            L.gdn_decay_fwd.restype = i
+            L.gdn_decay_bwd_workspace.argtypes = [dd, i]
+            L.gdn_decay_bwd_workspace.restype = sz
+            L.gdn_decay_bwd.argtypes = [dd, vp, i, vp, vp, vp, fp, fp, vp, fp, vp, vp, vp, fp, fp,
+                                        vp, sz, vp]
+            L.gdn_decay_bwd.restype = i
+            L.gdn_decay_step.argtypes = [i, i, i, i, i, i, f, vp, vp, vp, fp, fp, vp, vp]
+            L.gdn_decay_step.restype = i
+            L.gdn_tree_attn_workspace.argtypes = [i, i, i, i, i, i, i, i]
+            L.gdn_tree_attn_workspace.restype = sz
+            L.gdn_tree_attn.argtypes = [i, i, i, i, i, i, f, i, vp, vp, vp, vp, i, i, i, vp, vp, vp,
+                                        vp, vp, vp, sz, vp]
+            L.gdn_tree_attn.restype = i
+            L.gdn_tree_append.argtypes = [i, i, i, i, i, vp, vp, vp, vp, i, i, i, vp, vp, vp, vp,
+                                          vp, vp, vp]
+            L.gdn_tree_append.restype = i
+            L.gdn_gated_norm_fwd.argtypes = [ll, i, i, i, i, i, f, vp, vp, fp, vp, vp]
+            L.gdn_gated_norm_fwd.restype = i
+            L.gdn_gated_norm_bwd_workspace.argtypes = [ll, i, i, i]
+            L.gdn_gated_norm_bwd_workspace.restype = sz
+            L.gdn_gated_norm_bwd.argtypes = [ll, i, i, i, i, i, f, vp, vp, fp, vp, vp, vp, fp, vp,
+                                             sz, vp]
+            L.gdn_gated_norm_bwd.restype = i
             L.gdn_profile_begin.argtypes = [i]
             L.gdn_profile_begin.restype = i
             L.gdn_profile_end.argtypes = [ctypes.POINTER(ctypes.c_float),
@@ -652,3 +690,269 @@ def gdn_short_conv_bwd(x, w, dy, *, l2norm=True, workspace=None, stream=None):
                                   _stream(stream))
     _check(st, "gdn_short_conv_bwd")
     return dx, dw
+
+
+# ---- linear attention with a decay per head ----------------------------------
+@contextlib.contextmanager
+def _on(ref, stream, *others):
+    """The device of ``ref`` and, for the call's allocations, the stream it runs
+    on: what the call allocates then belongs to that stream.  Every tensor of
+    the call must be on the same device."""
+    import torch
+    for t in others:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"tensors on {ref.device} and {t.device} in one call")
+    with torch.cuda.device(ref.device):
+        if stream is None:
+            yield torch.cuda.current_stream()
+        else:
+            if stream.device != ref.device:
+                raise ValueError(f"stream of {stream.device} for tensors on {ref.device}")
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def _given(t, name, like_shape, dtype, device):
+    """``t`` checked as an output, or a new tensor when it is None."""
+    import torch
+    if t is None:
+        return torch.empty(like_shape, dtype=dtype, device=device)
+    _need(t, name, dtype, like_shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _scratch(nbytes, device, workspace):
+    """The caller's workspace, checked, or a new one."""
+    import torch
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device:
+        raise TypeError(f"workspace must be a tensor on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if _nbytes(workspace) < nbytes:
+        raise ValueError(f"workspace too small: need {nbytes} bytes")
+    return workspace
+
+
+def _decay_inputs(q, k, v, g, h0, cu_seqlens, scale):
+    import torch
+    _need(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hk, dk]")
+    B, T, Hk, dk = q.shape
+    _need(k, "k", q.dtype, (B, T, Hk, dk))
+    _need(v, "v", q.dtype)
+    if v.dim() != 4 or tuple(v.shape[:2]) != (B, T):
+        raise ValueError("v must be [B, T, H, dv] matching q")
+    H, dv = v.shape[2], v.shape[3]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} value heads cannot share {Hk} key heads")
+    _need(g, "g", torch.float32, (B, T, H))
+    nseq = 0
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [nseq + 1] int32")
+        if B != 1:
+            raise ValueError("packed sequences take q [1, total_tokens, Hk, dk]")
+        nseq = cu_seqlens.numel() - 1
+    states = (nseq or B, H, dv, dk)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, states)
+    return gdn_decay_dims(B, T, H, Hk, dk, dv, _dtype_code(q), float(scale)), nseq, states
+
+
+def gdn_decay_fwd_workspace(dims: gdn_decay_dims, nseq: int = 0) -> int:
+    return int(lib().gdn_decay_fwd_workspace(ctypes.byref(dims), nseq))
+
+
+def gdn_decay_bwd_workspace(dims: gdn_decay_dims, nseq: int = 0) -> int:
+    return int(lib().gdn_decay_bwd_workspace(ctypes.byref(dims), nseq))
+
+
+def gdn_decay_fwd(q, k, v, g, h0=None, *, cu_seqlens=None, scale=1.0, output_final_state=True,
+                  o=None, hT=None, workspace=None, stream=None):
+    """Linear attention S_t = e^{g_t} S_{t-1} + v_t k_t^T, o_t = S_t (scale q_t):
+    q, k [B,T,Hk,dk]; v [B,T,H,dv] (Hk divides H); g [B,T,H] fp32; h0
+    [B,H,dv,dk] fp32.  With ``cu_seqlens`` (int32 on the device) B is 1, the row
+    holds packed sequences and the states are [nseq,H,dv,dk].  Returns (o, hT);
+    hT is None unless requested."""
+    import torch
+    dims, nseq, states = _decay_inputs(q, k, v, g, h0, cu_seqlens, scale)
+    with _on(q, stream, k, v, g, h0, cu_seqlens) as s:
+        o = _given(o, "o", tuple(v.shape), q.dtype, q.device)
+        if output_final_state or hT is not None:
+            hT = _given(hT, "hT", states, torch.float32, q.device)
+        ws = _scratch(gdn_decay_fwd_workspace(dims, nseq), q.device, workspace)
+        st = lib().gdn_decay_fwd(ctypes.byref(dims), _ptr(cu_seqlens), nseq, _ptr(q), _ptr(k), _ptr(v),
+                                 _ptr(g), _ptr(h0), _ptr(o), _ptr(hT), _ptr(ws), _nbytes(ws), _stream(s))
+    _check(st, "gdn_decay_fwd")
+    return o, hT
+
+
+def gdn_decay_bwd(q, k, v, g, dO, h0=None, dhT=None, *, cu_seqlens=None, scale=1.0, out=None,
+                  workspace=None, stream=None):
+    """Backward of <dO,o> + <dhT,hT> for gdn_decay_fwd.  Returns a dict with dq,
+    dk, dv (dtype of q), dg, dh0 (None when h0 is None).  ``out``: optional dict
+    of preallocated results, filled in place."""
+    import torch
+    dims, nseq, states = _decay_inputs(q, k, v, g, h0, cu_seqlens, scale)
+    _need(dO, "dO", q.dtype, tuple(v.shape))
+    if dhT is not None:
+        _need(dhT, "dhT", torch.float32, states)
+    with _on(q, stream, k, v, g, dO, h0, dhT, cu_seqlens) as s:
+        out = dict(out or {})
+        for n, ref in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dh0", h0)):
+            out[n] = None if ref is None else _given(out.get(n), n, tuple(ref.shape), ref.dtype, q.device)
+        ws = _scratch(gdn_decay_bwd_workspace(dims, nseq), q.device, workspace)
+        st = lib().gdn_decay_bwd(ctypes.byref(dims), _ptr(cu_seqlens), nseq, _ptr(q), _ptr(k), _ptr(v),
+                                 _ptr(g), _ptr(h0), _ptr(dO), _ptr(dhT), _ptr(out["dq"]),
+                                 _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dh0"]),
+                                 _ptr(ws), _nbytes(ws), _stream(s))
+    _check(st, "gdn_decay_bwd")
+    return out
+
+
+def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
+    """One decode token of gdn_decay_fwd's recurrence, in place on ``state``
+    [N,H,dv,dk] fp32: q, k [N,Hk,dk]; v [N,H,dv]; g [N,H] fp32.  Returns o."""
+    import torch
+    _need(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [N, Hk, dk]")
+    N, Hk, dk = q.shape
+    _need(k, "k", q.dtype, (N, Hk, dk))
+    _need(v, "v", q.dtype)
+    if v.dim() != 3 or v.shape[0] != N:
+        raise ValueError("v must be [N, H, dv] matching q")
+    H, dv = v.shape[1], v.shape[2]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} value heads cannot share {Hk} key heads")
+    _need(g, "g", torch.float32, (N, H))
+    _need(state, "state", torch.float32, (N, H, dv, dk))
+    with _on(q, stream, k, v, g, state) as s:
+        o = _given(o, "o", (N, H, dv), q.dtype, q.device)
+        st = lib().gdn_decay_step(N, H, Hk, dk, dv, _dtype_code(q), float(scale), _ptr(q), _ptr(k),
+                                  _ptr(v), _ptr(g), _ptr(state), _ptr(o), _stream(s))
+    _check(st, "gdn_decay_step")
+    return o
+
+
+# ---- draft-tree attention over a paged cache ---------------------------------
+def _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len):
+    import torch
+    _need(parent, "parent", torch.int32)
+    if parent.dim() != 2:
+        raise ValueError("parent must be [N, M] int32")
+    N, M = parent.shape
+    _need(k, "k")
+    if k.dim() != 4 or tuple(k.shape[:2]) != (N, M):
+        raise ValueError("k must be [N, M, Hkv, d]")
+    Hkv, d = k.shape[2], k.shape[3]
+    _need(v, "v", k.dtype, tuple(k.shape))
+    _need(k_cache, "k_cache", k.dtype)
+    if k_cache.dim() != 4 or tuple(k_cache.shape[2:]) != (Hkv, d):
+        raise ValueError("k_cache must be [pages, page, Hkv, d]")
+    _need(v_cache, "v_cache", k.dtype, tuple(k_cache.shape))
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError("block_table must be [N, width] int32")
+    _need(cache_len, "cache_len", torch.int32, (N,))
+    return N, M, Hkv, d, k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
+
+
+def gdn_tree_attn(parent, q, k, v, k_cache, v_cache, block_table, cache_len, *, scale=1.0, window=0,
+                  o=None, workspace=None, stream=None):
+    """Softmax attention of every draft-tree node over its sequence's cached
+    tokens, its ancestors and itself: parent [N,M] int32; q [N,M,Hq,d]; k, v
+    [N,M,Hkv,d]; k_cache, v_cache [pages,page,Hkv,d]; block_table [N,width] and
+    cache_len [N] int32.  window > 0: only positions less than ``window`` back.
+    Returns o [N,M,Hq,d]."""
+    N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len)
+    _need(q, "q", k.dtype)
+    if q.dim() != 4 or tuple(q.shape[:2]) != (N, M) or q.shape[3] != d:
+        raise ValueError("q must be [N, M, Hq, d] matching k")
+    Hq = q.shape[2]
+    with _on(q, stream, parent, k, v, k_cache, v_cache, block_table, cache_len) as s:
+        o = _given(o, "o", tuple(q.shape), q.dtype, q.device)
+        need = int(lib().gdn_tree_attn_workspace(N, M, Hq, Hkv, d, _dtype_code(q), page, width))
+        ws = _scratch(need, q.device, workspace)
+        st = lib().gdn_tree_attn(N, M, Hq, Hkv, d, _dtype_code(q), float(scale), int(window), _ptr(parent),
+                                 _ptr(q), _ptr(k), _ptr(v), pages, page, width, _ptr(k_cache),
+                                 _ptr(v_cache), _ptr(block_table), _ptr(cache_len), _ptr(o), _ptr(ws),
+                                 _nbytes(ws), _stream(s))
+    _check(st, "gdn_tree_attn")
+    return o
+
+
+def gdn_tree_append(parent, accepted, k, v, k_cache, v_cache, block_table, cache_len, *, new_len=None,
+                    status=None, stream=None):
+    """Appends the k and v rows of the root path of node accepted[n] (int32 [N];
+    -1: nothing) to sequence n's pages, in place on k_cache and v_cache.  Returns
+    the new lengths (``new_len`` may be ``cache_len``)."""
+    import torch
+    N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len)
+    _need(accepted, "accepted", torch.int32, (N,))
+    if status is not None:
+        _need(status, "status", torch.int32)
+        if status.numel() < 1:
+            raise ValueError("status must hold a word")
+    with _on(k, stream, parent, accepted, v, k_cache, v_cache, block_table, cache_len, status) as s:
+        new_len = _given(new_len, "new_len", (N,), torch.int32, k.device)
+        st = lib().gdn_tree_append(N, M, Hkv, d, _dtype_code(k), _ptr(parent), _ptr(accepted), _ptr(k),
+                                   _ptr(v), pages, page, width, _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(block_table), _ptr(cache_len), _ptr(new_len), _ptr(status),
+                                   _stream(s))
+    _check(st, "gdn_tree_append")
+    return new_len
+
+
+# ---- output norm and gate ----------------------------------------------------
+def _norm_inputs(x, z, w):
+    import torch
+    _need(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must be [..., H, d]")
+    H, d = x.shape[-2], x.shape[-1]
+    _need(z, "z", x.dtype, tuple(x.shape))
+    _need(w, "w", torch.float32)
+    if tuple(w.shape) not in ((d,), (H, d)):
+        raise ValueError(f"w must be [d] or [H, d] for x [..., {H}, {d}]")
+    return x.numel() // max(d, 1), H, d, 1 if w.dim() == 1 else H
+
+
+def gdn_gated_norm_fwd(x, z, w, *, eps=1e-6, center=False, y=None, stream=None):
+    """y = w * norm(x) * SiLU(z), the norm over the last axis of x [...,H,d]: RMS,
+    or mean and variance with ``center``; w [d] or [H,d] fp32."""
+    rows, H, d, wheads = _norm_inputs(x, z, w)
+    with _on(x, stream, z, w) as s:
+        y = _given(y, "y", tuple(x.shape), x.dtype, x.device)
+        st = lib().gdn_gated_norm_fwd(rows, H, d, wheads, _dtype_code(x), int(bool(center)), float(eps),
+                                      _ptr(x), _ptr(z), _ptr(w), _ptr(y), _stream(s))
+    _check(st, "gdn_gated_norm_fwd")
+    return y
+
+
+def gdn_gated_norm_bwd(x, z, w, dy, *, eps=1e-6, center=False, dx=None, dz=None, dw=None, workspace=None,
+                       stream=None):
+    """Gradients of <dy, y> for gdn_gated_norm_fwd: returns (dx, dz, dw)."""
+    rows, H, d, wheads = _norm_inputs(x, z, w)
+    _need(dy, "dy", x.dtype, tuple(x.shape))
+    with _on(x, stream, z, w, dy) as s:
+        dx = _given(dx, "dx", tuple(x.shape), x.dtype, x.device)
+        dz = _given(dz, "dz", tuple(x.shape), x.dtype, x.device)
+        dw = _given(dw, "dw", tuple(w.shape), w.dtype, x.device)
+        need = int(lib().gdn_gated_norm_bwd_workspace(rows, H, d, _dtype_code(x)))
+        ws = _scratch(need, x.device, workspace)
+        st = lib().gdn_gated_norm_bwd(rows, H, d, wheads, _dtype_code(x), int(bool(center)), float(eps),
+                                      _ptr(x), _ptr(z), _ptr(w), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw),
+                                      _ptr(ws), _nbytes(ws), _stream(s))
+    _check(st, "gdn_gated_norm_bwd")
+    return dx, dz, dw

@@ -1,0 +1,45 @@
+// decay.h -- shapes and launchers of linear attention with a decay per head
+// (gdn_decay_*), shared between its entry points and its kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "../../include/gdn.h"
+
+namespace gdn {
+namespace decay {
+
+// The sequences of a call: nseq sequences of one row of `rows` tokens.  cu is
+// null for a batch (sequence s = tokens s*len .. s*len + len - 1).
+struct Seqs {
+    const int* cu;
+    int nseq, len;
+    int rows;  // tokens of the tensors in all
+};
+
+struct Problem {
+    Seqs seq;
+    int H, Hk, dk, dv;
+    gdn_dtype dtype;
+    float scale;
+};
+
+// Chunks of C tokens are cut from each sequence's own first token; chunk c of
+// sequence s has slot (first token / C) + s + c.  Slots of different sequences
+// never meet, whatever their lengths, so no prefix sum over them is needed.
+__host__ __device__ inline long long chunk_slots(const Seqs& q, int C) { return q.rows / C + (long long)q.nseq; }
+
+// fp32 arithmetic on CUDA cores, any supported dims (decay.cu).
+size_t simt_bwd_workspace(const Problem& p);
+void launch_simt_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g,
+                     const float* h0, void* o, float* hT, unsigned int* status, cudaStream_t st);
+void launch_decay_step(int N, int H, int Hk, int dk, int dv, gdn_dtype dtype, float scale, const void* q,
+                       const void* k, const void* v, const float* g, float* state, void* o,
+                       cudaStream_t st);
+void launch_simt_bwd(const Problem& p, const void* q, const void* k, const void* v, const float* g,
+                     const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
+                     float* dg, float* dh0, void* ws, cudaStream_t st);
+
+}  // namespace decay
+}  // namespace gdn

@@ -1,0 +1,260 @@
+// gated_norm.cu -- the layer's output norm and gate, forward and backward.
+//
+// Per token and head, over the d channels of the head (channels last):
+//     c = x - mean (centred form) or x,  h = c / sqrt(mean(c^2) + eps),
+//     y = w h s(z),   s(z) = z sigmoid(z).
+// Backward, with e = dy w s(z):
+//     dx = (e - h mean(e h) [- mean(e)]) / sqrt(mean(c^2) + eps),
+//     dz = dy w h sigmoid(z) (1 + z (1 - sigmoid(z))),   dw = sum dy h s(z).
+// Each tensor is read or written once, in 16-byte pieces: LPR lanes hold a row
+// and reduce it with shuffles, so HBM bandwidth bounds both directions.
+//
+// The rows are dealt to `units` (groups of LPR lanes) in turn, unit u taking
+// rows u, u + U, ... with U a multiple of the heads: neighbouring units read
+// neighbouring rows, and a unit's head, and so its slice of w, never changes.  A
+// unit therefore sums its dw in registers; a second kernel adds the units of a
+// head (of all heads, for a shared w) in a fixed order.
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "checks.h"
+#include "common.cuh"
+#include "mma.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int NT = 256;
+
+template <typename T>
+GDN_DEV void load16(float* v, const T* p);
+template <>
+GDN_DEV void load16<__nv_bfloat16>(float* v, const __nv_bfloat16* p) {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_bf16(x[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+template <>
+GDN_DEV void load16<float>(float* v, const float* p) {
+    const float4 r = __ldcs(reinterpret_cast<const float4*>(p));
+    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+}
+GDN_DEV void store16(__nv_bfloat16* p, const float* v) {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                   pack_bf16(v[6], v[7])));
+}
+GDN_DEV void store16(float* p, const float* v) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+}
+
+template <int LPR>
+GDN_DEV float row_sum(float x) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Shapes of a row: VEC channels per 16 bytes, LPR lanes, NV pieces per lane.
+template <typename T, int D>
+struct Row {
+    static constexpr int VEC = 16 / sizeof(T), LPR = D / VEC < 32 ? D / VEC : 32, NV = D / (VEC * LPR), CPL = VEC * NV;
+    static constexpr int UPC = NT / LPR;  // units per CTA
+};
+
+template <typename T, int D, bool CENTER, bool BWD>
+__global__ void __launch_bounds__(NT)
+gated_norm_kernel(long long rows, int H, int wheads, long long U, float eps, const T* __restrict__ x,
+                  const T* __restrict__ z, const float* __restrict__ w, const T* __restrict__ dy,
+                  T* __restrict__ out, T* __restrict__ dz, float* __restrict__ part) {
+    using R = Row<T, D>;
+    const int sub = threadIdx.x % R::LPR;
+    const long long unit = (long long)blockIdx.x * R::UPC + threadIdx.x / R::LPR;
+    const int wh = wheads == 1 ? 0 : (int)(unit % H);
+    float wr[R::CPL], dw[R::CPL];
+#pragma unroll
+    for (int j = 0; j < R::CPL; ++j) {
+        wr[j] = w[wh * D + (j / R::VEC * R::LPR + sub) * R::VEC + j % R::VEC];
+        dw[j] = 0.f;
+    }
+    // every lane of a warp runs the same number of turns: the shuffles need them all
+    const long long first = (long long)blockIdx.x * R::UPC + (threadIdx.x / 32) * (32 / R::LPR);
+    for (long long base = 0; base + first < rows; base += U) {
+        const long long r = base + unit;
+        const bool in = unit < U && r < rows;
+        float xv[R::CPL], zv[R::CPL], g[R::CPL];
+#pragma unroll
+        for (int p = 0; p < R::NV; ++p) {
+            const size_t at = (size_t)(in ? r : 0) * D + (p * R::LPR + sub) * R::VEC;
+            load16<T>(xv + p * R::VEC, x + at);
+            load16<T>(zv + p * R::VEC, z + at);
+            if constexpr (BWD) load16<T>(g + p * R::VEC, dy + at);
+        }
+        float mean = 0.f;
+        if constexpr (CENTER) {
+#pragma unroll
+            for (int j = 0; j < R::CPL; ++j) mean += xv[j];
+            mean = row_sum<R::LPR>(mean) * (1.f / D);
+        }
+        float sq = 0.f;
+#pragma unroll
+        for (int j = 0; j < R::CPL; ++j) {
+            xv[j] -= mean;
+            sq += xv[j] * xv[j];
+        }
+        const float rs = 1.f / sqrtf(row_sum<R::LPR>(sq) * (1.f / D) + eps);
+        float eh = 0.f, es = 0.f;
+#pragma unroll
+        for (int j = 0; j < R::CPL; ++j) {
+            const float h = xv[j] * rs, sg = 1.f / (1.f + expf(-zv[j])), act = zv[j] * sg;
+            if constexpr (BWD) {
+                const float gh = g[j] * h, e = g[j] * wr[j] * act;
+                if (in) dw[j] += gh * act;
+                zv[j] = gh * wr[j] * sg * (1.f + zv[j] * (1.f - sg));
+                eh += e * h;
+                es += e;
+                xv[j] = h;
+                g[j] = e;
+            } else {
+                xv[j] = wr[j] * h * act;
+            }
+        }
+        if constexpr (BWD) {
+            eh = row_sum<R::LPR>(eh) * (1.f / D);
+            es = CENTER ? row_sum<R::LPR>(es) * (1.f / D) : 0.f;
+#pragma unroll
+            for (int j = 0; j < R::CPL; ++j) xv[j] = (g[j] - xv[j] * eh - es) * rs;
+        }
+        if (!in) continue;
+#pragma unroll
+        for (int p = 0; p < R::NV; ++p) {
+            const size_t at = (size_t)r * D + (p * R::LPR + sub) * R::VEC;
+            store16(out + at, xv + p * R::VEC);
+            if constexpr (BWD) store16(dz + at, zv + p * R::VEC);
+        }
+    }
+    if constexpr (BWD) {
+        if (unit < U) {
+#pragma unroll
+            for (int j = 0; j < R::CPL; ++j)
+                part[unit * D + (j / R::VEC * R::LPR + sub) * R::VEC + j % R::VEC] = dw[j];
+        }
+    }
+}
+
+// dw[h] = sum of the units' parts over u = h, h + heads, ... (heads = 1 for a
+// shared w), 32 sums in parallel per channel, joined in a fixed order.
+__global__ void __launch_bounds__(1024)
+gated_norm_dw_kernel(long long U, int heads, int D, const float* __restrict__ part, float* __restrict__ dw) {
+    __shared__ float s[32][33];
+    const int c = blockIdx.y * 32 + threadIdx.x, h = blockIdx.x;
+    float sum = 0.f;
+    for (long long u = h + (long long)threadIdx.y * heads; u < U; u += 32ll * heads) sum += part[u * D + c];
+    s[threadIdx.y][threadIdx.x] = sum;
+    __syncthreads();
+    const float t = warp_sum(s[threadIdx.x][threadIdx.y]);
+    if (threadIdx.x == 0) dw[h * D + blockIdx.y * 32 + threadIdx.y] = t;
+}
+
+// Units of a call: as many as fill the device twice over, in whole turns of
+// the heads, and no more than there are rows.
+long long units(long long rows, int H, int lpr) {
+    const long long fill = 148ll * 16 * (NT / lpr) / 2;
+    return std::max<long long>(std::min(rows, fill) / H, 1) * H;
+}
+
+int lanes_per_row(gdn_dtype t, int d) { return std::min(32, d * (t == GDN_BF16 ? 2 : 4) / 16); }
+
+template <bool BWD>
+gdn_status run(long long rows, int H, int d, int wheads, gdn_dtype dtype, int center, float eps, const void* x,
+               const void* z, const float* w, const void* dy, void* out, void* dz, float* part, cudaStream_t st) {
+    auto go = [&](auto t, auto dd, auto cc) {
+        using T = decltype(t);
+        constexpr int D = decltype(dd)::value;
+        constexpr bool C = decltype(cc)::value;
+        using R = Row<T, D>;
+        const long long U = units(rows, H, R::LPR);
+        const unsigned grid = (unsigned)((U + R::UPC - 1) / R::UPC);
+        GDN_LAUNCH(BWD ? "gated_norm_bwd" : "gated_norm_fwd", st, (gated_norm_kernel<T, D, C, BWD><<<grid, NT, 0, st>>>(
+            rows, H, wheads, U, eps, (const T*)x, (const T*)z, w, (const T*)dy, (T*)out, (T*)dz, part)));
+    };
+    auto by_center = [&](auto t, auto dd) {
+        if (center) go(t, dd, std::true_type{});
+        else go(t, dd, std::false_type{});
+    };
+    auto by_dim = [&](auto t) {
+        switch (d) {
+            case 32: by_center(t, std::integral_constant<int, 32>{}); break;
+            case 64: by_center(t, std::integral_constant<int, 64>{}); break;
+            case 128: by_center(t, std::integral_constant<int, 128>{}); break;
+            default: by_center(t, std::integral_constant<int, 256>{}); break;
+        }
+    };
+    if (dtype == GDN_BF16) by_dim(__nv_bfloat16{});
+    else by_dim(float{});
+    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status check(long long rows, int H, int d, int wheads, gdn_dtype dtype, float eps) {
+    if (rows < 1 || H < 1 || rows % H || (wheads != 1 && wheads != H)) return GDN_ERR_INVALID_ARG;
+    if (rows > (1ll << 40) || H > (1 << 20)) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
+    if (!isfinite(eps) || eps < 0.f) return GDN_ERR_INVALID_ARG;
+    if (d != 32 && d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_gated_norm_fwd(long long rows, int H, int d, int wheads, gdn_dtype dtype, int center, float eps,
+                              const void* x, const void* z, const float* w, void* y, gdn_stream_t stream) {
+    const gdn_status s = check(rows, H, d, wheads, dtype, eps);
+    if (s != GDN_OK) return s;
+    if (!x || !z || !w || !y) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned_to(16, {x, z, y}) || !aligned_to(w, 4)) return GDN_ERR_INVALID_ARG;
+    const size_t n = (size_t)rows * d * (dtype == GDN_BF16 ? 2 : 4);
+    if (outputs_overlap({{x, n}, {z, n}, {w, (size_t)wheads * d * 4}}, {{y, n}})) return GDN_ERR_INVALID_ARG;
+    cudaGetLastError();
+    return run<false>(rows, H, d, wheads, dtype, center, eps, x, z, w, nullptr, y, nullptr, nullptr,
+                      (cudaStream_t)stream);
+}
+
+size_t gdn_gated_norm_bwd_workspace(long long rows, int H, int d, gdn_dtype dtype) {
+    if (check(rows, H, d, 1, dtype, 0.f) != GDN_OK) return 0;
+    return (size_t)units(rows, H, lanes_per_row(dtype, d)) * d * 4;
+}
+
+gdn_status gdn_gated_norm_bwd(long long rows, int H, int d, int wheads, gdn_dtype dtype, int center, float eps,
+                              const void* x, const void* z, const float* w, const void* dy, void* dx, void* dz,
+                              float* dw, void* ws, size_t ws_bytes, gdn_stream_t stream) {
+    gdn_status s = check(rows, H, d, wheads, dtype, eps);
+    if (s != GDN_OK) return s;
+    if (!x || !z || !w || !dy || !dx || !dz || !dw) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned_to(16, {x, z, dy, dx, dz}) || !all_aligned_to(4, {w, dw})) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn_gated_norm_bwd_workspace(rows, H, d, dtype);
+    if (!ws || ws_bytes < need || !aligned_to(ws, 256)) return GDN_ERR_WORKSPACE;
+    const size_t n = (size_t)rows * d * (dtype == GDN_BF16 ? 2 : 4), nw = (size_t)wheads * d * 4;
+    if (outputs_overlap({{x, n}, {z, n}, {dy, n}, {w, nw}}, {{dx, n}, {dz, n}, {dw, nw}, {ws, need}}))
+        return GDN_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaGetLastError();
+    s = run<true>(rows, H, d, wheads, dtype, center, eps, x, z, w, dy, dx, dz, (float*)ws, st);
+    if (s != GDN_OK) return s;
+    const long long U = units(rows, H, lanes_per_row(dtype, d));
+    GDN_LAUNCH("gated_norm_dw", st, (gated_norm_dw_kernel<<<dim3((unsigned)wheads, d / 32), dim3(32, 32), 0, st>>>(
+        U, wheads, d, (const float*)ws, dw)));
+    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -319,6 +319,134 @@ gdn_status gdn_recurrent_step(int N, int H, int dk, int dv, gdn_dtype dtype,
                               const float *beta, float *state, void *o,
                               gdn_stream_t stream);
 
+/* Linear attention with a decay per head, the gated recurrence without the
+ * delta correction (the "Mamba2" / gated linear attention form that "Gated
+ * Delta Networks: Improving Mamba2 with Delta Rule" (paper review), section
+ * "Background", sets the delta rule against, and that its hybrid stacks put
+ * beside it).  Per (sequence, head), with a_t = exp(g_t),
+ *     S_t = a_t S_{t-1} + v_t k_t^T,   o_t = S_t (scale q_t).
+ * q and k have Hk heads, v, o and g have H, Hk divides H, and value head h
+ * reads key head h / (H / Hk).  Their gradients are summed over the heads that
+ * share them, in a fixed order: every result is deterministic.
+ * Layouts (contiguous): q, k, dq, dk [B, T, Hk, dk]; v, o, dO, dv [B, T, H, dv]
+ * in `dtype`; g, dg [B, T, H] fp32; h0, hT, dhT, dh0 [B, H, dv, dk] fp32 (row =
+ * value index).  With cu_seqlens (device, int32[nseq + 1]) B must be 1, the row
+ * holds nseq sequences, sequence s at tokens cu_seqlens[s] ..
+ * cu_seqlens[s + 1] - 1, and the states are [nseq, H, dv, dk]; empty sequences
+ * pass h0 to hT (dhT to dh0).  Tokens of no sequence (before the first, behind
+ * the last) are not read, and their rows of o, dq, dk, dv, dg are left as they
+ * were.  A sequence whose offsets are not 0 <= cu[s] <= cu[s+1] <= T is skipped
+ * and makes gdn_query_device_status on the workspace return
+ * GDN_ERR_INVALID_ARG; sequences must not overlap.  nseq = 0 with a null
+ * cu_seqlens is the plain batch.
+ * Values: g <= 0 (documented, not checked); g = -inf is a reset.  The decay of a
+ * pair of tokens is formed from an fp64 cumsum or token by token, the state and
+ * dg from products exact to fp32: hT, dh0 and dg carry fp32 accuracy with bf16
+ * inputs too; o, dq, dk, dv are rounded to `dtype` once more at the end.
+ * The backward is that of <dO, o> + <dhT, hT> (dhT NULL = 0) and recomputes the
+ * states; dh0 is required exactly when h0 is given.
+ * dk, dv in {16, 32, 64, 128} (else GDN_ERR_UNSUPPORTED); all pointers 16-byte
+ * aligned, cu_seqlens 4; outputs must not overlap inputs, each other or the
+ * workspace (GDN_ERR_INVALID_ARG); workspace as the queries say, 256-byte
+ * aligned (GDN_ERR_WORKSPACE). */
+typedef struct {
+    int B, T, H, Hk, dk, dv;
+    gdn_dtype dtype;
+    float scale;
+} gdn_decay_dims;
+size_t gdn_decay_fwd_workspace(const gdn_decay_dims *dims, int nseq);
+gdn_status gdn_decay_fwd(const gdn_decay_dims *dims, const int *cu_seqlens,
+                         int nseq, const void *q, const void *k, const void *v,
+                         const float *g, const float *h0, void *o, float *hT,
+                         void *ws, size_t ws_bytes, gdn_stream_t stream);
+size_t gdn_decay_bwd_workspace(const gdn_decay_dims *dims, int nseq);
+gdn_status gdn_decay_bwd(const gdn_decay_dims *dims, const int *cu_seqlens,
+                         int nseq, const void *q, const void *k, const void *v,
+                         const float *g, const float *h0, const void *dO,
+                         const float *dhT, void *dq, void *dk, void *dv,
+                         float *dg, float *dh0, void *ws, size_t ws_bytes,
+                         gdn_stream_t stream);
+
+/* One decode token of the same recurrence for N sequences, in place on state
+ * [N, H, dv, dk] fp32 (read once, written once): q, k [N, Hk, dk]; v, o
+ * [N, H, dv] in `dtype`; g [N, H] fp32.  o_t uses the updated state. */
+gdn_status gdn_decay_step(int N, int H, int Hk, int dk, int dv, gdn_dtype dtype,
+                          float scale, const void *q, const void *k,
+                          const void *v, const float *g, float *state, void *o,
+                          gdn_stream_t stream);
+
+/* Softmax attention of a draft tree over a paged cache, and the append of the
+ * accepted path to it: what the softmax layers of a hybrid stack do while
+ * gdn_tree_verify / gdn_tree_commit serve its linear layers ("TreeWY:
+ * Speculative Verification for Gated DeltaNet Hybrids", the "Linked reviews"
+ * entry of the "Gated Delta Networks: Improving Mamba2 with Delta Rule" review
+ * page).  Trees as there: N sequences, M <= 64 nodes, parent[n, i] in [-1, i).
+ * Node i of sequence n stands at position cache_len[n] + depth(i) (a child of
+ * the root at depth 0) and sees the cached positions, its ancestors and
+ * itself; with window > 0 (sliding-window attention) only positions less than
+ * `window` back.  M = 1 with parent -1 is plain decoding.  Query head h reads key
+ * head h / (Hq / Hkv):
+ *     o_i = sum_p softmax_p(scale q_i . k_p) v_p,
+ * the softmax statistics and sums in fp32, the weights rounded to bf16 for their
+ * product with v.
+ * gdn_tree_append copies the k and v rows of the root path of accepted[n] (-1:
+ * nothing) to the cache positions cache_len[n] .. and writes the new length to
+ * new_len[n] (new_len may be cache_len).
+ * Layouts (contiguous): parent [N, M], accepted, cache_len, new_len [N],
+ * block_table [N, width] int32; q, o [N, M, Hq, d]; k, v [N, M, Hkv, d];
+ * k_cache, v_cache [pages, page, Hkv, d].  Position p of sequence n is row
+ * p % page of page block_table[n, p / page]; entries past the last used page
+ * are not read.  Pages may be shared by sequences, but not one that is appended
+ * to.
+ * GDN_BF16, d in {64, 128}, page in {16, 32, 64, 128}, M <= 64 (else
+ * GDN_ERR_UNSUPPORTED).  Device data is checked on the device: a parent out of
+ * range reads as -1, an accepted node as -1; a length that the table cannot hold
+ * reads as an empty cache (append: the sequence is left as it is); a page out
+ * of range is not read, its positions are not seen (append: the sequence is left
+ * as it is).  Each makes gdn_query_device_status, on the workspace of
+ * gdn_tree_attn or the optional word *status of gdn_tree_append, return
+ * GDN_ERR_INVALID_ARG.  Alignment, overlap and workspace rules as gdn_decay_fwd. */
+size_t gdn_tree_attn_workspace(int N, int M, int Hq, int Hkv, int d,
+                               gdn_dtype dtype, int page, int width);
+gdn_status gdn_tree_attn(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype,
+                         float scale, int window, const int *parent,
+                         const void *q, const void *k, const void *v, int pages,
+                         int page, int width, const void *k_cache,
+                         const void *v_cache, const int *block_table,
+                         const int *cache_len, void *o, void *ws,
+                         size_t ws_bytes, gdn_stream_t stream);
+gdn_status gdn_tree_append(int N, int M, int Hkv, int d, gdn_dtype dtype,
+                           const int *parent, const int *accepted, const void *k,
+                           const void *v, int pages, int page, int width,
+                           void *k_cache, void *v_cache, const int *block_table,
+                           const int *cache_len, int *new_len,
+                           unsigned int *status, gdn_stream_t stream);
+
+/* The layer's output norm and gate (block design of "Gated Delta Networks:
+ * Improving Mamba2 with Delta Rule" (paper review), section "Method": the
+ * read-out passes an output norm and gate).  Per token and head, over the d
+ * channels of the head:
+ *     c = x (center = 0, RMS norm) or x - mean(x) (center = 1, group norm),
+ *     y = w c / sqrt(mean(c^2) + eps) * z sigmoid(z).
+ * x, z, y, dy, dx, dz are [rows, d] in `dtype` with rows = tokens * H, head last;
+ * w, dw are [wheads, d] fp32 with wheads = 1 (shared by the heads) or H.
+ * gdn_gated_norm_bwd writes the gradients of <dy, y>; dw is overwritten and
+ * summed in a fixed order.  Statistics and sums are fp32.
+ * d in {32, 64, 128, 256} (else GDN_ERR_UNSUPPORTED); rows a positive multiple of
+ * H, eps >= 0; x, z, y, dy, dx, dz 16-byte aligned; overlap and workspace
+ * rules as gdn_decay_fwd. */
+gdn_status gdn_gated_norm_fwd(long long rows, int H, int d, int wheads,
+                              gdn_dtype dtype, int center, float eps,
+                              const void *x, const void *z, const float *w,
+                              void *y, gdn_stream_t stream);
+size_t gdn_gated_norm_bwd_workspace(long long rows, int H, int d,
+                                    gdn_dtype dtype);
+gdn_status gdn_gated_norm_bwd(long long rows, int H, int d, int wheads,
+                              gdn_dtype dtype, int center, float eps,
+                              const void *x, const void *z, const float *w,
+                              const void *dy, void *dx, void *dz, float *dw,
+                              void *ws, size_t ws_bytes, gdn_stream_t stream);
+
 /* Test hook for the bounded device waits (no counterpart in the paper): runs
  * gdn_chunk_fwd's tensor-core forward with the loads of chain step
  * `stall_at` (and after) never issued, so the waits on that step, which no

@@ -1,0 +1,290 @@
+"""gdn_decay_fwd / gdn_decay_bwd / gdn_decay_step against the fp64 token loop.
+
+Bounds, element by element, from what the kernels round.  Every result is a sum
+of products of inputs and decays; ``mag`` is the same sum of absolute values (the
+oracle on absolute inputs).  With u = 2^-24 (half a step of fp32):
+* a term passes at most T decays (exp: 2 steps = 4 u, its product: u) or one exp of
+  an fp64 difference, a dot product of dk or dv terms, and sums of at most
+  T + dk + dv + 32 terms: (6 T + 2 dk + 2 dv + 64) u mag;
+* bf16 with dk and dv in {64, 128} runs on tensor cores, where a weight or a state
+  entry is rounded to bf16 once on its way into o, dq, dk, dv (2^-8 mag), and
+  goes into hT, dh0, dg as a sum of two bf16 terms at least (2^-16 mag);
+* dg_t is a difference of sums over the tokens up to the end of its chunk (at most
+  128 tokens), so its bound takes |q_i . dq_i| + |k_i . dk_i| of those for ``mag``;
+* the result is rounded to its type: half a step of the result.
+"""
+import pytest
+import torch
+
+import gated_delta_rule_153_b200 as gdn
+from oracle import decay
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def make(B, T, H, Hk, dk, dv, dtype, seed=0, shift=-2.0, nstates=None, g=None):
+    gen = torch.Generator().manual_seed(seed * 131 + T)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True).clamp(min=1e-6)  # noqa: E731
+    dt, n = DT[dtype], nstates or B
+    return dict(q=unit(r(B, T, Hk, dk)).to(dt), k=unit(r(B, T, Hk, dk)).to(dt), v=r(B, T, H, dv).to(dt),
+                g=-torch.nn.functional.softplus(r(B, T, H) + shift) if g is None else g,
+                dO=r(B, T, H, dv).to(dt), h0=0.3 * r(n, H, dv, dk), dhT=0.3 * r(n, H, dv, dk))
+
+
+def absolute(x):
+    return {n: (t if n == "g" else t.abs()) for n, t in x.items()}
+
+
+def oracle_both(x, cu, scale):
+    """Forward and backward, by name."""
+    a = [x[n] for n in ("q", "k", "v", "g")]
+    if cu is None:
+        o, hT, _ = decay.forward(*a, x["h0"], scale=scale)
+        r = decay.backward(*a, x["dO"], x["h0"], x["dhT"], scale=scale)
+    else:
+        o, hT = decay.packed(decay.forward, cu, *a, x["h0"], scale=scale)
+        r = decay.packed(decay.backward, cu, *a, x["dO"], x["h0"], x["dhT"], scale=scale)
+    return dict(o=o, hT=hT, **{n: t for n, t in r.items() if t is not None})
+
+
+def tolerance(name, ref, mag, x, T):
+    dtype, dk, dv = x["q"].dtype, x["q"].shape[-1], x["v"].shape[-1]
+    c = (6 * T + 2 * dk + 2 * dv + 64) * 2.0 ** -24
+    wide = dtype == torch.bfloat16 and dk in (64, 128) and dv in (64, 128)
+    full = name in ("hT", "dh0", "dg")
+    if wide:
+        c += 2.0 ** -16 if full else 2.0 ** -8
+    u = 2.0 ** -8 if dtype == torch.bfloat16 and not full else 2.0 ** -24
+    return c * mag + u * (ref.abs() + c * mag) + 1e-30
+
+
+def check(got, x, cu=None, scale=1.0, T=None):
+    ref, mag = oracle_both(x, cu, scale), oracle_both(absolute(x), cu, abs(scale))
+    T = T or x["q"].shape[1]
+    own = (x["q"].double().abs() * mag["dq"] + x["k"].double().abs() * mag["dk"]).sum(-1)
+    own = own.repeat_interleave(x["v"].shape[2] // own.shape[2], 2)
+    for i in range(T):
+        mag["dg"][:, i] += own[:, i:i + 128].sum(1)
+    bad = {}
+    for n, t in got.items():
+        if t is None:
+            continue
+        err = (t.detach().double().cpu() - ref[n]).abs()
+        lim = tolerance(n, ref[n], mag[n], x, T)
+        if not bool((err <= lim).all()):
+            bad[n] = float((err / lim).max())
+    assert not bad, f"times over the bound: {bad}"
+
+
+def run(x, dev, cu=None, scale=1.0, states=True, **kw):
+    d = {n: t.to(dev) for n, t in x.items()}
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=dev)
+    h0, dhT = (d["h0"], d["dhT"]) if states else (None, None)
+    o, hT = gdn.gdn_decay_fwd(d["q"], d["k"], d["v"], d["g"], h0, cu_seqlens=c, scale=scale, **kw)
+    r = gdn.gdn_decay_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], h0, dhT, cu_seqlens=c, scale=scale, **kw)
+    torch.cuda.synchronize()
+    return dict(o=o, hT=hT, **r)
+
+
+SHAPES = [(1, 1, 1, 1, 128, 128), (2, 127, 2, 2, 128, 128), (1, 128, 2, 1, 128, 64), (1, 129, 4, 2, 64, 128),
+          (2, 64, 3, 3, 64, 64), (1, 300, 4, 1, 128, 128), (3, 65, 2, 2, 16, 32), (1, 257, 2, 1, 32, 16),
+          (1, 31, 6, 2, 128, 16)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_matches_oracle(dev, shape, dtype):
+    x = make(*shape, dtype, seed=1)
+    check(run(x, dev, scale=0.7), x, scale=0.7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [-7.0, 2.0, 5.0])
+def test_slow_and_fast_decay(dev, dtype, shift):
+    """Decays that keep the state over the whole sequence, and ones that end it
+    within a few tokens (cumsums of hundreds)."""
+    x = make(1, 260, 2, 2, 128, 128, dtype, seed=2, shift=shift)
+    check(run(x, dev), x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [float("-inf"), -3.0e38, -200.0])
+def test_reset_gates(dev, dtype, low):
+    x = make(1, 200, 2, 1, 64, 128, dtype, seed=3)
+    for t in (0, 5, 127, 128, 199):
+        x["g"][0, t, 0] = low
+    x["g"][0, 60:70, 1] = low
+    got = run(x, dev)
+    # the oracle's decay of a reset token is exactly zero, and so is its gradient
+    check(got, x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H,Hk,dk,dv", [(2, 2, 128, 128), (4, 1, 128, 64), (3, 3, 16, 32)])
+def test_packed_sequences(dev, dtype, H, Hk, dk, dv):
+    cu = [0, 0, 1, 64, 192, 321, 321, 328]
+    x = make(1, 328, H, Hk, dk, dv, dtype, seed=4, nstates=7)
+    got = run(x, dev, cu, scale=0.5)
+    check(got, x, cu, scale=0.5)
+    for s in (0, 5):  # empty sequences pass their states through
+        assert torch.equal(got["hT"][s].cpu(), x["h0"][s])
+        assert torch.equal(got["dh0"][s].cpu(), x["dhT"][s])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_of_no_sequence_are_left(dev, dtype):
+    """Tokens before the first sequence and behind the last hold NaN: they are
+    neither read nor written."""
+    cu = [3, 100, 231]
+    x = make(1, 300, 2, 1, 64, 64, dtype, seed=5, nstates=2)
+    for n in ("q", "k", "v", "g", "dO"):
+        x[n][:, :3] = float("nan")
+        x[n][:, 231:] = float("nan")
+    d = {n: t.to(dev) for n, t in x.items()}
+    c = torch.tensor(cu, dtype=torch.int32, device=dev)
+    o = torch.full_like(d["v"], 7.0)
+    out = {n: torch.full_like(d[n[1:]], 7.0) for n in ("dq", "dk", "dv", "dg", "dh0")}
+    o, hT = gdn.gdn_decay_fwd(d["q"], d["k"], d["v"], d["g"], d["h0"], cu_seqlens=c, o=o)
+    r = gdn.gdn_decay_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], d["h0"], d["dhT"], cu_seqlens=c, out=out)
+    torch.cuda.synchronize()
+    for t in (o, r["dq"], r["dk"], r["dv"], r["dg"]):
+        assert bool((t[:, :3] == 7.0).all()) and bool((t[:, 231:] == 7.0).all())
+    y = {n: (t if t.dim() == 4 and t.shape[0] == 2 else t[:, 3:231]) for n, t in x.items()}
+    got = {n: (t if n in ("hT", "dh0") else t[:, 3:231]) for n, t in dict(o=o, hT=hT, **r).items()}
+    check(got, y, [0, 97, 228])
+
+
+def test_bad_offsets_are_reported(dev):
+    """Offsets that are no sequence skip it and set the status; the others run."""
+    x = make(1, 200, 2, 2, 128, 128, "bf16", seed=6, nstates=3)
+    d = {n: t.to(dev) for n, t in x.items()}
+    dims = gdn.gdn_decay_dims(1, 200, 2, 2, 128, 128, gdn.GDN_BF16, 1.0)
+    ws = torch.empty(max(gdn.gdn_decay_fwd_workspace(dims, 3), gdn.gdn_decay_bwd_workspace(dims, 3)),
+                     dtype=torch.uint8, device=dev)
+    good = torch.tensor([0, 50, 120, 200], dtype=torch.int32, device=dev)
+    a = [d[n] for n in ("q", "k", "v", "g")]
+    o1, _ = gdn.gdn_decay_fwd(*a, cu_seqlens=good, workspace=ws)
+    assert gdn.gdn_query_device_status(ws) == gdn.GDN_OK
+    for cu in ([0, 50, 120, 201], [0, 50, 40, 200], [-1, 50, 120, 200]):
+        c = torch.tensor(cu, dtype=torch.int32, device=dev)
+        o, _ = gdn.gdn_decay_fwd(*a, cu_seqlens=c, workspace=ws, o=torch.zeros_like(d["v"]))
+        assert gdn.gdn_query_device_status(ws) == gdn.GDN_ERR_INVALID_ARG
+        if cu[1] == 50 and cu[0] == 0:
+            assert torch.equal(o[:, :50], o1[:, :50])
+        gdn.gdn_decay_bwd(*a, d["dO"], cu_seqlens=c, workspace=ws)
+        assert gdn.gdn_query_device_status(ws) == gdn.GDN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_without_states_and_repeatable(dev, dtype):
+    x = make(2, 150, 4, 2, 128, 128, dtype, seed=7)
+    a, b = run(x, dev, states=False), run(x, dev, states=False)
+    for n in a:
+        assert (a[n] is None and b[n] is None) or torch.equal(a[n], b[n]), n
+    zero = dict(x, h0=torch.zeros_like(x["h0"]), dhT=torch.zeros_like(x["dhT"]))
+    check(a, zero)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_long_chains(dev, dtype):
+    """Few heads and many chunks: sequences may be cut into runs; resuming from a
+    returned state must agree too."""
+    x = make(1, 1500, 1, 1, 64, 64, dtype, seed=8, shift=-5.0)
+    got = run(x, dev)
+    check(got, x)
+    d = {n: t.to(dev) for n, t in x.items()}
+    cut = 700
+    first = [d[n][:, :cut].contiguous() for n in ("q", "k", "v", "g")]
+    rest = [d[n][:, cut:].contiguous() for n in ("q", "k", "v", "g")]
+    _, h = gdn.gdn_decay_fwd(*first, d["h0"])
+    o2, hT2 = gdn.gdn_decay_fwd(*rest, h)
+    y = {n: t[:, :] for n, t in x.items()}
+    check(dict(o=torch.cat([got["o"][:, :cut], o2], 1), hT=hT2), y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_side_stream_and_graph(dev, dtype):
+    """On a stream of its own, and captured (with its workspaces) and replayed on
+    new inputs in the same buffers."""
+    x = make(2, 200, 4, 2, 128, 64, dtype, seed=9)
+    y = make(2, 200, 4, 2, 128, 64, dtype, seed=10)
+    plain, want = run(x, dev), run(y, dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = run(x, dev, stream=side)
+    for n in plain:
+        assert torch.equal(plain[n], other[n]), n
+    d = {n: t.to(dev) for n, t in x.items()}
+
+    def step():
+        o, hT = gdn.gdn_decay_fwd(d["q"], d["k"], d["v"], d["g"], d["h0"])
+        return dict(o=o, hT=hT, **gdn.gdn_decay_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], d["h0"], d["dhT"]))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for n in d:
+        d[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    for n in want:
+        assert torch.equal(out[n], want[n]), n
+
+
+def test_gradients_are_the_differences(dev):
+    """fp32: the directional derivative along random directions of every input,
+    by central differences of the forward with fp64 sums."""
+    x = make(1, 70, 4, 2, 32, 64, "f32", seed=11)
+    got = run(x, dev, scale=0.8)
+    gen = torch.Generator().manual_seed(5)
+
+    def loss(y):
+        o, hT, _ = decay.forward(y["q"], y["k"], y["v"], y["g"], y["h0"], scale=0.8)
+        return float((o * x["dO"].double()).sum() + (hT * x["dhT"].double()).sum())
+
+    for n in ("q", "k", "v", "g", "h0"):
+        u = torch.randn(x[n].shape, generator=gen, dtype=torch.float64)
+        e = 1e-4
+        y = {m: t.double() for m, t in x.items()}
+        diff = (loss(dict(y, **{n: y[n] + e * u})) - loss(dict(y, **{n: y[n] - e * u}))) / (2 * e)
+        mine = (got["d" + n].double().cpu() * u).sum()
+        mag = (got["d" + n].double().cpu() * u).abs().sum()
+        # the differences are off by e^2 third derivatives (below 1e-6 of the terms)
+        assert abs(float(mine) - diff) <= 1e-5 * float(mag), n
+
+
+STEPS = [(1, 1, 1, 128, 128), (3, 4, 2, 64, 128), (5, 6, 3, 16, 32), (2, 4, 1, 32, 16), (40, 8, 8, 128, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", STEPS)
+def test_step_matches_oracle(dev, shape, dtype):
+    N, H, Hk, dk, dv = shape
+    x = make(N, 3, H, Hk, dk, dv, dtype, seed=12)
+    x["g"][0, 1, 0] = float("-inf")
+    S, o = x["h0"].to(dev), []
+    for t in range(3):
+        a = [x[n][:, t].contiguous().to(dev) for n in ("q", "k", "v", "g")]
+        o.append(gdn.gdn_decay_step(*a, S, scale=0.6))
+    torch.cuda.synchronize()
+    ref, hT, _ = decay.forward(x["q"], x["k"], x["v"], x["g"], x["h0"], scale=0.6)
+    m = absolute(x)
+    mo, mh, _ = decay.forward(m["q"], m["k"], m["v"], m["g"], m["h0"], scale=0.6)
+    c, u = (6 * 3 + 2 * dk + 64) * 2.0 ** -24, 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    assert bool(((torch.stack(o, 1).double().cpu() - ref).abs() <= c * mo + u * (ref.abs() + c * mo)).all())
+    assert bool(((S.double().cpu() - hT).abs() <= c * mh).all())
+
+
+def test_prompt_then_steps_is_one_prompt(dev):
+    """A prompt's final state continued by single tokens is the longer prompt."""
+    x = make(2, 140, 4, 2, 128, 128, "bf16", seed=13)
+    d = {n: t.to(dev) for n, t in x.items()}
+    names = ("q", "k", "v", "g")
+    o1, S = gdn.gdn_decay_fwd(*[d[n][:, :133].contiguous() for n in names], d["h0"], scale=0.5)
+    steps = [gdn.gdn_decay_step(*[d[n][:, t].contiguous() for n in names], S, scale=0.5) for t in range(133, 140)]
+    check(dict(o=torch.cat([o1, torch.stack(steps, 1)], 1), hT=S), x, scale=0.5)
