@@ -85,16 +85,11 @@ decay_walk_kernel(const Walk p) {
     const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane % L, grp = lane / L;
-    long long tok0 = (long long)s * p.seq.len;
-    int n = p.seq.len;
-    if (p.seq.cu) {
-        const int a = p.seq.cu[s], b = p.seq.cu[s + 1];
-        if (a < 0 || b < a || b > p.seq.rows) {  // not a sequence: nothing of it is read or written
-            if (tid == 0) atomicOr(p.status, 2u);
-            return;
-        }
-        tok0 = a;
-        n = b - a;
+    long long tok0;
+    int n;
+    if (!span_of(p.seq, s, tok0, n)) {
+        if (tid == 0) atomicOr(p.status, 2u);
+        return;
     }
     const size_t sh = (size_t)s * p.H + h;
     const long long slot0 = tok0 / AC + s;
@@ -239,17 +234,6 @@ decay_walk_kernel(const Walk p) {
     }
 }
 
-// The token range of sequence s; false if its offsets are not one.
-GDN_DEV bool span(const Seqs& q, int s, long long& tok0, int& n) {
-    tok0 = (long long)s * q.len;
-    n = q.len;
-    if (!q.cu) return true;
-    const int a = q.cu[s], b = q.cu[s + 1];
-    tok0 = a;
-    n = b - a;
-    return !(a < 0 || b < a || b > q.rows);
-}
-
 // dg of one chunk per warp: the suffix sums of q.dq' - k.dk' and the chunk end's <S, dS>.
 __global__ void __launch_bounds__(128)
 decay_gate_kernel(Seqs q, int H, int nb, const float* __restrict__ g, const float* __restrict__ dotq,
@@ -257,7 +241,7 @@ decay_gate_kernel(Seqs q, int H, int nb, const float* __restrict__ g, const floa
     const int s = blockIdx.x / H, h = blockIdx.x % H, lane = threadIdx.x & 31;
     long long tok0;
     int n;
-    if (!span(q, s, tok0, n)) return;
+    if (!span_of(q, s, tok0, n)) return;
     const long long slots = chunk_slots(q, AC);
     for (int c = blockIdx.y * 4 + (threadIdx.x >> 5); c * AC < n; c += gridDim.y * 4) {
         float x[2];
@@ -294,7 +278,7 @@ __global__ void __launch_bounds__(256)
 decay_group_sum_kernel(Seqs q, int Hk, int rep, int d, const float* __restrict__ part, T* __restrict__ out) {
     long long tok0;
     int n;
-    if (!span(q, blockIdx.x, tok0, n)) return;
+    if (!span_of(q, blockIdx.x, tok0, n)) return;
     const size_t total = (size_t)n * Hk * d;
     for (size_t e = (size_t)blockIdx.y * 256 + threadIdx.x; e < total; e += (size_t)gridDim.y * 256) {
         const size_t row = e / d;  // token * Hk + key head

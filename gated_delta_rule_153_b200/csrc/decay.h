@@ -30,6 +30,21 @@ struct Problem {
 // never meet, whatever their lengths, so no prefix sum over them is needed.
 __host__ __device__ inline long long chunk_slots(const Seqs& q, int C) { return q.rows / C + (long long)q.nseq; }
 
+#ifdef __CUDACC__
+// The token range of sequence s.  False if its offsets are not one: out of the
+// row, decreasing, or below the offset before them (it would then share tokens
+// with an earlier sequence); nothing of such a sequence is read or written.
+__device__ __forceinline__ bool span_of(const Seqs& q, int s, long long& tok0, int& n) {
+    tok0 = (long long)s * q.len;
+    n = q.len;
+    if (!q.cu) return true;
+    const int a = q.cu[s], b = q.cu[s + 1];
+    tok0 = a;
+    n = b - a;
+    return !(a < 0 || b < a || b > q.rows || (s > 0 && q.cu[s - 1] > a));
+}
+#endif
+
 // fp32 arithmetic on CUDA cores, any supported dims (decay.cu).
 size_t simt_bwd_workspace(const Problem& p);
 void launch_simt_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g,
@@ -40,6 +55,14 @@ void launch_decay_step(int N, int H, int Hk, int dk, int dv, gdn_dtype dtype, fl
 void launch_simt_bwd(const Problem& p, const void* q, const void* k, const void* v, const float* g,
                      const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
                      float* dg, float* dh0, void* ws, cudaStream_t st);
+
+
+// Tensor cores: bf16 with dk, dv in {64, 128} (decay_walk.cu).  The launchers return
+// false if a tensor map could not be encoded (nothing launched).
+bool tc_supported(const Problem& p);
+size_t tc_fwd_workspace(const Problem& p);
+bool launch_tc_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
+                   void* o, float* hT, void* ws, cudaStream_t st);
 
 }  // namespace decay
 }  // namespace gdn

@@ -1,0 +1,505 @@
+// decay_walk.cu -- linear attention with a decay per head on the fifth-generation
+// tensor cores: the walk along a chain of 128-token chunks, with its state on
+// chip from the first chunk to the last.
+//
+// One CTA walks one (sequence, head) for 64 of its dv value channels.  Per chunk,
+// with S (key channels x value channels) entering it and D the pair decays:
+//     A = Q K^T                        128 x 128 x dk     lane = query token
+//     P = scale A .* D, causal         -> bf16 A operand in tensor memory
+//     X = Q S                          128 x 64 x dk      lane = query token
+//     Y = P V                          128 x 64 x 128
+//     O = diag(scale e^G) X + Y
+//     N = K^T (diag(e^{G_last - G}) V) dk x 64 x 128      lane = key channel
+//     S <- e^{G_last} S + N            in fp32 registers
+// Only the last line is sequential, and it is one multiply-add per element: N does
+// not depend on S.  The products are issued in the order A X N Y, so that the tensor
+// pipe has X and N to do while P is made from A, and Y and the next A while N goes
+// into S.
+//
+// Rounding.  Products take bf16 operands and accumulate in fp32.  q, k, v are
+// bf16 already.  P and, for X, the state are rounded to bf16 once: o itself is
+// bf16, and the two errors are of the size of its own rounding.  The decayed V of
+// the state is split into three bf16 terms (exact to fp32), because errors there
+// would stay in the state, which is kept and returned in fp32.
+//
+// Roles: warps 0-3 turn A into P and combine O (thread = query token); warps 4-11
+// split V and own the state (thread = key channel, half of the value channels);
+// warp 12 issues the loads, warp 13 the products, warp 14 forms the gate vectors.
+// Each stage of the two-stage ring holds Q, K and V of a chunk as TMA boxes.
+//
+// MODE 1 walks K and V alone and writes the state a run of chunks adds to a zero
+// state, with the run's decay.  With few chains, each is cut into runs: MODE 1 over
+// all runs but the last, then MODE 0 over all runs at once, each starting from the
+// sum of the runs before it.
+#include <algorithm>
+
+#include "decay_tc.cuh"
+
+namespace gdn {
+namespace decay {
+namespace {
+
+constexpr int NB = 64;               // value channels per CTA
+constexpr int PANEL = CT * 128;      // bytes of a 128-row, 64-channel tile
+constexpr int kEpi = 4, kState = 8;  // warps of the two epilogue groups
+constexpr int kThreads = 32 * (kEpi + kState + 3);
+constexpr int NST = 2;
+
+template <int DK>
+struct alignas(1024) Smem {
+    struct Stage {
+        unsigned char Q[DK / 64][PANEL], K[DK / 64][PANEL], V[PANEL];
+    } st[NST];
+    // decayed V, three bf16 terms; the third's place first holds the entering
+    // state in bf16, [key channel][64 value channels], until X has read it
+    unsigned char Vt[3][PANEL];
+    Gates gate[NST];
+    uint64_t full[NST], gfull[NST], gfree[NST];
+    uint64_t a_done, p_ready, vt_ready, vt2_ready, n_done, s_ready, x_done, o_done, o_free, drain;
+    uint32_t tmem;
+};
+
+struct Params {
+    CUtensorMap qmap, kmap, vmap;
+    Seqs seq;
+    int H, rep, dv;
+    float scale;
+    const float *g, *h0;
+    __nv_bfloat16* o;
+    float* hT;
+    int runs, len;        // runs per chain, chunks per run
+    float *runS, *runG;   // [chain][value block][run][DK][64] and [chain][run] of MODE 1
+    unsigned int* status;
+};
+
+// tensor-memory columns: A / P of two chunks, X, Y, N
+constexpr uint32_t TA = 0, TX = 256, TY = 320, TN = 384, kCols = 512;
+
+template <int DK, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+decay_tc_walk_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) unsigned char raw[];
+    Smem<DK>& s = *reinterpret_cast<Smem<DK>*>(align1k(raw));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int vb = blockIdx.y, run = blockIdx.z;
+    const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    long long tok0;
+    int n;
+    if (!span_of(p.seq, seq, tok0, n)) {
+        if (tid == 0) atomicOr(p.status, 2u);
+        return;
+    }
+    const int chunks = (n + CT - 1) / CT;
+    const int c0 = run * p.len, c1 = min(chunks, c0 + p.len);
+    // the run that ends the chain (the first of an empty one) writes hT; runs past the end do nothing
+    const bool last = c1 == chunks && (run == 0 || c0 < chunks);
+    if (MODE == 0 ? (c0 >= chunks && !last) : c1 >= chunks) return;
+    const int nc = c1 - c0;
+    const size_t chain = (size_t)seq * p.H + h;
+    const size_t slab = (size_t)DK * NB;
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.gfull[i], 32);
+            mbar_init(&s.gfree[i], MODE == 0 ? kEpi + kState : kState);
+        }
+        mbar_init(&s.a_done, 1);
+        mbar_init(&s.p_ready, kEpi);
+        mbar_init(&s.vt_ready, kState);
+        mbar_init(&s.vt2_ready, kState);
+        mbar_init(&s.n_done, 1);
+        mbar_init(&s.s_ready, kState);
+        mbar_init(&s.x_done, 1);
+        mbar_init(&s.o_done, 1);
+        mbar_init(&s.o_free, kEpi);
+        mbar_init(&s.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == kEpi + kState + 1) tc5::alloc(&s.tmem, kCols);
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    const uint32_t tm = s.tmem;
+    const uint32_t trow = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+
+    if (warp < kEpi) {
+        if constexpr (MODE == 0) {
+            // ---- P, then O: thread = query token --------------------------------
+            const int i = 32 * warp + lane;
+            for (int c = 0; c < nc; ++c) {
+                const int st = c % NST, L = min(CT, n - (c0 + c) * CT);
+                const Gates& G = s.gate[st];
+                const uint32_t ta = trow + TA + 128 * (c & 1);
+                if (!warp_wait(&s.gfull[st], (c / NST) & 1, p.status)) break;
+                if (!warp_wait(&s.a_done, c & 1, p.status)) break;
+                tc5::fence_after();
+                const float rf = warp ? G.row[i] : 0.f;
+                const float2 gi = G.G[i];
+#pragma unroll 1
+                for (int J = 0; J < 4; ++J) {
+                    uint32_t pk[16];
+                    if (J < warp) {
+                        float a[32];
+                        tc5::ld32(a, ta + 32 * J);
+                        tc5::wait_ld();
+                        const float4* cf = reinterpret_cast<const float4*>(&G.col[warp - 1][32 * J]);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float4 f = cf[q];
+                            pk[2 * q] = pack_bf16(a[4 * q] * (rf * f.x), a[4 * q + 1] * (rf * f.y));
+                            pk[2 * q + 1] = pack_bf16(a[4 * q + 2] * (rf * f.z), a[4 * q + 3] * (rf * f.w));
+                        }
+                    } else if (J == warp) {
+                        float a[32];
+                        tc5::ld32(a, ta + 32 * J);
+                        tc5::wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) {
+                            const float d = p.scale * pair_decay(gi, G.G[32 * warp + q]);
+                            a[q] = q <= lane ? a[q] * d : 0.f;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) pk[q] = pack_bf16(a[2 * q], a[2 * q + 1]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) pk[q] = 0;
+                    }
+                    tc5::st16(ta + 16 * J, pk);
+                }
+                tc5::wait_st();
+                tc5::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_ready);
+                const float ein = G.in[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.gfree[st]);
+                if (!warp_wait(&s.o_done, c & 1, p.status)) break;
+                tc5::fence_after();
+                uint32_t w[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float x[32], y[32];
+                    tc5::ld32(x, trow + TX + 32 * q);
+                    tc5::ld32(y, trow + TY + 32 * q);
+                    tc5::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[16 * q + e] = pack_bf16(ein * x[2 * e] + y[2 * e], ein * x[2 * e + 1] + y[2 * e + 1]);
+                }
+                tc5::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.o_free);
+                // lanes 2m, 2m+1 trade 16-byte pieces, so that each store instruction
+                // writes whole 32-byte sectors: first row 2m, then row 2m + 1
+                const bool odd = lane & 1;
+                __nv_bfloat16* row = p.o + ((size_t)(tok0 + (long long)(c0 + c) * CT + (i & ~1)) * p.H + h) * p.dv +
+                                     vb * NB + (odd ? 8 : 0);
+                const size_t next = (size_t)p.H * p.dv;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // pieces 2q and 2q + 1
+                    uint32_t mine[4], got[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        mine[e] = odd ? w[8 * q + 4 + e] : w[8 * q + e];
+                        got[e] = __shfl_xor_sync(0xffffffffu, odd ? w[8 * q + e] : w[8 * q + 4 + e], 1);
+                    }
+                    // even lanes hold piece 2q of both rows, odd lanes piece 2q + 1
+                    const uint4 up = odd ? make_uint4(got[0], got[1], got[2], got[3]) : make_uint4(mine[0], mine[1], mine[2], mine[3]);
+                    const uint4 dn = odd ? make_uint4(mine[0], mine[1], mine[2], mine[3]) : make_uint4(got[0], got[1], got[2], got[3]);
+                    if ((i & ~1) < L) *reinterpret_cast<uint4*>(row + 16 * q) = up;
+                    if ((i | 1) < L) *reinterpret_cast<uint4*>(row + next + 16 * q) = dn;
+                }
+            }
+        }
+    } else if (warp < kEpi + kState) {
+        // ---- the state: thread = key channel r, value channels 32 half .. +31 ------
+        // (and, to split V, thread = token r of the same channels)
+        const int half = (warp - kEpi) >> 2, r = 32 * (warp & 3) + lane;
+        const bool own = r < DK;
+        float S[32];
+        const float* h0 = MODE == 0 && p.h0 && own ? p.h0 + (chain * p.dv + vb * NB + 32 * half) * DK + r : nullptr;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[e] = h0 ? h0[(size_t)e * DK] : 0.f;
+        if (MODE == 0 && own) {
+            for (int q = 0; q < run; ++q) {  // what the runs before this one leave
+                const float a = p.runG[chain * p.runs + q];
+                const float* N = p.runS + ((chain * gridDim.y + vb) * p.runs + q) * slab + (size_t)(32 * half) * DK + r;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[e] = a * S[e] + N[(size_t)e * DK];
+            }
+        }
+        unsigned char* const slot = s.Vt[2];
+        bool ok = true;
+        float total = 1.f, decay = 1.f;
+        for (int c = 0; c < nc; ++c) {
+            const int st = c % NST, L = min(CT, n - (c0 + c) * CT);
+            if (c > 0) {  // S entering chunk c
+                if (!(ok = warp_wait(&s.n_done, (c - 1) & 1, p.status))) break;
+                tc5::fence_after();
+                float N[32];
+                tc5::ld32(N, trow + TN + 32 * half);
+                tc5::wait_ld();
+                tc5::fence_before();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[e] = total * S[e] + N[e];
+            }
+            if constexpr (MODE == 0) {
+                if (own) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(slot + 2 * swz<64>(r, 32 * half + 8 * q)) =
+                            make_uint4(pack_bf16(S[8 * q], S[8 * q + 1]), pack_bf16(S[8 * q + 2], S[8 * q + 3]),
+                                       pack_bf16(S[8 * q + 4], S[8 * q + 5]), pack_bf16(S[8 * q + 6], S[8 * q + 7]));
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.s_ready);
+            }
+            if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1, p.status))) break;
+            if (!(ok = warp_wait(&s.full[st], (c / NST) & 1, p.status))) break;
+            // decayed V in three terms; rows past the chunk's tokens become zero in V and K too
+            const float wt = s.gate[st].out[r];
+            total = s.gate[st].total;
+            decay *= total;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.gfree[st]);
+            uint4 third[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t at = 2 * swz<64>(r, 32 * half + 8 * q);
+                uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
+                if (r >= L) {
+                    v = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
+                }
+                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                uint32_t t[4][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack_bf16(in[e]);
+                    split_bf16<3>(t[e], wt * f.x, wt * f.y);
+                }
+                *reinterpret_cast<uint4*>(s.Vt[0] + at) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
+                *reinterpret_cast<uint4*>(s.Vt[1] + at) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+                third[q] = make_uint4(t[0][2], t[1][2], t[2][2], t[3][2]);
+            }
+            if (r >= L) {
+#pragma unroll
+                for (int q = 0; q < DK / 16; ++q) {
+                    const int ch = half * (DK / 16) + q;  // 16-byte piece of the K row
+                    *reinterpret_cast<uint4*>(s.st[st].K[ch >> 3] + 2 * swz<64>(r, 8 * (ch & 7))) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.vt_ready);
+            if (MODE == 0 && !(ok = warp_wait(&s.x_done, c & 1, p.status))) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(slot + 2 * swz<64>(r, 32 * half + 8 * q)) = third[q];
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.vt2_ready);
+        }
+        if (ok && nc > 0) {
+            if (warp_wait(&s.n_done, (nc - 1) & 1, p.status)) {
+                tc5::fence_after();
+                float N[32];
+                tc5::ld32(N, trow + TN + 32 * half);
+                tc5::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[e] = total * S[e] + N[e];
+            }
+        }
+        if (own) {
+            float* to = nullptr;
+            if (MODE == 1) to = p.runS + ((chain * gridDim.y + vb) * p.runs + run) * slab + (size_t)(32 * half) * DK + r;
+            else if (last && p.hT) to = p.hT + (chain * p.dv + vb * NB + 32 * half) * DK + r;
+            if (to) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) to[(size_t)e * DK] = S[e];
+            }
+        }
+        if (MODE == 1 && vb == 0 && warp == kEpi && lane == 0) p.runG[chain * p.runs + run] = decay;
+    } else if (warp == kEpi + kState) {
+        // ---- loads -----------------------------------------------------------
+        if (lane == 0) {
+            int c = 0;
+            for (; c < nc; ++c) {
+                // each operand goes in as soon as the products of two chunks before are done with it
+                const int st = c % NST, ph = (c - NST) & 1;
+                auto& q = s.st[st];
+                const int tok = (int)(tok0 + (long long)(c0 + c) * CT), kh = h / p.rep;
+                if constexpr (MODE == 0) {
+                    if (c >= NST && !mbar_wait(&s.x_done, ph, p.status)) break;
+                    mbar_arrive_expect(&s.full[st], (2 * DK / 64 + 1) * PANEL);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) tma_load_3d(q.Q[x], &p.qmap, 64 * x, kh, tok, &s.full[st]);
+                }
+                const bool go = c < NST || mbar_wait(&s.n_done, ph, p.status);
+                if constexpr (MODE == 1) {
+                    if (!go) break;
+                    mbar_arrive_expect(&s.full[st], (DK / 64 + 1) * PANEL);
+                }
+                if (go) {
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) tma_load_3d(q.K[x], &p.kmap, 64 * x, kh, tok, &s.full[st]);
+                }
+                if (!go || (MODE == 0 && c >= NST && !mbar_wait(&s.o_done, ph, p.status))) {
+                    ++c;  // part of this chunk's loads are in flight, the others will not come
+                    break;
+                }
+                tma_load_3d(q.V, &p.vmap, vb * NB, h, tok, &s.full[st]);
+            }
+            // no copy may be in flight when the CTA ends (after a wait that gave up, a
+            // stage that is not whole makes this one give up too: by then its copies are in)
+            for (int d = max(0, c - NST); d < c; ++d) mbar_wait(&s.full[d % NST], (d / NST) & 1, p.status);
+        }
+    } else if (warp == kEpi + kState + 1) {
+        // ---- products ----------------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t ID_A = tc5::idesc_bf16(128, 128, false, false);
+            constexpr uint32_t ID_X = tc5::idesc_bf16(128, NB, false, true);
+            constexpr uint32_t ID_N = tc5::idesc_bf16(128, NB, true, true);
+            const uint32_t sVt = smem_u32(s.Vt);
+            for (int c = 0; c < nc; ++c) {
+                const int st = c % NST;
+                const uint32_t sK = smem_u32(s.st[st].K), sV = smem_u32(s.st[st].V), sQ = smem_u32(s.st[st].Q);
+                const uint32_t ta = tm + TA + 128 * (c & 1);
+                if constexpr (MODE == 0) {
+                    // A(c) goes where P(c-2) was: chunk c-2's o_free came before X(c-1)
+                    if (!mbar_wait(&s.full[st], (c / NST) & 1, p.status)) break;
+                    tc5::fence_after();
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k) tc5::mma(ta, tc5::kmajor<CT>(sQ, k), tc5::kmajor<CT>(sK, k), ID_A, k > 0);
+                    tc5::commit(&s.a_done);
+                    if (!mbar_wait(&s.s_ready, c & 1, p.status)) break;
+                    if (c > 0 && !mbar_wait(&s.o_free, (c - 1) & 1, p.status)) break;
+                    tc5::fence_after();
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k)
+                        tc5::mma(tm + TX, tc5::kmajor<CT>(sQ, k), tc5::mnmajor(sVt + 2 * PANEL, k, PANEL), ID_X, k > 0);
+                    tc5::commit(&s.x_done);
+                }
+                // N(c); with 64 key channels lanes 64-127 read the V tile behind K and are ignored
+                if (!mbar_wait(&s.vt_ready, c & 1, p.status)) break;
+                tc5::fence_after();
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < CT / 16; ++k)
+                        tc5::mma(tm + TN, tc5::mnmajor(sK, k, PANEL), tc5::mnmajor(sVt + t * PANEL, k, PANEL), ID_N, t + k > 0);
+                if (!mbar_wait(&s.vt2_ready, c & 1, p.status)) break;
+                tc5::fence_after();
+#pragma unroll
+                for (int k = 0; k < CT / 16; ++k)
+                    tc5::mma(tm + TN, tc5::mnmajor(sK, k, PANEL), tc5::mnmajor(sVt + 2 * PANEL, k, PANEL), ID_N, true);
+                tc5::commit(&s.n_done);
+                if constexpr (MODE == 0) {
+                    if (!mbar_wait(&s.p_ready, c & 1, p.status)) break;
+                    tc5::fence_after();
+#pragma unroll
+                    for (int k = 0; k < CT / 16; ++k)
+                        tc5::mma_ts(tm + TY, ta + 8 * k, tc5::mnmajor(sV, k, PANEL), ID_X, k > 0);
+                    tc5::commit(&s.o_done);
+                }
+            }
+            tc5::commit(&s.drain);  // no product may be in flight when the CTA ends
+            mbar_wait(&s.drain, 0, p.status);
+        }
+    } else {
+        // ---- gates: the next chunk's values are loaded before this one's are needed ----
+        float x[4], y[4];
+        const float* g = p.g + (size_t)(tok0 + (long long)c0 * CT) * p.H + h;
+        if (nc > 0) load_gates(x, g, p.H, min(CT, n - c0 * CT));
+        for (int c = 0; c < nc; ++c) {
+            const int st = c % NST;
+            if (c + 1 < nc) load_gates(y, g + (size_t)(c + 1) * CT * p.H, p.H, min(CT, n - (c0 + c + 1) * CT));
+            if (c >= NST && !warp_wait(&s.gfree[st], ((c / NST) - 1) & 1, p.status)) break;
+            form_gates(s.gate[st], x, min(CT, n - (c0 + c) * CT), p.scale, MODE == 0);
+            mbar_arrive(&s.gfull[st]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = y[j];
+        }
+    }
+    tc5::fence_before();
+    __syncthreads();
+    if (warp == kEpi + kState + 1) {
+        tc5::fence_after();
+        tc5::dealloc(tm, kCols);
+    }
+}
+
+// Runs per chain: 1 when the chains fill the device; otherwise the number that
+// gives the shortest estimated time, in chunk steps on the critical path.  A
+// step of the walk costs about 1, one of the map (MODE 1) about 0.7, and the
+// second launch about 4.
+struct Cut {
+    int runs, len;
+};
+Cut cut(long long ctas, int chunks) {
+    Cut best{1, std::max(chunks, 1)};
+    auto waves = [](long long n) { return (double)((n + 147) / 148); };
+    double cost = chunks * waves(ctas);
+    for (int r = 2; r <= 16 && r <= chunks; ++r) {
+        const int len = (chunks + r - 1) / r, runs = (chunks + len - 1) / len;
+        const double c = len * (waves(ctas * runs) + 0.7 * waves(ctas * (runs - 1))) + 4;
+        if (c < 0.9 * cost) {
+            cost = c;
+            best = Cut{runs, len};
+        }
+    }
+    return best;
+}
+
+Cut cut_of(const Problem& p) {
+    return cut((long long)p.seq.nseq * p.H * (p.dv / NB), ((p.seq.cu ? p.seq.rows : p.seq.len) + CT - 1) / CT);
+}
+
+template <int DK, int MODE>
+void launch(const Params& a, dim3 grid, cudaStream_t st) {
+    const int smem = sizeof(Smem<DK>) + 1024;
+    cudaFuncSetAttribute(decay_tc_walk_kernel<DK, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    GDN_LAUNCH(MODE == 0 ? "decay_tc_walk" : "decay_tc_map", st, (decay_tc_walk_kernel<DK, MODE><<<grid, kThreads, smem, st>>>(a)));
+}
+
+}  // namespace
+
+bool tc_supported(const Problem& p) {
+    return p.dtype == GDN_BF16 && (p.dk == 64 || p.dk == 128) && (p.dv == 64 || p.dv == 128);
+}
+
+size_t tc_fwd_workspace(const Problem& p) {
+    const Cut c = cut_of(p);
+    if (c.runs == 1) return kStatusBytes;
+    const size_t chains = (size_t)p.seq.nseq * p.H;
+    return kStatusBytes + chains * c.runs * ((size_t)p.dk * p.dv * 4) + ((chains * c.runs * 4 + 255) & ~(size_t)255);
+}
+
+bool launch_tc_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
+                   void* o, float* hT, void* ws, cudaStream_t st) {
+    Params a{};
+    if (!encode_head_map(&a.qmap, q, p.seq.rows, p.Hk, p.dk, CT) || !encode_head_map(&a.kmap, k, p.seq.rows, p.Hk, p.dk, CT) ||
+        !encode_head_map(&a.vmap, v, p.seq.rows, p.H, p.dv, CT))
+        return false;
+    const Cut c = cut_of(p);
+    const size_t chains = (size_t)p.seq.nseq * p.H;
+    a.seq = p.seq; a.H = p.H; a.rep = p.H / p.Hk; a.dv = p.dv; a.scale = p.scale;
+    a.g = g; a.h0 = h0; a.o = (__nv_bfloat16*)o; a.hT = hT;
+    a.runs = c.runs; a.len = c.len;
+    a.status = (unsigned int*)ws;
+    a.runS = (float*)((char*)ws + kStatusBytes);
+    a.runG = a.runS + chains * c.runs * p.dk * p.dv;
+    const dim3 grid((unsigned)chains, p.dv / NB, c.runs);
+    if (c.runs > 1) {
+        const dim3 maps(grid.x, grid.y, c.runs - 1);
+        if (p.dk == 64) launch<64, 1>(a, maps, st);
+        else launch<128, 1>(a, maps, st);
+    }
+    if (p.dk == 64) launch<64, 0>(a, grid, st);
+    else launch<128, 0>(a, grid, st);
+    return true;
+}
+
+}  // namespace decay
+}  // namespace gdn

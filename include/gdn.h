@@ -335,9 +335,9 @@ gdn_status gdn_recurrent_step(int N, int H, int dk, int dv, gdn_dtype dtype,
  * cu_seqlens[s + 1] - 1, and the states are [nseq, H, dv, dk]; empty sequences
  * pass h0 to hT (dhT to dh0).  Tokens of no sequence (before the first, behind
  * the last) are not read, and their rows of o, dq, dk, dv, dg are left as they
- * were.  A sequence whose offsets are not 0 <= cu[s] <= cu[s+1] <= T is skipped
- * and makes gdn_query_device_status on the workspace return
- * GDN_ERR_INVALID_ARG; sequences must not overlap.  nseq = 0 with a null
+ * were.  A sequence whose offsets are not 0 <= cu[s] <= cu[s+1] <= T, or where
+ * cu[s-1] > cu[s], is skipped and makes gdn_query_device_status on the workspace
+ * return GDN_ERR_INVALID_ARG; sequences must not overlap.  nseq = 0 with a null
  * cu_seqlens is the plain batch.
  * Values: g <= 0 (documented, not checked); g = -inf is a reset.  The decay of a
  * pair of tokens is formed from an fp64 cumsum or token by token, the state and
