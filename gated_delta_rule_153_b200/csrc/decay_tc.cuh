@@ -14,78 +14,64 @@ namespace decay {
 
 constexpr int CT = 128;  // tokens per chunk of the tensor-core kernels
 
-// What the products of a chunk need of its gates.  G is the inclusive cumsum of
-// log2(e) g over the chunk, formed in fp64 and kept as a pair of floats: the
-// decay of a pair of tokens is then exact to fp32 however long the cumsum.
-// Decays between 32-token blocks factor into one of the row and one of the
-// column about the end of the block before the row's; both are at most 1.
+// 2^x; results below 2^-126 are zero.
+GDN_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The gates of a chunk: the inclusive cumsum of log2(e) g over its tokens, as an
+// unevaluated sum of two floats, so that the decay of a pair of tokens is exact to
+// fp32 however long the cumsum.  Tokens past the sequence repeat the last value.
 struct alignas(16) Gates {
-    float2 G[CT];        // high and low part
-    float in[CT];        // scale e^{G_i}: from the state entering the chunk to token i
-    float out[CT];       // e^{G_last - G_j}: from token j to the chunk's end (zero past its tokens)
-    float row[CT];       // scale e^{G_i - G_b}, b = the last token before i's block (rows of block 0 unused)
-    float col[3][96];    // [block - 1][j] e^{G_b - G_j}, j <= b
-    float total;         // e^{G_last}
-    double scratch[CT];
+    float2 G[CT];
 };
 
-// One warp: the gates of a chunk of L <= 128 tokens; lane l holds tokens 4l ..
-// 4l+3.  g points at the chunk's first token's gate, tokens `stride` apart.
+// One warp: the gates of a chunk of L <= 128 tokens; lane l holds tokens 4l .. 4l+3.
+// g points at the chunk's first token's gate, tokens `stride` apart.
 GDN_DEV void load_gates(float (&x)[4], const float* g, size_t stride, int L) {
-    const int lane = threadIdx.x & 31;
+    const int t = 4 * (threadIdx.x & 31);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int t = 4 * lane + j;
-        x[j] = t < L ? g[(size_t)t * stride] : 0.f;
-    }
+    for (int j = 0; j < 4; ++j) x[j] = t + j < L ? g[(size_t)(t + j) * stride] : 0.f;
 }
-GDN_DEV void form_gates(Gates& s, const float (&x)[4], int L, float scale, bool pairs) {
+// (a, b) <- a + b in two floats each: the rounding error of the high parts' sum
+// (exact, from the difference of what went in and what came out) joins the low.
+GDN_DEV float2 add2(float2 a, float2 b) {
+    const float s = a.x + b.x, v = s - a.x;
+    const float e = ((a.x - (s - v)) + (b.x - v)) + (a.y + b.y);
+    const float hi = s + e;
+    return make_float2(hi, e - (hi - s));
+}
+GDN_DEV float diff2(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
+
+// From token j to token i of a chunk, j <= i.
+GDN_DEV float pair_decay(float2 gi, float2 gj) { return ex2(diff2(gi, gj)); }
+// From the chunk's start to token i.
+GDN_DEV float start_decay(float2 gi) { return ex2(gi.x) * fmaf(gi.y, 0.693147182f, 1.f); }
+
+GDN_DEV void form_gates(Gates& s, const float (&x)[4]) {
     const int lane = threadIdx.x & 31;
-    double c[4], run = 0.0;
+    float2 c[4];  // sums within the lane
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         // e^g below 2^-400 is zero in fp32 as it is; -inf would not survive a difference
-        const double y = (double)x[j] * 1.4426950408889634;
-        run += y < -400.0 ? -400.0 : y;
-        c[j] = run;
+        const float g = x[j] < -277.f ? -277.f : x[j];
+        const float hi = g * 1.44269502f;
+        c[j] = make_float2(hi, fmaf(g, 1.44269502f, -hi) + g * 1.92596299e-8f);
+        if (j > 0) c[j] = add2(c[j], c[j - 1]);
     }
-    double before = run;
-#pragma unroll
+    float2 run = c[3];  // over this lane and those before it
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += y;
+        const float2 y = make_float2(__shfl_up_sync(0xffffffffu, run.x, o), __shfl_up_sync(0xffffffffu, run.y, o));
+        if (lane >= o) run = add2(run, y);
     }
-    const double last = __shfl_sync(0xffffffffu, before, 31);
-    before -= run;
+    float2 before = make_float2(__shfl_up_sync(0xffffffffu, run.x, 1), __shfl_up_sync(0xffffffffu, run.y, 1));
+    if (lane == 0) before = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int t = 4 * lane + j;
-        c[j] += before;
-        const float hi = (float)c[j];
-        s.G[t] = make_float2(hi, (float)(c[j] - (double)hi));
-        s.in[t] = scale * exp2f((float)c[j]);
-        s.out[t] = t < L ? exp2f((float)(last - c[j])) : 0.f;
-        s.scratch[t] = c[j];
-    }
-    if (lane == 0) s.total = exp2f((float)last);
-    __syncwarp();
-    if (pairs) {
-        const int b = lane / 8;  // this lane's tokens are all of block b
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (b > 0) s.row[4 * lane + j] = scale * exp2f((float)(c[j] - s.scratch[32 * b - 1]));
-#pragma unroll
-        for (int k = 1; k < 4; ++k) {
-            const double base = s.scratch[32 * k - 1];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (b < k) s.col[k - 1][4 * lane + j] = exp2f((float)(base - c[j]));
-        }
-    }
+    for (int j = 0; j < 4; ++j) s.G[4 * lane + j] = add2(c[j], before);
 }
-
-// Decay between two tokens of one block, from their pairs.
-GDN_DEV float pair_decay(float2 gi, float2 gj) { return exp2f((gi.x - gj.x) + (gi.y - gj.y)); }
 
 // x and y as sums of TERMS bf16 values each (2 terms: to 2^-16, 3: to 2^-24),
 // packed as (x, y) per term.
@@ -102,11 +88,35 @@ GDN_DEV void split_bf16(uint32_t (&t)[TERMS], float x, float y) {
     }
 }
 
-// mbar_wait by a whole warp with one answer for all its lanes, whose next
-// instructions (tensor-memory loads, shuffles) need them together.
-GDN_DEV bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+// A bounded wait in few instructions: these kernels run five roles' loops side by
+// side, and their footprint in the instruction cache counts.  Each try is given
+// a microsecond, a million of them are a second at most.  The caller reports a
+// wait that gave up once, after its loop.
+GDN_DEV bool wait_for(uint64_t* bar, uint32_t parity) {
+    uint32_t ok, n = 0;
+    const uint32_t at = smem_u32(bar);
+    do {
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(at), "r"(parity), "r"(1000) : "memory");
+    } while (!ok && ++n < 1000000);
+    return ok != 0;
 }
+
+// One lane of a converged warp, chosen so that the compiler knows the branch to
+// be the whole warp's: the products behind it take their operands from uniform
+// registers (M = 128, N = 64: 48 cycles each against 56 behind lane == 0).
+GDN_DEV bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// wait_for by a whole warp with one answer for all its lanes, whose next
+// instructions (tensor-memory loads, shuffles) need them together.
+GDN_DEV bool warp_wait(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity)); }
 
 GDN_DEV unsigned char* align1k(unsigned char* p) {
     return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));

@@ -22,10 +22,11 @@
 // the state is split into three bf16 terms (exact to fp32), because errors there
 // would stay in the state, which is kept and returned in fp32.
 //
-// Roles: warps 0-3 turn A into P and combine O (thread = query token); warps 4-11
+// Roles: warps 0-7 turn A into P and combine O (thread = query token); warps 8-15
 // split V and own the state (thread = key channel, half of the value channels);
-// warp 12 issues the loads, warp 13 the products, warp 14 forms the gate vectors.
-// Each stage of the two-stage ring holds Q, K and V of a chunk as TMA boxes.
+// warp 16 issues the loads, warp 17 the products, warp 18 forms the gates' cumsum.
+// K and V tiles go through a two-stage ring; Q, which A and X are done with early
+// in a chunk, has one place.
 //
 // MODE 1 walks K and V alone and writes the state a run of chunks adds to a zero
 // state, with the run's decay.  With few chains, each is cut into runs: MODE 1 over
@@ -41,21 +42,22 @@ namespace {
 
 constexpr int NB = 64;               // value channels per CTA
 constexpr int PANEL = CT * 128;      // bytes of a 128-row, 64-channel tile
-constexpr int kEpi = 4, kState = 8;  // warps of the two epilogue groups
+constexpr int kEpi = 8, kState = 8;  // warps of the two epilogue groups
 constexpr int kThreads = 32 * (kEpi + kState + 3);
 constexpr int NST = 2;
 
 template <int DK>
 struct alignas(1024) Smem {
+    unsigned char Q[DK / 64][PANEL];
     struct Stage {
-        unsigned char Q[DK / 64][PANEL], K[DK / 64][PANEL], V[PANEL];
+        unsigned char K[DK / 64][PANEL], V[PANEL];
     } st[NST];
-    // decayed V, three bf16 terms; the third's place first holds the entering
-    // state in bf16, [key channel][64 value channels], until X has read it
-    unsigned char Vt[3][PANEL];
+    unsigned char Vt[3][PANEL];  // decayed V, three bf16 terms
+    unsigned char S[DK * 128];   // the entering state in bf16, [key channel][64 value channels]
     Gates gate[NST];
+    float col[kEpi][96];         // per warp of P: decays from token j to the end of the block before its own
     uint64_t full[NST], gfull[NST], gfree[NST];
-    uint64_t a_done, p_ready, vt_ready, vt2_ready, n_done, s_ready, x_done, o_done, o_free, drain;
+    uint64_t q_full, a_done, p_ready, vt_ready, n_done, s_ready, x_done, o_done, o_free, drain;
     uint32_t tmem;
 };
 
@@ -72,8 +74,8 @@ struct Params {
     unsigned int* status;
 };
 
-// tensor-memory columns: A / P of two chunks, X, Y, N
-constexpr uint32_t TA = 0, TX = 256, TY = 320, TN = 384, kCols = 512;
+// tensor-memory columns: A, P (bf16 pairs), X, Y, N (the terms of V apart)
+constexpr uint32_t TA = 0, TP = 128, TX = 192, TY = 256, TN = 320, kCols = 512;
 
 template <int DK, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -104,10 +106,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             mbar_init(&s.gfull[i], 32);
             mbar_init(&s.gfree[i], MODE == 0 ? kEpi + kState : kState);
         }
+        mbar_init(&s.q_full, 1);
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
         mbar_init(&s.vt_ready, kState);
-        mbar_init(&s.vt2_ready, kState);
         mbar_init(&s.n_done, 1);
         mbar_init(&s.s_ready, kState);
         mbar_init(&s.x_done, 1);
@@ -120,96 +122,113 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
-    const uint32_t tm = s.tmem;
+    const uint32_t tm = __shfl_sync(0xffffffffu, s.tmem, 0);
+    int done = 0;  // chunks this warp went through: fewer than nc after a wait that gave up
     const uint32_t trow = tm + ((uint32_t)(32 * (warp & 3)) << 16);
 
     if (warp < kEpi) {
         if constexpr (MODE == 0) {
             // ---- P, then O: thread = query token --------------------------------
-            const int i = 32 * warp + lane;
+            // (two warps per 32 tokens: odd and even 16-column pieces of A, halves of O)
+            const int blk = warp & 3, half = warp >> 2, i = 32 * blk + lane;
             for (int c = 0; c < nc; ++c) {
                 const int st = c % NST, L = min(CT, n - (c0 + c) * CT);
                 const Gates& G = s.gate[st];
-                const uint32_t ta = trow + TA + 128 * (c & 1);
-                if (!warp_wait(&s.gfull[st], (c / NST) & 1, p.status)) break;
-                if (!warp_wait(&s.a_done, c & 1, p.status)) break;
-                tc5::fence_after();
-                const float rf = warp ? G.row[i] : 0.f;
+                if (!warp_wait(&s.gfull[st], (c / NST) & 1)) break;
+                // decays between blocks factor at the end of the block before this row's: both
+                // factors are at most 1.  Those of the columns are shared by the warp's rows.
                 const float2 gi = G.G[i];
+                float rf = 0.f, *const col = s.col[warp];
+                if (blk) {
+                    const float2 gb = G.G[32 * blk - 1];
+                    rf = p.scale * pair_decay(gi, gb);
+                    __syncwarp();
 #pragma unroll 1
-                for (int J = 0; J < 4; ++J) {
-                    uint32_t pk[16];
-                    if (J < warp) {
-                        float a[32];
-                        tc5::ld32(a, ta + 32 * J);
-                        tc5::wait_ld();
-                        const float4* cf = reinterpret_cast<const float4*>(&G.col[warp - 1][32 * J]);
+                    for (int j = lane; j < 32 * blk; j += 32) col[j] = pair_decay(gb, G.G[j]);
+                    __syncwarp();
+                }
+                const float ein = p.scale * start_decay(gi);
+                const uint32_t tp = trow + TP;
+                if (!warp_wait(&s.a_done, c & 1)) break;
+                tc5::fence_after();
+#pragma unroll 1
+                for (int J = half; J < 2 * blk; J += 2) {  // the blocks before this row's
+                    float a[16];
+                    uint32_t pk[8];
+                    tc5::ld16(a, trow + TA + 16 * J);
+                    tc5::wait_ld();
+                    const float4* cf = reinterpret_cast<const float4*>(col + 16 * J);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float4 f = cf[q];
-                            pk[2 * q] = pack_bf16(a[4 * q] * (rf * f.x), a[4 * q + 1] * (rf * f.y));
-                            pk[2 * q + 1] = pack_bf16(a[4 * q + 2] * (rf * f.z), a[4 * q + 3] * (rf * f.w));
-                        }
-                    } else if (J == warp) {
-                        float a[32];
-                        tc5::ld32(a, ta + 32 * J);
-                        tc5::wait_ld();
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) {
-                            const float d = p.scale * pair_decay(gi, G.G[32 * warp + q]);
-                            a[q] = q <= lane ? a[q] * d : 0.f;
-                        }
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) pk[q] = pack_bf16(a[2 * q], a[2 * q + 1]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) pk[q] = 0;
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 f = cf[q];
+                        pk[2 * q] = pack_bf16(a[4 * q] * (rf * f.x), a[4 * q + 1] * (rf * f.y));
+                        pk[2 * q + 1] = pack_bf16(a[4 * q + 2] * (rf * f.z), a[4 * q + 3] * (rf * f.w));
                     }
-                    tc5::st16(ta + 16 * J, pk);
+                    tc5::st8(tp + 8 * J, pk);
+                }
+                {   // the diagonal block
+                    const int j0 = 32 * blk + 16 * half;
+                    float a[16];
+                    uint32_t pk[8];
+                    tc5::ld16(a, trow + TA + j0);
+                    tc5::wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float d = p.scale * pair_decay(gi, G.G[j0 + q]);
+                        a[q] = j0 + q <= i ? a[q] * d : 0.f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) pk[q] = pack_bf16(a[2 * q], a[2 * q + 1]);
+                    tc5::st8(tp + j0 / 2, pk);
+                }
+                {
+                    const uint32_t zero[8] = {};
+#pragma unroll 1
+                    for (int J = 2 * blk + 2 + half; J < 8; J += 2) tc5::st8(tp + 8 * J, zero);
                 }
                 tc5::wait_st();
                 tc5::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_ready);
-                const float ein = G.in[i];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.gfree[st]);
-                if (!warp_wait(&s.o_done, c & 1, p.status)) break;
-                tc5::fence_after();
-                uint32_t w[32];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float x[32], y[32];
-                    tc5::ld32(x, trow + TX + 32 * q);
-                    tc5::ld32(y, trow + TY + 32 * q);
-                    tc5::wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        w[16 * q + e] = pack_bf16(ein * x[2 * e] + y[2 * e], ein * x[2 * e + 1] + y[2 * e + 1]);
+                if (lane == 0) {
+                    mbar_arrive(&s.p_ready);
+                    mbar_arrive(&s.gfree[st]);
                 }
-                tc5::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.o_free);
+                if (!warp_wait(&s.o_done, c & 1)) break;
+                tc5::fence_after();
                 // lanes 2m, 2m+1 trade 16-byte pieces, so that each store instruction
                 // writes whole 32-byte sectors: first row 2m, then row 2m + 1
                 const bool odd = lane & 1;
                 __nv_bfloat16* row = p.o + ((size_t)(tok0 + (long long)(c0 + c) * CT + (i & ~1)) * p.H + h) * p.dv +
-                                     vb * NB + (odd ? 8 : 0);
+                                     vb * NB + 32 * half + (odd ? 8 : 0);
                 const size_t next = (size_t)p.H * p.dv;
+                const bool up = (i & ~1) < L, dn = (i | 1) < L;
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    float x[16], y[16];
+                    tc5::ld16(x, trow + TX + 32 * half + 16 * q);
+                    tc5::ld16(y, trow + TY + 32 * half + 16 * q);
+                    tc5::wait_ld();
+                    if (q == 1) {
+                        tc5::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.o_free);
+                    }
+                    uint32_t w[8], mine[4], got[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {  // pieces 2q and 2q + 1
-                    uint32_t mine[4], got[4];
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = pack_bf16(ein * x[2 * e] + y[2 * e], ein * x[2 * e + 1] + y[2 * e + 1]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        mine[e] = odd ? w[8 * q + 4 + e] : w[8 * q + e];
-                        got[e] = __shfl_xor_sync(0xffffffffu, odd ? w[8 * q + e] : w[8 * q + 4 + e], 1);
+                        mine[e] = odd ? w[4 + e] : w[e];
+                        got[e] = __shfl_xor_sync(0xffffffffu, odd ? w[e] : w[4 + e], 1);
                     }
-                    // even lanes hold piece 2q of both rows, odd lanes piece 2q + 1
-                    const uint4 up = odd ? make_uint4(got[0], got[1], got[2], got[3]) : make_uint4(mine[0], mine[1], mine[2], mine[3]);
-                    const uint4 dn = odd ? make_uint4(mine[0], mine[1], mine[2], mine[3]) : make_uint4(got[0], got[1], got[2], got[3]);
-                    if ((i & ~1) < L) *reinterpret_cast<uint4*>(row + 16 * q) = up;
-                    if ((i | 1) < L) *reinterpret_cast<uint4*>(row + next + 16 * q) = dn;
+                    // even lanes now hold the first piece of both rows, odd lanes the second
+                    const uint4 a = make_uint4(mine[0], mine[1], mine[2], mine[3]);
+                    const uint4 b = make_uint4(got[0], got[1], got[2], got[3]);
+                    if (up) *reinterpret_cast<uint4*>(row + 16 * q) = odd ? b : a;
+                    if (dn) *reinterpret_cast<uint4*>(row + next + 16 * q) = odd ? a : b;
                 }
+                ++done;
             }
         }
     } else if (warp < kEpi + kState) {
@@ -229,26 +248,32 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 for (int e = 0; e < 32; ++e) S[e] = a * S[e] + N[(size_t)e * DK];
             }
         }
-        unsigned char* const slot = s.Vt[2];
         bool ok = true;
         float total = 1.f, decay = 1.f;
+        auto add_n = [&]() {  // S <- e^{G_last} S + N, N in one accumulator per term of V
+#pragma unroll 1
+            for (int x = 0; x < 3; ++x) {
+                float N[32];
+                tc5::ld32(N, trow + TN + NB * x + 32 * half);
+                tc5::wait_ld();
+                const float a = x ? 1.f : total;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[e] = a * S[e] + N[e];
+            }
+            tc5::fence_before();
+        };
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST, L = min(CT, n - (c0 + c) * CT);
-            if (c > 0) {  // S entering chunk c
-                if (!(ok = warp_wait(&s.n_done, (c - 1) & 1, p.status))) break;
+            if (c > 0) {  // S entering chunk c; X(c-1), which read the last one, came before N(c-1)
+                if (!(ok = warp_wait(&s.n_done, (c - 1) & 1))) break;
                 tc5::fence_after();
-                float N[32];
-                tc5::ld32(N, trow + TN + 32 * half);
-                tc5::wait_ld();
-                tc5::fence_before();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) S[e] = total * S[e] + N[e];
+                add_n();
             }
             if constexpr (MODE == 0) {
                 if (own) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4*>(slot + 2 * swz<64>(r, 32 * half + 8 * q)) =
+                        *reinterpret_cast<uint4*>(s.S + 2 * swz<64>(r, 32 * half + 8 * q)) =
                             make_uint4(pack_bf16(S[8 * q], S[8 * q + 1]), pack_bf16(S[8 * q + 2], S[8 * q + 3]),
                                        pack_bf16(S[8 * q + 4], S[8 * q + 5]), pack_bf16(S[8 * q + 6], S[8 * q + 7]));
                 }
@@ -256,16 +281,16 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.s_ready);
             }
-            if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1, p.status))) break;
-            if (!(ok = warp_wait(&s.full[st], (c / NST) & 1, p.status))) break;
-            // decayed V in three terms; rows past the chunk's tokens become zero in V and K too
-            const float wt = s.gate[st].out[r];
-            total = s.gate[st].total;
+            if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
+            const float2 ge = s.gate[st].G[CT - 1];
+            const float wt = r < L ? pair_decay(ge, s.gate[st].G[r]) : 0.f;
+            total = start_decay(ge);
             decay *= total;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.gfree[st]);
-            uint4 third[4];
-#pragma unroll
+            if (!(ok = warp_wait(&s.full[st], (c / NST) & 1))) break;
+            // decayed V in three terms; rows past the chunk's tokens become zero in V and K too
+#pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 const uint32_t at = 2 * swz<64>(r, 32 * half + 8 * q);
                 uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
@@ -280,12 +305,12 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     const float2 f = unpack_bf16(in[e]);
                     split_bf16<3>(t[e], wt * f.x, wt * f.y);
                 }
-                *reinterpret_cast<uint4*>(s.Vt[0] + at) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
-                *reinterpret_cast<uint4*>(s.Vt[1] + at) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
-                third[q] = make_uint4(t[0][2], t[1][2], t[2][2], t[3][2]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
             }
             if (r >= L) {
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < DK / 16; ++q) {
                     const int ch = half * (DK / 16) + q;  // 16-byte piece of the K row
                     *reinterpret_cast<uint4*>(s.st[st].K[ch >> 3] + 2 * swz<64>(r, 8 * (ch & 7))) = make_uint4(0, 0, 0, 0);
@@ -294,21 +319,12 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.vt_ready);
-            if (MODE == 0 && !(ok = warp_wait(&s.x_done, c & 1, p.status))) break;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(slot + 2 * swz<64>(r, 32 * half + 8 * q)) = third[q];
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.vt2_ready);
+            ++done;
         }
         if (ok && nc > 0) {
-            if (warp_wait(&s.n_done, (nc - 1) & 1, p.status)) {
+            if (warp_wait(&s.n_done, (nc - 1) & 1)) {
                 tc5::fence_after();
-                float N[32];
-                tc5::ld32(N, trow + TN + 32 * half);
-                tc5::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) S[e] = total * S[e] + N[e];
+                add_n();
             }
         }
         if (own) {
@@ -324,104 +340,115 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     } else if (warp == kEpi + kState) {
         // ---- loads -----------------------------------------------------------
         if (lane == 0) {
-            int c = 0;
+            int c = 0, nq = 0;
             for (; c < nc; ++c) {
-                // each operand goes in as soon as the products of two chunks before are done with it
+                // each operand goes in as soon as the products are done with the last in its place
                 const int st = c % NST, ph = (c - NST) & 1;
                 auto& q = s.st[st];
                 const int tok = (int)(tok0 + (long long)(c0 + c) * CT), kh = h / p.rep;
-                if constexpr (MODE == 0) {
-                    if (c >= NST && !mbar_wait(&s.x_done, ph, p.status)) break;
-                    mbar_arrive_expect(&s.full[st], (2 * DK / 64 + 1) * PANEL);
+                if (c >= NST && !wait_for(&s.n_done, ph)) break;
+                mbar_arrive_expect(&s.full[st], (DK / 64 + 1) * PANEL);
 #pragma unroll
-                    for (int x = 0; x < DK / 64; ++x) tma_load_3d(q.Q[x], &p.qmap, 64 * x, kh, tok, &s.full[st]);
-                }
-                const bool go = c < NST || mbar_wait(&s.n_done, ph, p.status);
-                if constexpr (MODE == 1) {
-                    if (!go) break;
-                    mbar_arrive_expect(&s.full[st], (DK / 64 + 1) * PANEL);
-                }
-                if (go) {
-#pragma unroll
-                    for (int x = 0; x < DK / 64; ++x) tma_load_3d(q.K[x], &p.kmap, 64 * x, kh, tok, &s.full[st]);
-                }
-                if (!go || (MODE == 0 && c >= NST && !mbar_wait(&s.o_done, ph, p.status))) {
-                    ++c;  // part of this chunk's loads are in flight, the others will not come
+                for (int x = 0; x < DK / 64; ++x) tma_load_3d(q.K[x], &p.kmap, 64 * x, kh, tok, &s.full[st]);
+                if (MODE == 0 && c >= NST && !wait_for(&s.o_done, ph)) {
+                    ++c;  // K's copies are in flight, V's will not come
                     break;
                 }
                 tma_load_3d(q.V, &p.vmap, vb * NB, h, tok, &s.full[st]);
+                if constexpr (MODE == 0) {
+                    if (c > 0 && !wait_for(&s.x_done, (c - 1) & 1)) {
+                        ++c;
+                        break;
+                    }
+                    mbar_arrive_expect(&s.q_full, DK / 64 * PANEL);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) tma_load_3d(s.Q[x], &p.qmap, 64 * x, kh, tok, &s.q_full);
+                    nq = c + 1;
+                }
+                ++done;
             }
             // no copy may be in flight when the CTA ends (after a wait that gave up, a
             // stage that is not whole makes this one give up too: by then its copies are in)
-            for (int d = max(0, c - NST); d < c; ++d) mbar_wait(&s.full[d % NST], (d / NST) & 1, p.status);
+            for (int d = max(0, c - NST); d < c; ++d) wait_for(&s.full[d % NST], (d / NST) & 1);
+            if (nq) wait_for(&s.q_full, (nq - 1) & 1);
         }
     } else if (warp == kEpi + kState + 1) {
-        // ---- products ----------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t ID_A = tc5::idesc_bf16(128, 128, false, false);
-            constexpr uint32_t ID_X = tc5::idesc_bf16(128, NB, false, true);
-            constexpr uint32_t ID_N = tc5::idesc_bf16(128, NB, true, true);
-            const uint32_t sVt = smem_u32(s.Vt);
-            for (int c = 0; c < nc; ++c) {
-                const int st = c % NST;
-                const uint32_t sK = smem_u32(s.st[st].K), sV = smem_u32(s.st[st].V), sQ = smem_u32(s.st[st].Q);
-                const uint32_t ta = tm + TA + 128 * (c & 1);
-                if constexpr (MODE == 0) {
-                    // A(c) goes where P(c-2) was: chunk c-2's o_free came before X(c-1)
-                    if (!mbar_wait(&s.full[st], (c / NST) & 1, p.status)) break;
-                    tc5::fence_after();
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k) tc5::mma(ta, tc5::kmajor<CT>(sQ, k), tc5::kmajor<CT>(sK, k), ID_A, k > 0);
+        // ---- products: the warp stays together, one lane issues ----------------
+        constexpr uint32_t ID_A = tc5::idesc_bf16(128, 128, false, false);
+        constexpr uint32_t ID_X = tc5::idesc_bf16(128, NB, false, true);
+        constexpr uint32_t ID_N = tc5::idesc_bf16(128, 3 * NB, true, true);
+        // descriptors of step 0; a K step is 32 bytes along 64-channel rows (then the
+        // next panel), or 16 rows down a tile
+        constexpr uint64_t KROWS = (16 * 128) >> 4, KCOLS = 32 >> 4, KPANEL = PANEL >> 4;
+        const uint64_t dVt = tc5::mnmajor(smem_u32(s.Vt), 0, PANEL), dS = tc5::mnmajor(smem_u32(s.S), 0, PANEL);
+        const uint64_t dQ = tc5::kmajor<CT>(smem_u32(s.Q), 0);
+        for (int c = 0; c < nc; ++c) {
+            const int st = c % NST;
+            const uint64_t dK = tc5::kmajor<CT>(smem_u32(s.st[st].K), 0);
+            const uint64_t dKt = tc5::mnmajor(smem_u32(s.st[st].K), 0, PANEL), dV = tc5::mnmajor(smem_u32(s.st[st].V), 0, PANEL);
+            if constexpr (MODE == 0) {
+                // A(c) goes where A(c-1) was, which P(c-1) is made of: p_ready came before Y(c-1)
+                if (!warp_wait(&s.full[st], (c / NST) & 1)) break;
+                if (!warp_wait(&s.q_full, c & 1)) break;
+                tc5::fence_after();
+                if (elect_one()) {
+#pragma unroll 2
+                    for (int k = 0; k < DK / 16; ++k) {
+                        const uint64_t at = (k >> 2) * KPANEL + (k & 3) * KCOLS;
+                        tc5::mma(tm + TA, dQ + at, dK + at, ID_A, k > 0);
+                    }
                     tc5::commit(&s.a_done);
-                    if (!mbar_wait(&s.s_ready, c & 1, p.status)) break;
-                    if (c > 0 && !mbar_wait(&s.o_free, (c - 1) & 1, p.status)) break;
-                    tc5::fence_after();
-#pragma unroll
+                }
+                __syncwarp();
+                if (!warp_wait(&s.s_ready, c & 1)) break;
+                if (c > 0 && !warp_wait(&s.o_free, (c - 1) & 1)) break;
+                tc5::fence_after();
+                if (elect_one()) {
+#pragma unroll 2
                     for (int k = 0; k < DK / 16; ++k)
-                        tc5::mma(tm + TX, tc5::kmajor<CT>(sQ, k), tc5::mnmajor(sVt + 2 * PANEL, k, PANEL), ID_X, k > 0);
+                        tc5::mma(tm + TX, dQ + (k >> 2) * KPANEL + (k & 3) * KCOLS, dS + k * KROWS, ID_X, k > 0);
                     tc5::commit(&s.x_done);
                 }
-                // N(c); with 64 key channels lanes 64-127 read the V tile behind K and are ignored
-                if (!mbar_wait(&s.vt_ready, c & 1, p.status)) break;
-                tc5::fence_after();
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int k = 0; k < CT / 16; ++k)
-                        tc5::mma(tm + TN, tc5::mnmajor(sK, k, PANEL), tc5::mnmajor(sVt + t * PANEL, k, PANEL), ID_N, t + k > 0);
-                if (!mbar_wait(&s.vt2_ready, c & 1, p.status)) break;
-                tc5::fence_after();
-#pragma unroll
-                for (int k = 0; k < CT / 16; ++k)
-                    tc5::mma(tm + TN, tc5::mnmajor(sK, k, PANEL), tc5::mnmajor(sVt + 2 * PANEL, k, PANEL), ID_N, true);
+                __syncwarp();
+            }
+            // N(c); with 64 key channels lanes 64-127 read the V tile behind K and are ignored
+            if (!warp_wait(&s.vt_ready, c & 1)) break;
+            tc5::fence_after();
+            if (elect_one()) {
+#pragma unroll 2
+                for (int k = 0; k < CT / 16; ++k) tc5::mma(tm + TN, dKt + k * KROWS, dVt + k * KROWS, ID_N, k > 0);
                 tc5::commit(&s.n_done);
-                if constexpr (MODE == 0) {
-                    if (!mbar_wait(&s.p_ready, c & 1, p.status)) break;
-                    tc5::fence_after();
-#pragma unroll
-                    for (int k = 0; k < CT / 16; ++k)
-                        tc5::mma_ts(tm + TY, ta + 8 * k, tc5::mnmajor(sV, k, PANEL), ID_X, k > 0);
+            }
+            __syncwarp();
+            if constexpr (MODE == 0) {
+                if (!warp_wait(&s.p_ready, c & 1)) break;
+                tc5::fence_after();
+                if (elect_one()) {
+#pragma unroll 2
+                    for (int k = 0; k < CT / 16; ++k) tc5::mma_ts(tm + TY, tm + TP + 8 * k, dV + k * KROWS, ID_X, k > 0);
                     tc5::commit(&s.o_done);
                 }
+                __syncwarp();
             }
-            tc5::commit(&s.drain);  // no product may be in flight when the CTA ends
-            mbar_wait(&s.drain, 0, p.status);
+            ++done;
         }
+        if (elect_one()) tc5::commit(&s.drain);  // no product may be in flight when the CTA ends
+        warp_wait(&s.drain, 0);
     } else {
-        // ---- gates: the next chunk's values are loaded before this one's are needed ----
-        float x[4], y[4];
+        // ---- gates: the next chunk's values are on their way while this one's wait ----
+        float x[4];
         const float* g = p.g + (size_t)(tok0 + (long long)c0 * CT) * p.H + h;
         if (nc > 0) load_gates(x, g, p.H, min(CT, n - c0 * CT));
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST;
-            if (c + 1 < nc) load_gates(y, g + (size_t)(c + 1) * CT * p.H, p.H, min(CT, n - (c0 + c + 1) * CT));
-            if (c >= NST && !warp_wait(&s.gfree[st], ((c / NST) - 1) & 1, p.status)) break;
-            form_gates(s.gate[st], x, min(CT, n - (c0 + c) * CT), p.scale, MODE == 0);
+            if (c >= NST && !warp_wait(&s.gfree[st], ((c / NST) - 1) & 1)) break;
+            form_gates(s.gate[st], x);
             mbar_arrive(&s.gfull[st]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = y[j];
+            if (c + 1 < nc) load_gates(x, g + (size_t)(c + 1) * CT * p.H, p.H, min(CT, n - (c0 + c + 1) * CT));
+            ++done;
         }
     }
+    if (lane == 0 && done < nc && (MODE == 0 || warp >= kEpi)) atomicOr(p.status, 1u);
     tc5::fence_before();
     __syncthreads();
     if (warp == kEpi + kState + 1) {
