@@ -12,7 +12,10 @@
 
 #include "checks.h"
 #include "common.cuh"
+#include "decay_tc.cuh"
 #include "mma.cuh"
+#include "tc5.cuh"
+#include "tma.cuh"
 
 namespace gdn {
 namespace {
@@ -45,58 +48,621 @@ GDN_DEV int parent_of(const int* parent, int i, unsigned int* status) {
     return p;
 }
 
-// One warp per (sequence, node, query head); a lane holds D / 32 channels.
+// ---- attention -----------------------------------------------------------------
+// A unit is a (sequence, key head, 128 rows): the rows are the nodes' query heads of
+// that key head, row = node * group + head in group.  Its keys come in tiles of
+// 128, the cached ones first, the nodes themselves as the last.  Every key tile
+// of every unit is one step of work, and the steps of the whole call, in order, are
+// cut evenly over one CTA per SM, so that sequences of any lengths fill the
+// device.  A CTA whose share starts or ends within a unit leaves a partial result
+// (maximum, sum, weighted sum) for a second kernel.
+//
+// Per tile:  S = Q K^T (tcgen05, 128 x 128 x d, lane = row),  P = e^{S - m} as a
+// bf16 A operand over S in tensor memory,  O += P V.  Two groups of four softmax
+// warps take the tiles in turn, each with its own m, l and O, so that one group's
+// products run under the other's exponentials; they are joined at the segment's
+// end.  O is rescaled only when the maximum grew by more than 2^8: until then
+// the weights, and their sums, are just that much larger.  Keys and values arrive
+// by TMA, page by page, through a three-stage ring.
+// What bounds it is the HBM read of the cached keys and values.
+constexpr int KT = 128;              // keys per tile
+constexpr int PANEL = KT * 128;      // bytes of a 128-row, 64-channel tile
+constexpr int NST = 3;
+constexpr int kSoft = 8;             // softmax warps, two groups
+constexpr int kThreads = 32 * (kSoft + 2);
+
 template <int D>
-__global__ void __launch_bounds__(128)
-tree_attn_kernel(int N, int M, int Hq, int Hkv, float scale, int window, const int* __restrict__ parent,
-                 const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
-                 const __nv_bfloat16* __restrict__ v, Cache c, __nv_bfloat16* __restrict__ o,
-                 unsigned int* status) {
-    constexpr int E = D / 32;
-    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (w >= (long long)N * M * Hq) return;
-    const int lane = threadIdx.x & 31;
-    const int h = (int)(w % Hq), i = (int)(w / Hq % M), n = (int)(w / Hq / M), kh = h / (Hq / Hkv);
-    float qr[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qr[e] = scale * __bfloat162float(q[(size_t)w * D + lane * E + e]);
-        acc[e] = 0.f;
-    }
-    auto take = [&](const __nv_bfloat16* kr, const __nv_bfloat16* vr) {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += qr[e] * __bfloat162float(kr[lane * E + e]);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s);
-        const float a = m == -INFINITY ? 0.f : expf(m - mn), p = expf(s - mn);
-        l = a * l + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = a * acc[e] + p * __bfloat162float(vr[lane * E + e]);
-        m = mn;
-    };
-    const int* par = parent + (size_t)n * M;
-    int depth = 0;
-    for (int j = parent_of(par, i, status); j >= 0; j = parent_of(par, j, status)) ++depth;
-    const int len = cached(c, n, status);
-    const long long far = window > 0 ? (long long)len + depth - window + 1 : 0;
-    for (int p = far > 0 ? (int)min(far, (long long)len) : 0; p < len; ++p) {
-        const int pg = c.table[(size_t)n * c.width + p / c.page];
-        if (pg < 0 || pg >= c.pages) {
-            if (status) atomicOr(status, 2u);
-            continue;
+struct alignas(1024) Smem {
+    unsigned char Q[D / 64][PANEL];  // at a segment's end: maxima and sums of the groups
+    unsigned char K[NST][D / 64][PANEL], V[NST][D / 64][PANEL];
+    int parent[kMaxNodes];
+    // 16-row pieces of a step's tile that hold cached rows; twice the stages, as the
+    // loader may be that far ahead of the softmax warps
+    uint32_t have[2 * NST];
+    uint64_t k_full[NST], v_full[NST], k_free[NST], v_free[NST], s_ready[2], p_ready[2], o_done[2], q_ready, seg_done, meet, drain;
+    long long warp_sum[kSoft + 2];
+    int n0;
+    long long before, total;
+    uint32_t tmem;
+};
+
+struct Params {
+    CUtensorMap kmap, vmap, knode, vnode;
+    Cache c;
+    int N, M, Hq, Hkv, group, row_tiles, window;
+    float scale;
+    const int* parent;
+    const __nv_bfloat16* q;
+    __nv_bfloat16* o;
+    float* part;                     // [CTA][2][rows][D + 2]: sum, then m and l
+    int part_rows;
+    unsigned int* status;
+};
+
+// The steps of sequence n: its first key tile that any node sees, the tiles from
+// there, and the one of the nodes.
+struct Span {
+    int len, first, steps;
+};
+GDN_DEV Span span_of(const Params& p, int n) {
+    Span s;
+    s.len = cached(p.c, n, p.status);
+    const int lo = p.window > 0 ? max(0, s.len - p.window + 1) : 0;
+    s.first = lo / KT;
+    s.steps = (s.len + KT - 1) / KT - s.first + 1;
+    return s;
+}
+
+// A CTA's share of one unit: steps t0 .. t1 - 1 of its `span.steps`.
+struct Segment {
+    int n, kh, rt, t0, t1;
+    Span span;
+};
+
+// Walks the segments of a CTA's share [at, end) of all steps.
+struct Walk {
+    long long at, end, base;  // base: steps before sequence n
+    int n;
+    Span span;
+    GDN_DEV bool next(const Params& p, Segment& g) {
+        if (at >= end) return false;
+        const int units = p.Hkv * p.row_tiles;
+        while (at >= base + (long long)span.steps * units) {
+            base += (long long)span.steps * units;
+            span = span_of(p, ++n);
         }
-        const size_t at = (((size_t)pg * c.page + p % c.page) * Hkv + kh) * D;
-        take(c.k + at, c.v + at);
+        const int u = (int)((at - base) / span.steps);
+        g.n = n;
+        g.kh = u / p.row_tiles;
+        g.rt = u % p.row_tiles;
+        g.span = span;
+        g.t0 = (int)((at - base) % span.steps);
+        g.t1 = (int)min((long long)span.steps, g.t0 + (end - at));
+        at += g.t1 - g.t0;
+        return true;
     }
-    int back = 0;
-    for (int j = i; j >= 0; j = parent_of(par, j, status), ++back) {
-        if (window > 0 && back >= window) break;
-        const size_t at = (((size_t)n * M + j) * Hkv + kh) * D;
-        take(k + at, v + at);
+};
+
+// The shares of a call of `total` steps: at least two steps each.
+GDN_DEV long long shares(long long total, int ctas) { return min((long long)ctas, (total + 1) / 2); }
+GDN_DEV long long share_start(long long total, long long parts, long long b) { return total * b / parts; }
+
+// All threads: total steps, and the sequence that holds step `at` with the steps
+// before it (s.n0, s.before).  Every thread sums a run of sequences.
+template <class S>
+GDN_DEV void locate(S& s, const Params& p, long long (*at_of)(long long, int, int), int b, int ctas) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.N + kThreads - 1) / kThreads, a = min(p.N, tid * per), e = min(p.N, a + per);
+    const int units = p.Hkv * p.row_tiles;
+    long long mine = 0;
+    for (int n = a; n < e; ++n) mine += span_of(p, n).steps;
+    long long run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+    }
+    if (lane == 31) s.warp_sum[warp] = run;
+    __syncthreads();
+    long long before = run - mine, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s.warp_sum[w];
+        all += s.warp_sum[w];
+    }
+    all *= units;
+    before *= units;
+    const long long at = at_of(all, b, ctas);
+    if (at >= before && at < before + mine * units) {
+        int n = a;
+        for (;; ++n) {
+            const long long st = (long long)span_of(p, n).steps * units;
+            if (at < before + st) break;
+            before += st;
+        }
+        s.n0 = n;
+        s.before = before;
+    }
+    if (tid == 0) s.total = all;
+    __syncthreads();
+}
+GDN_DEV long long cta_start(long long total, int b, int ctas) { return share_start(total, shares(total, ctas), b); }
+
+GDN_DEV unsigned char* align1k(unsigned char* p) {
+    return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+using decay::elect_one;
+using decay::ex2;
+using decay::wait_for;
+using decay::warp_wait;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attn_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) unsigned char raw[];
+    Smem<D>& s = *reinterpret_cast<Smem<D>*>(align1k(raw));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = gridDim.x, b = blockIdx.x;
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.k_free[i], 1);
+            mbar_init(&s.v_free[i], 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&s.s_ready[g], 1);
+            mbar_init(&s.p_ready[g], kSoft / 2);
+            mbar_init(&s.o_done[g], 1);
+        }
+        mbar_init(&s.q_ready, kSoft);
+        mbar_init(&s.seg_done, kSoft);
+        mbar_init(&s.meet, kSoft);
+        mbar_init(&s.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == kSoft + 1) tc5::alloc(&s.tmem, 512);
+    locate(s, p, [](long long total, int i, int n) { return cta_start(total, i, n); }, b, ctas);
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    const uint32_t tm = __shfl_sync(0xffffffffu, s.tmem, 0);
+    const long long parts = shares(s.total, ctas);
+    Walk w{share_start(s.total, parts, b), b < parts ? share_start(s.total, parts, b + 1) : 0, s.before, s.n0, {}};
+    if (b < parts) w.span = span_of(p, w.n);
+    else w.end = w.at;
+    // tensor-memory columns of a group: S (P over it, as bf16 pairs), O
+    constexpr uint32_t TG = 256, TO = 128;
+    int x = 0;      // steps so far: the group and the phases of its barriers follow from it
+    int segs = 0;
+    bool ok = true;
+    Segment g;
+    if (warp < kSoft) {
+        const int grp = warp >> 2, r = 32 * (warp & 3) + lane;
+        const uint32_t tg = tm + ((uint32_t)(32 * (warp & 3)) << 16) + TG * grp;
+        const float sc = p.scale == 0.f ? 1.4426950408889634f : fabsf(p.scale) * 1.4426950408889634f;
+        const int R = p.M * p.group;
+        int met = 0;
+        auto meet = [&]() {  // the softmax warps come together (within the bounds of a wait)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.meet);
+            return ok = warp_wait(&s.meet, met++ & 1);
+        };
+        while (ok && w.next(p, g)) {
+            const int row = g.rt * 128 + r, node = row / p.group, head = g.kh * p.group + row % p.group;
+            const bool live = row < R;
+            const bool busy = g.rt * 128 + 32 * (warp & 3) < R;  // this warp has rows
+            // Q of the unit (its sign with the scale's; zero for a zero scale and past the rows)
+            const size_t qrow = (((size_t)g.n * p.M + (live ? node : 0)) * p.Hq + (live ? head : 0)) * D;
+            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u, keep = p.scale == 0.f || !live ? 0u : 0xffffffffu;
+#pragma unroll 1
+            for (int j = 0; j < D / 16; ++j) {
+                const int ch = grp * (D / 16) + j;  // 16-byte piece of the row
+                uint4 v = *reinterpret_cast<const uint4*>(p.q + qrow + 8 * ch);
+                v = make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep);
+                *reinterpret_cast<uint4*>(s.Q[ch >> 3] + 2 * swz<64>(r, 8 * (ch & 7))) = v;
+            }
+            if (tid < p.M) s.parent[tid] = parent_of(p.parent + (size_t)g.n * p.M, tid, p.status);
+            fence_async_smem();
+            tc5::fence_before();
+            if (!meet()) break;
+            if (lane == 0) mbar_arrive(&s.q_ready);
+            // what this row sees: cached positions from `lo`, nodes in `anc`
+            unsigned long long anc = 0;
+            int depth = 0;
+            if (live) {
+                for (int j = node, back = 0; j >= 0; j = s.parent[j], ++back) {
+                    if (p.window == 0 || back < p.window) anc |= 1ull << j;
+                    depth = back;
+                }
+            }
+            const long long far = p.window > 0 ? (long long)g.span.len + depth - p.window + 1 : 0;
+            const int lo = far > 0 ? (int)min(far, (long long)g.span.len) : 0;
+            float m = -INFINITY, l = 0.f;
+            bool any = false;  // this group had a step in this segment
+            for (int t = g.t0; t < g.t1; ++t, ++x) {
+                if ((x & 1) != grp) continue;
+                const int st = x % NST, ph = (x >> 1) & 1;
+                const bool tree = t == g.span.steps - 1;
+                const int key0 = (g.span.first + t) * KT;
+                if (!(ok = warp_wait(&s.s_ready[grp], ph))) break;
+                tc5::fence_after();
+                uint32_t have = 0xff;
+                if (!tree) {
+                    // the loader wrote `have` before it armed k_full, which the product waited for
+                    have = s.have[x % (2 * NST)];
+                }
+                const bool partly = tree || have != 0xff || key0 + KT > g.span.len ||
+                                    (p.window > 0 && key0 < g.span.len + p.M - p.window);
+                if (partly) {
+                    if (busy) {  // scores that this row does not see become -inf
+#pragma unroll 1
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t seen;
+                            if (tree) {
+                                seen = j < 4 ? (uint32_t)(anc >> (16 * j)) & 0xffffu : 0u;
+                            } else {
+                                const int k0 = key0 + 16 * j, a = max(lo - k0, 0), e = min(g.span.len - k0, 16);
+                                seen = e > 0 && a < 16 && (have >> j & 1) ? ((1u << e) - 1u) & ~((1u << a) - 1u) : 0u;
+                            }
+                            float v[16];
+                            uint32_t u[16];
+                            tc5::ld16(v, tg + 16 * j);
+                            tc5::wait_ld();
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) u[q] = (seen >> q) & 1 ? __float_as_uint(v[q]) : 0xff800000u;
+                            tc5::st16(tg + 16 * j, u);
+                        }
+                        tc5::wait_st();
+                    }
+                    // and values that no row sees become zero: whatever the places hold, a
+                    // zero weight times it must be zero
+                    if (!(ok = warp_wait(&s.v_full[st], (x / NST) & 1))) break;
+                    const bool dead = tree ? r >= p.M
+                                           : key0 + r >= g.span.len || !(have >> (r >> 4) & 1) ||
+                                                 (p.window > 0 && key0 + r <= g.span.len - p.window);
+                    if (dead) {
+#pragma unroll 1
+                        for (int j = 0; j < D / 8; ++j)
+                            *reinterpret_cast<uint4*>(s.V[st][j >> 3] + 2 * swz<64>(r, 8 * (j & 7))) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                }
+                if (busy) {
+                    float mt = -INFINITY;
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        float v[32];
+                        tc5::ld32(v, tg + 32 * j);
+                        tc5::wait_ld();
+                        float a = v[0], c = v[1];
+#pragma unroll
+                        for (int q = 2; q < 32; q += 2) {
+                            a = fmaxf(a, v[q]);
+                            c = fmaxf(c, v[q + 1]);
+                        }
+                        mt = fmaxf(mt, fmaxf(a, c));
+                    }
+                    mt *= sc;
+                    const bool grow = mt > m + 8.f;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float mn = grow ? mt : m;
+                        const float f = grow ? ex2(m - mn) : 1.f;
+                        l *= f;
+                        m = mn;
+                        if (any) {
+                            // O of the last step of this group must be in
+                            if (!(ok = warp_wait(&s.o_done[grp], ph ^ 1))) break;
+                            tc5::fence_after();
+#pragma unroll 1
+                            for (int j = 0; j < D / 16; ++j) {
+                                float v[16];
+                                uint32_t u[16];
+                                tc5::ld16(v, tg + TO + 16 * j);
+                                tc5::wait_ld();
+#pragma unroll
+                                for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(f * v[q]);
+                                tc5::st16(tg + TO + 16 * j, u);
+                            }
+                            tc5::wait_st();
+                        }
+                    }
+                    const float off = m == -INFINITY ? 0.f : -m;
+                    float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        float v[32];
+                        uint32_t u[16];
+                        tc5::ld32(v, tg + 32 * j);
+                        tc5::wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float a = ex2(fmaf(v[2 * q], sc, off)), c = ex2(fmaf(v[2 * q + 1], sc, off));
+                            l0 += a;
+                            l1 += c;
+                            u[q] = pack_bf16(a, c);
+                        }
+                        tc5::st16(tg + 16 * j, u);
+                    }
+                    l += l0 + l1;
+                    tc5::wait_st();
+                }
+                any = true;
+                tc5::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_ready[grp]);
+            }
+            if (!ok) break;
+            // ---- the segment's result: both groups' O, each group half of the channels ----
+            // (x is now past the segment; the last step of each group is the one of its parity)
+            for (int q = 0; q < 2 && ok; ++q) {
+                const int y = x - 1 - ((x - 1 - q) & 1);  // the last step of group q so far
+                if (y >= x - (g.t1 - g.t0)) ok = warp_wait(&s.o_done[q], (y >> 1) & 1);
+            }
+            if (!ok) break;
+            tc5::fence_after();
+            float* ml = reinterpret_cast<float*>(s.Q[0]);  // every product of this Q is done
+            ml[grp * 256 + r] = m;
+            ml[grp * 256 + 128 + r] = any ? l : 0.f;
+            if (!meet()) break;
+            const float m0 = ml[r], l0 = ml[128 + r], m1 = ml[256 + r], l1 = ml[384 + r];
+            const float mx = fmaxf(m0, m1);
+            const float f0 = l0 > 0.f ? ex2(m0 - mx) : 0.f, f1 = l1 > 0.f ? ex2(m1 - mx) : 0.f;
+            const float lt = l0 * f0 + l1 * f1;
+            const bool whole = g.t0 == 0 && g.t1 == g.span.steps;
+            if (busy) {
+                const float inv = whole ? 1.f / lt : 1.f;
+                // a CTA that starts within the unit leaves its part in place 0, else in 1
+                float* part = p.part + (((size_t)b * 2 + (g.t0 > 0 ? 0 : 1)) * p.part_rows + r) * (D + 2);
+                __nv_bfloat16* out = p.o + qrow;
+                const uint32_t t0 = tg - TG * grp + TO, t1 = t0 + TG;
+#pragma unroll 1
+                for (int j = 0; j < D / 32; ++j) {
+                    const int c0 = grp * (D / 2) + 16 * j;
+                    float u[16], v[16];
+                    tc5::ld16(u, t0 + c0);
+                    tc5::ld16(v, t1 + c0);
+                    tc5::wait_ld();
+                    // a group without a step has nothing in its O
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) u[q] = ((f0 > 0.f ? f0 * u[q] : 0.f) + (f1 > 0.f ? f1 * v[q] : 0.f)) * inv;
+                    if (!live) continue;
+                    if (whole) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) h[q] = pack_bf16(u[2 * q], u[2 * q + 1]);
+                        *reinterpret_cast<uint4*>(out + c0) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(out + c0 + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<float2*>(part + c0 + 2 * q) = make_float2(u[2 * q], u[2 * q + 1]);
+                    }
+                }
+                if (!whole && live && grp == 0) *reinterpret_cast<float2*>(part + D) = make_float2(mx, lt);
+            }
+            tc5::fence_before();
+            if (!meet()) break;  // before the next Q goes over the sums
+            if (lane == 0) mbar_arrive(&s.seg_done);
+            ++segs;
+        }
+    } else if (warp == kSoft) {
+        // ---- loads: a lane per page -------------------------------------------------
+        const int pages = KT / p.c.page;
+        while (ok && w.next(p, g)) {
+            for (int t = g.t0; t < g.t1; ++t, ++x) {
+                const int st = x % NST, use = x / NST;
+                if (t == g.span.steps - 1) {  // the nodes
+                    if (use > 0 && !(ok = warp_wait(&s.k_free[st], (use - 1) & 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect(&s.k_full[st], D / 64 * PANEL / 2);
+#pragma unroll
+                        for (int y = 0; y < D / 64; ++y) tma_load_3d(s.K[st][y], &p.knode, 64 * y, g.kh, g.n * p.M, &s.k_full[st]);
+                    }
+                    if (use > 0 && !(ok = warp_wait(&s.v_free[st], (use - 1) & 1))) { ++x; break; }
+                    if (lane == 0) {
+                        mbar_arrive_expect(&s.v_full[st], D / 64 * PANEL / 2);
+#pragma unroll
+                        for (int y = 0; y < D / 64; ++y) tma_load_3d(s.V[st][y], &p.vnode, 64 * y, g.kh, g.n * p.M, &s.v_full[st]);
+                    }
+                    continue;
+                }
+                const int pos = (g.span.first + t) * KT + lane * p.c.page;
+                int pg = -1;
+                if (lane < pages && pos < g.span.len) {
+                    pg = p.c.table[(size_t)g.n * p.c.width + pos / p.c.page];
+                    if (pg < 0 || pg >= p.c.pages) {
+                        atomicOr(p.status, 2u);
+                        pg = -1;
+                    }
+                }
+                const uint32_t got = __ballot_sync(0xffffffffu, pg >= 0);
+                const uint32_t bytes = (uint32_t)__popc(got) * p.c.page * D * 2;
+                const int at = lane * p.c.page * 128;
+                if (use > 0 && !(ok = warp_wait(&s.k_free[st], (use - 1) & 1))) break;
+                if (lane == 0) {
+                    uint32_t have = 0;
+                    for (int i = 0; i < pages; ++i)
+                        if (got >> i & 1) have |= ((1u << (p.c.page / 16)) - 1u) << (i * (p.c.page / 16));
+                    s.have[x % (2 * NST)] = have;
+                    mbar_arrive_expect(&s.k_full[st], bytes);
+                }
+                __syncwarp();
+                if (pg >= 0) {
+#pragma unroll
+                    for (int y = 0; y < D / 64; ++y) tma_load_3d(s.K[st][y] + at, &p.kmap, 64 * y, g.kh, pg * p.c.page, &s.k_full[st]);
+                }
+                __syncwarp();
+                if (use > 0 && !(ok = warp_wait(&s.v_free[st], (use - 1) & 1))) { ++x; break; }
+                if (lane == 0) mbar_arrive_expect(&s.v_full[st], bytes);
+                __syncwarp();
+                if (pg >= 0) {
+#pragma unroll
+                    for (int y = 0; y < D / 64; ++y) tma_load_3d(s.V[st][y] + at, &p.vmap, 64 * y, g.kh, pg * p.c.page, &s.v_full[st]);
+                }
+                __syncwarp();
+            }
+        }
+        // no copy may be in flight when the CTA ends (a stage that a wait gave up on makes this
+        // one give up as well: its copies are in by then)
+        for (int y = max(0, x - NST); y < x; ++y) {
+            warp_wait(&s.k_full[y % NST], (y / NST) & 1);
+            warp_wait(&s.v_full[y % NST], (y / NST) & 1);
+        }
+    } else {
+        // ---- products: S of step x, then O of the step before -------------------------
+        constexpr uint32_t ID_S = tc5::idesc_bf16(128, KT, false, false), ID_O = tc5::idesc_bf16(128, D, false, true);
+        constexpr uint64_t KROWS = (16 * 128) >> 4, KCOLS = 32 >> 4, KPANEL = PANEL >> 4;
+        const uint64_t dQ = tc5::kmajor<KT>(smem_u32(s.Q), 0);
+        while (ok && w.next(p, g)) {
+            if (segs > 0 && !(ok = warp_wait(&s.seg_done, (segs - 1) & 1))) break;
+            if (!(ok = warp_wait(&s.q_ready, segs & 1))) break;
+            const int x0 = x, x1 = x + (g.t1 - g.t0);
+            for (; x <= x1; ++x) {
+                if (x < x1) {
+                    const int st = x % NST;
+                    // S goes where P of two steps before was: its product must be done with it
+                    if (x >= 2 && !(ok = warp_wait(&s.o_done[x & 1], ((x >> 1) & 1) ^ 1))) break;
+                    if (!(ok = warp_wait(&s.k_full[st], (x / NST) & 1))) break;
+                    tc5::fence_after();
+                    if (elect_one()) {
+                        const uint64_t dK = tc5::kmajor<KT>(smem_u32(s.K[st]), 0);
+#pragma unroll 2
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t at = (k >> 2) * KPANEL + (k & 3) * KCOLS;
+                            tc5::mma(tm + TG * (x & 1), dQ + at, dK + at, ID_S, k > 0);
+                        }
+                        tc5::commit(&s.s_ready[x & 1]);
+                        tc5::commit(&s.k_free[st]);
+                    }
+                    __syncwarp();
+                }
+                if (x > x0) {
+                    const int y = x - 1, st = y % NST;
+                    if (!(ok = warp_wait(&s.v_full[st], (y / NST) & 1))) break;
+                    if (!(ok = warp_wait(&s.p_ready[y & 1], (y >> 1) & 1))) break;
+                    tc5::fence_after();
+                    if (elect_one()) {
+                        const uint64_t dV = tc5::mnmajor(smem_u32(s.V[st]), 0, PANEL);
+                        const uint32_t tp = tm + TG * (y & 1);
+#pragma unroll 2
+                        for (int k = 0; k < KT / 16; ++k)
+                            tc5::mma_ts(tp + TO, tp + 8 * k, dV + k * KROWS, ID_O, k > 0 || y - x0 >= 2);
+                        tc5::commit(&s.o_done[y & 1]);
+                        tc5::commit(&s.v_free[st]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) break;
+            x = x1;
+            ++segs;
+        }
+        if (elect_one()) tc5::commit(&s.drain);  // no product may be in flight when the CTA ends
+        warp_wait(&s.drain, 0);
+    }
+    if (!ok && lane == 0) atomicOr(p.status, 1u);
+    tc5::fence_before();
+    __syncthreads();
+    if (warp == kSoft + 1) {
+        tc5::fence_after();
+        tc5::dealloc(tm, 512);
+    }
+}
+
+// Units that more than one CTA worked on: their parts, joined in order.  A CTA per
+// unit and 16 rows, a warp per row.
+constexpr int JT = 256, JR = 16;
+template <int D>
+__global__ void __launch_bounds__(JT)
+tree_attn_join_kernel(const __grid_constant__ Params p, int ctas) {
+    const int u = blockIdx.x, units = p.Hkv * p.row_tiles, n = u / units;
+    // steps before sequence n: summed as in the first kernel
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long before = 0, all = 0;
+    for (int i = tid; i < p.N; i += JT) {
+        const int st = span_of(p, i).steps;
+        all += st;
+        if (i < n) before += st;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[(size_t)w * D + lane * E + e] = __float2bfloat16_rn(acc[e] / l);
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    __shared__ long long part_all[JT / 32], part_before[JT / 32];
+    if (lane == 0) {
+        part_all[warp] = all;
+        part_before[warp] = before;
+    }
+    __syncthreads();
+    all = before = 0;
+    for (int i = 0; i < JT / 32; ++i) {
+        all += part_all[i];
+        before += part_before[i];
+    }
+    const long long total = all * units, parts = shares(total, ctas);
+    const int steps = span_of(p, n).steps;
+    const long long u0 = before * units + (long long)(u % units) * steps, u1 = u0 + steps;
+    // the CTAs that hold its first and last step
+    auto owner = [&](long long at) {
+        long long b = at * parts / total;
+        while (share_start(total, parts, b + 1) <= at) ++b;
+        while (share_start(total, parts, b) > at) --b;
+        return (int)b;
+    };
+    const int b0 = owner(u0), b1 = owner(u1 - 1);
+    if (b0 == b1) return;  // one CTA had all of it and wrote the result
+    const int kh = (u % units) / p.row_tiles, rt = u % p.row_tiles, R = p.M * p.group;
+    for (int r = blockIdx.y * JR + warp; r < (blockIdx.y + 1) * JR && rt * 128 + r < R; r += JT / 32) {
+        auto part_of = [&](int b) {
+            return p.part + (((size_t)b * 2 + (share_start(total, parts, b) > u0 ? 0 : 1)) * p.part_rows + r) * (D + 2);
+        };
+        float m = -INFINITY;
+        for (int b = b0; b <= b1; ++b) m = fmaxf(m, part_of(b)[D]);
+        float l = 0.f, acc[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+        for (int b = b0; b <= b1; ++b) {
+            const float* q = part_of(b);
+            const float f = q[D + 1] > 0.f ? ex2(q[D] - m) : 0.f;
+            l += f * q[D + 1];
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+                const float2 v = *reinterpret_cast<const float2*>(q + 64 * e + 2 * lane);
+                acc[2 * e] += f * v.x;
+                acc[2 * e + 1] += f * v.y;
+            }
+        }
+        const int row = rt * 128 + r, node = row / p.group, head = kh * p.group + row % p.group;
+        __nv_bfloat16* out = p.o + (((size_t)n * p.M + node) * p.Hq + head) * D;
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e)
+            *reinterpret_cast<uint32_t*>(out + 64 * e + 2 * lane) = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    }
+}
+
+constexpr int kCtas = 148;  // one per SM
+
+size_t part_bytes(int M, int group, int d) {
+    const int rows = M * group < 128 ? M * group : 128;
+    return (size_t)kCtas * 2 * rows * (d + 2) * 4;
+}
+
+template <int D>
+bool launch_attn(Params& a, const void* k, const void* v, cudaStream_t st) {
+    const int box = a.c.page;
+    if (!encode_head_map(&a.kmap, a.c.k, (long long)a.c.pages * a.c.page, a.Hkv, D, box) ||
+        !encode_head_map(&a.vmap, a.c.v, (long long)a.c.pages * a.c.page, a.Hkv, D, box) ||
+        !encode_head_map(&a.knode, k, (long long)a.N * a.M, a.Hkv, D, KT / 2) ||
+        !encode_head_map(&a.vnode, v, (long long)a.N * a.M, a.Hkv, D, KT / 2))
+        return false;
+    const int smem = sizeof(Smem<D>) + 1024;
+    cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    GDN_LAUNCH("tree_attn", st, (tree_attn_kernel<D><<<kCtas, kThreads, smem, st>>>(a)));
+    GDN_LAUNCH("tree_attn_join", st, (tree_attn_join_kernel<D><<<dim3((unsigned)(a.N * a.Hkv * a.row_tiles), (a.part_rows + JR - 1) / JR), JT, 0, st>>>(a, kCtas)));
+    return true;
 }
 
 // ---- append ------------------------------------------------------------------
@@ -168,7 +734,7 @@ extern "C" {
 
 size_t gdn_tree_attn_workspace(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, int page, int width) {
     if (check(N, M, Hq, Hkv, d, dtype, 1, page, width) != GDN_OK) return 0;
-    return kStatusBytes;
+    return kStatusBytes + part_bytes(M, Hq / Hkv, d);
 }
 
 gdn_status gdn_tree_attn(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, float scale, int window,
@@ -193,14 +759,17 @@ gdn_status gdn_tree_attn(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, 
     cudaGetLastError();
     if (cudaMemsetAsync(ws, 0, sizeof(unsigned int), st) != cudaSuccess) return GDN_ERR_CUDA;
     const Cache c{(const __nv_bfloat16*)k_cache, (const __nv_bfloat16*)v_cache, block_table, cache_len, pages, page, width};
-    const unsigned grid = (unsigned)(((long long)N * M * Hq + 3) / 4);
-    auto go = [&](auto dd) {
-        GDN_LAUNCH("tree_attn", st, (tree_attn_kernel<decltype(dd)::value><<<grid, 128, 0, st>>>(
-            N, M, Hq, Hkv, scale, window, parent, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k,
-            (const __nv_bfloat16*)v, c, (__nv_bfloat16*)o, (unsigned int*)ws)));
-    };
-    if (d == 64) go(std::integral_constant<int, 64>{});
-    else go(std::integral_constant<int, 128>{});
+    Params a{};
+    a.c = c;
+    a.N = N; a.M = M; a.Hq = Hq; a.Hkv = Hkv; a.group = Hq / Hkv;
+    a.row_tiles = (M * a.group + 127) / 128;
+    a.window = window; a.scale = scale; a.parent = parent;
+    a.q = (const __nv_bfloat16*)q; a.o = (__nv_bfloat16*)o;
+    a.part = (float*)((char*)ws + kStatusBytes);
+    a.part_rows = M * a.group < 128 ? M * a.group : 128;
+    a.status = (unsigned int*)ws;
+    const bool fine = d == 64 ? launch_attn<64>(a, k, v, st) : launch_attn<128>(a, k, v, st);
+    if (!fine) return GDN_ERR_CUDA;
     return launched();
 }
 
