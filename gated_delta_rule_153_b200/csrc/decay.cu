@@ -376,11 +376,8 @@ void run_bwd(const Problem& p, const void* q, const void* k, const void* v, cons
         p.seq, p.H, row_blocks(p.dk, p.dv), g, (const float*)(base + l.dotq), (const float*)(base + l.dotk),
         (const float*)(base + l.cross), dg)));
     if (rep > 1) {
-        const unsigned y = spread(p, ((long long)(p.seq.cu ? p.seq.rows : p.seq.len) * p.Hk * p.dk) / 1024 + 1);
-        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<T><<<dim3((unsigned)p.seq.nseq, y), 256, 0, st>>>(
-            p.seq, p.Hk, rep, p.dk, (const float*)(base + l.dq), (T*)dq)));
-        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<T><<<dim3((unsigned)p.seq.nseq, y), 256, 0, st>>>(
-            p.seq, p.Hk, rep, p.dk, (const float*)(base + l.dk), (T*)dk)));
+        launch_group_sum(p, p.dk, (const float*)(base + l.dq), dq, st);
+        launch_group_sum(p, p.dk, (const float*)(base + l.dk), dk, st);
     }
 }
 
@@ -469,6 +466,14 @@ void run_step(int N, int H, int Hk, int dk, int dv, float scale, const void* q, 
 }
 
 }  // namespace
+
+void launch_group_sum(const Problem& p, int d, const float* part, void* out, cudaStream_t st) {
+    const dim3 grid((unsigned)p.seq.nseq, spread(p, ((long long)(p.seq.cu ? p.seq.rows : p.seq.len) * p.Hk * d) / 1024 + 1));
+    if (p.dtype == GDN_BF16)
+        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<<<grid, 256, 0, st>>>(p.seq, p.Hk, p.H / p.Hk, d, part, (__nv_bfloat16*)out)));
+    else
+        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<<<grid, 256, 0, st>>>(p.seq, p.Hk, p.H / p.Hk, d, part, (float*)out)));
+}
 
 size_t simt_bwd_workspace(const Problem& p) { return bwd_layout(p).end; }
 

@@ -56,11 +56,24 @@ void launch_simt_bwd(const Problem& p, const void* q, const void* k, const void*
                      const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
                      float* dg, float* dh0, void* ws, cudaStream_t st);
 
+// dq or dk of shared key heads: [token][H][d] fp32 summed over each group into [token][Hk][d].
+void launch_group_sum(const Problem& p, int d, const float* part, void* out, cudaStream_t st);
 
 // Tensor cores: bf16 with dk, dv in {64, 128} (decay_walk.cu).  The launchers return
 // false if a tensor map could not be encoded (nothing launched).
 bool tc_supported(const Problem& p);
 size_t tc_fwd_workspace(const Problem& p);
+// The backward (decay_bwd.cu).  launch_tc_states: the state entering each chunk of
+// 128 tokens and the gradient of the one leaving it, [slot][head][2 terms][dv/64][dk][64]
+// bf16 images, and cross [dv/64][slot][head] = e^{G_last} <S, dS>.
+size_t tc_states_workspace(const Problem& p);
+bool launch_tc_states(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
+                      const void* dO, const float* dhT, float* dh0, void* S, void* dS, float* cross, void* runs, void* ws,
+                      cudaStream_t st);
+size_t tc_bwd_workspace(const Problem& p);
+bool launch_tc_bwd(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
+                   const void* dO, const float* dhT, void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws,
+                   cudaStream_t st);
 bool launch_tc_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
                    void* o, float* hT, void* ws, cudaStream_t st);
 

@@ -47,7 +47,7 @@ gdn_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
 gdn_status launched() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 size_t fwd_need(const Problem& p) { return tc_supported(p) ? tc_fwd_workspace(p) : kStatusBytes; }
-size_t bwd_need(const Problem& p) { return simt_bwd_workspace(p); }
+size_t bwd_need(const Problem& p) { return tc_supported(p) ? tc_bwd_workspace(p) : simt_bwd_workspace(p); }
 
 // The workspace queries take no offsets: any non-null pointer stands for them.
 const int* const kSomeOffsets = reinterpret_cast<const int*>(4);
@@ -111,7 +111,11 @@ gdn_status gdn_decay_bwd(const gdn_decay_dims* d, const int* cu_seqlens, int nse
     cudaStream_t st = (cudaStream_t)stream;
     cudaGetLastError();
     if (cudaMemsetAsync(ws, 0, sizeof(unsigned int), st) != cudaSuccess) return GDN_ERR_CUDA;
-    launch_simt_bwd(p, q, k, v, g, h0, dO, dhT, dq, dk, dv, dg, dh0, ws, st);
+    if (tc_supported(p)) {
+        if (!launch_tc_bwd(p, q, k, v, g, h0, dO, dhT, dq, dk, dv, dg, dh0, ws, st)) return GDN_ERR_CUDA;
+    } else {
+        launch_simt_bwd(p, q, k, v, g, h0, dO, dhT, dq, dk, dv, dg, dh0, ws, st);
+    }
     return launched();
 }
 

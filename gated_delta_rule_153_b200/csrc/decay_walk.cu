@@ -28,11 +28,15 @@
 // K and V tiles go through a two-stage ring; Q, which A and X are done with early
 // in a chunk, has one place.
 //
+// MODE 2 walks K and V (backwards: Q and dO, with the gradient of the state) and
+// writes the state entering each chunk, as two bf16 terms, for the backward's
+// local products (decay_bwd.cu).
 // MODE 1 walks K and V alone and writes the state a run of chunks adds to a zero
 // state, with the run's decay.  With few chains, each is cut into runs: MODE 1 over
-// all runs but the last, then MODE 0 over all runs at once, each starting from the
+// all runs but the last, then MODE 0 or 2 over all runs at once, each starting from the
 // sum of the runs before it.
 #include <algorithm>
+#include <type_traits>
 
 #include "decay_tc.cuh"
 
@@ -57,7 +61,7 @@ struct alignas(1024) Smem {
     Gates gate[NST];
     float col[kEpi][96];         // per warp of P: decays from token j to the end of the block before its own
     uint64_t full[NST], gfull[NST], gfree[NST];
-    uint64_t q_full, a_done, p_ready, vt_ready, n_done, s_ready, x_done, o_done, o_free, drain;
+    uint64_t s_free, q_full, a_done, p_ready, vt_ready, n_done, s_ready, x_done, o_done, o_free, drain;
     uint32_t tmem;
 };
 
@@ -71,13 +75,17 @@ struct Params {
     float* hT;
     int runs, len;        // runs per chain, chunks per run
     float *runS, *runG;   // [chain][value block][run][DK][64] and [chain][run] of MODE 1
+    // MODE 2: [slot][head][2 terms][value block][DK][64] bf16, the state entering each chunk
+    __nv_bfloat16* image;
+    const __nv_bfloat16* other;  // backwards: the forward states, dotted into cross
+    float* cross;                // [value block][slot][head]
     unsigned int* status;
 };
 
 // tensor-memory columns: A, P (bf16 pairs), X, Y, N (the terms of V apart)
 constexpr uint32_t TA = 0, TP = 128, TX = 192, TY = 256, TN = 320, kCols = 512;
 
-template <int DK, int MODE>
+template <int DK, int MODE, bool REV>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_walk_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -95,10 +103,13 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     const int c0 = run * p.len, c1 = min(chunks, c0 + p.len);
     // the run that ends the chain (the first of an empty one) writes hT; runs past the end do nothing
     const bool last = c1 == chunks && (run == 0 || c0 < chunks);
-    if (MODE == 0 ? (c0 >= chunks && !last) : c1 >= chunks) return;
+    if (MODE != 1 ? (c0 >= chunks && !last) : c1 >= chunks) return;
     const int nc = c1 - c0;
     const size_t chain = (size_t)seq * p.H + h;
     const size_t slab = (size_t)DK * NB;
+    // chunk c of this run, in the order of the walk
+    auto chunk_of = [&](int c) { return REV ? chunks - 1 - (c0 + c) : c0 + c; };
+    const size_t slot0 = (size_t)(tok0 / CT) + seq;
 
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -107,6 +118,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             mbar_init(&s.gfree[i], MODE == 0 ? kEpi + kState : kState);
         }
         mbar_init(&s.q_full, 1);
+        mbar_init(&s.s_free, 1);
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
         mbar_init(&s.vt_ready, kState);
@@ -132,7 +144,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             // (two warps per 32 tokens: odd and even 16-column pieces of A, halves of O)
             const int blk = warp & 3, half = warp >> 2, i = 32 * blk + lane;
             for (int c = 0; c < nc; ++c) {
-                const int st = c % NST, L = min(CT, n - (c0 + c) * CT);
+                const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
                 const Gates& G = s.gate[st];
                 if (!warp_wait(&s.gfull[st], (c / NST) & 1)) break;
                 // decays between blocks factor at the end of the block before this row's: both
@@ -198,7 +210,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 // lanes 2m, 2m+1 trade 16-byte pieces, so that each store instruction
                 // writes whole 32-byte sectors: first row 2m, then row 2m + 1
                 const bool odd = lane & 1;
-                __nv_bfloat16* row = p.o + ((size_t)(tok0 + (long long)(c0 + c) * CT + (i & ~1)) * p.H + h) * p.dv +
+                __nv_bfloat16* row = p.o + ((size_t)(tok0 + (long long)chunk_of(c) * CT + (i & ~1)) * p.H + h) * p.dv +
                                      vb * NB + 32 * half + (odd ? 8 : 0);
                 const size_t next = (size_t)p.H * p.dv;
                 const bool up = (i & ~1) < L, dn = (i | 1) < L;
@@ -231,16 +243,33 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 ++done;
             }
         }
+        if constexpr (MODE == 2) {
+            // ---- the states' images to memory ------------------------------------
+            if (tid == 0) {
+                for (int c = 0; c < nc; ++c) {
+                    if (!wait_for(&s.s_ready, c & 1)) break;
+                    unsigned char* to = reinterpret_cast<unsigned char*>(p.image) +
+                                        ((slot0 + chunk_of(c)) * p.H + h) * (2 * gridDim.y * (size_t)(DK * 128)) + vb * (size_t)(DK * 128);
+                    bulk_s2g(to, s.Q, DK * 128);
+                    bulk_s2g(to + gridDim.y * (size_t)(DK * 128), (unsigned char*)s.Q + DK * 128, DK * 128);
+                    bulk_commit();
+                    bulk_wait_read<0>();
+                    mbar_arrive(&s.s_free);
+                    ++done;
+                }
+                bulk_wait<0>();
+            }
+        }
     } else if (warp < kEpi + kState) {
         // ---- the state: thread = key channel r, value channels 32 half .. +31 ------
         // (and, to split V, thread = token r of the same channels)
         const int half = (warp - kEpi) >> 2, r = 32 * (warp & 3) + lane;
         const bool own = r < DK;
         float S[32];
-        const float* h0 = MODE == 0 && p.h0 && own ? p.h0 + (chain * p.dv + vb * NB + 32 * half) * DK + r : nullptr;
+        const float* h0 = MODE != 1 && p.h0 && own ? p.h0 + (chain * p.dv + vb * NB + 32 * half) * DK + r : nullptr;
 #pragma unroll
         for (int e = 0; e < 32; ++e) S[e] = h0 ? h0[(size_t)e * DK] : 0.f;
-        if (MODE == 0 && own) {
+        if (MODE != 1 && own) {
             for (int q = 0; q < run; ++q) {  // what the runs before this one leave
                 const float a = p.runG[chain * p.runs + q];
                 const float* N = p.runS + ((chain * gridDim.y + vb) * p.runs + q) * slab + (size_t)(32 * half) * DK + r;
@@ -263,7 +292,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             tc5::fence_before();
         };
         for (int c = 0; c < nc; ++c) {
-            const int st = c % NST, L = min(CT, n - (c0 + c) * CT);
+            const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
             if (c > 0) {  // S entering chunk c; X(c-1), which read the last one, came before N(c-1)
                 if (!(ok = warp_wait(&s.n_done, (c - 1) & 1))) break;
                 tc5::fence_after();
@@ -281,9 +310,48 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.s_ready);
             }
+            if constexpr (MODE == 2) {
+                const size_t img = (((slot0 + chunk_of(c)) * p.H + h) * 2 * gridDim.y + vb) * slab;
+                if (REV) {
+                    // <S, dS> of the chunk: this thread's part of both
+                    float d = 0.f;
+                    if (own) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint4 a = *reinterpret_cast<const uint4*>(p.other + img + swz<64>(r, 32 * half + 8 * q));
+                            const uint4 b = *reinterpret_cast<const uint4*>(p.other + img + gridDim.y * slab + swz<64>(r, 32 * half + 8 * q));
+                            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 hi = unpack_bf16(x[e]), lo = unpack_bf16(y[e]);
+                                d += S[8 * q + 2 * e] * (hi.x + lo.x) + S[8 * q + 2 * e + 1] * (hi.y + lo.y);
+                            }
+                        }
+                    }
+                    d = warp_sum(d);
+                    if (lane == 0) s.col[warp - kEpi][c & 1] = d;
+                }
+                if (c > 0 && !(ok = warp_wait(&s.s_free, (c - 1) & 1))) break;
+                if (own) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t t[4][2];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) split_bf16<2>(t[e], S[8 * q + 2 * e], S[8 * q + 2 * e + 1]);
+                        unsigned char* at = (unsigned char*)s.Q + 2 * swz<64>(r, 32 * half + 8 * q);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
+                        *reinterpret_cast<uint4*>(at + DK * 128) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.s_ready);
+            }
             if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
             const float2 ge = s.gate[st].G[CT - 1];
-            const float wt = r < L ? pair_decay(ge, s.gate[st].G[r]) : 0.f;
+            // forwards what token r adds decays to the chunk's end, backwards from its start
+            const float2 gr = s.gate[st].G[r];
+            const float wt = r < L ? (REV ? p.scale * start_decay(gr) : pair_decay(ge, gr)) : 0.f;
             total = start_decay(ge);
             decay *= total;
             __syncwarp();
@@ -319,6 +387,13 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.vt_ready);
+            if (MODE == 2 && REV && warp == kEpi) {
+                // every state warp has left its part before its s_ready, which this one's wait follows
+                if (!(ok = warp_wait(&s.s_ready, c & 1))) break;
+                float d = lane < kState ? s.col[lane][c & 1] : 0.f;
+                d = warp_sum(d);
+                if (lane == 0) p.cross[(vb * (size_t)chunk_slots(p.seq, CT) + slot0 + chunk_of(c)) * p.H + h] = total * d;
+            }
             ++done;
         }
         if (ok && nc > 0) {
@@ -345,7 +420,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 // each operand goes in as soon as the products are done with the last in its place
                 const int st = c % NST, ph = (c - NST) & 1;
                 auto& q = s.st[st];
-                const int tok = (int)(tok0 + (long long)(c0 + c) * CT), kh = h / p.rep;
+                const int tok = (int)(tok0 + (long long)chunk_of(c) * CT), kh = h / p.rep;
                 if (c >= NST && !wait_for(&s.n_done, ph)) break;
                 mbar_arrive_expect(&s.full[st], (DK / 64 + 1) * PANEL);
 #pragma unroll
@@ -437,18 +512,20 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     } else {
         // ---- gates: the next chunk's values are on their way while this one's wait ----
         float x[4];
-        const float* g = p.g + (size_t)(tok0 + (long long)c0 * CT) * p.H + h;
-        if (nc > 0) load_gates(x, g, p.H, min(CT, n - c0 * CT));
+        auto load = [&](int c) {
+            load_gates(x, p.g + (size_t)(tok0 + (long long)chunk_of(c) * CT) * p.H + h, p.H, min(CT, n - chunk_of(c) * CT));
+        };
+        if (nc > 0) load(0);
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST;
             if (c >= NST && !warp_wait(&s.gfree[st], ((c / NST) - 1) & 1)) break;
             form_gates(s.gate[st], x);
             mbar_arrive(&s.gfull[st]);
-            if (c + 1 < nc) load_gates(x, g + (size_t)(c + 1) * CT * p.H, p.H, min(CT, n - (c0 + c + 1) * CT));
+            if (c + 1 < nc) load(c + 1);
             ++done;
         }
     }
-    if (lane == 0 && done < nc && (MODE == 0 || warp >= kEpi)) atomicOr(p.status, 1u);
+    if (lane == 0 && done < nc && (MODE == 0 || warp >= kEpi || (MODE == 2 && warp == 0))) atomicOr(p.status, 1u);
     tc5::fence_before();
     __syncthreads();
     if (warp == kEpi + kState + 1) {
@@ -483,11 +560,43 @@ Cut cut_of(const Problem& p) {
     return cut((long long)p.seq.nseq * p.H * (p.dv / NB), ((p.seq.cu ? p.seq.rows : p.seq.len) + CT - 1) / CT);
 }
 
-template <int DK, int MODE>
-void launch(const Params& a, dim3 grid, cudaStream_t st) {
-    const int smem = sizeof(Smem<DK>) + 1024;
-    cudaFuncSetAttribute(decay_tc_walk_kernel<DK, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    GDN_LAUNCH(MODE == 0 ? "decay_tc_walk" : "decay_tc_map", st, (decay_tc_walk_kernel<DK, MODE><<<grid, kThreads, smem, st>>>(a)));
+template <int MODE, bool REV>
+void launch(const Params& a, int dk, dim3 grid, cudaStream_t st) {
+    auto go = [&](auto d) {
+        constexpr int DK = decltype(d)::value;
+        const int smem = sizeof(Smem<DK>) + 1024;
+        cudaFuncSetAttribute(decay_tc_walk_kernel<DK, MODE, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        GDN_LAUNCH(MODE == 0 ? "decay_tc_walk" : MODE == 1 ? "decay_tc_map" : "decay_tc_states", st,
+                   (decay_tc_walk_kernel<DK, MODE, REV><<<grid, kThreads, smem, st>>>(a)));
+    };
+    if (dk == 64) go(std::integral_constant<int, 64>{});
+    else go(std::integral_constant<int, 128>{});
+}
+
+// Workspace of the runs, after `base` bytes: their states and decays.
+size_t runs_bytes(const Problem& p, const Cut& c) {
+    if (c.runs == 1) return 0;
+    const size_t chains = (size_t)p.seq.nseq * p.H;
+    return chains * c.runs * ((size_t)p.dk * p.dv * 4) + ((chains * c.runs * 4 + 255) & ~(size_t)255);
+}
+
+Params params_of(const Problem& p, const Cut& c, const float* g, void* runs, void* ws) {
+    Params a{};
+    a.seq = p.seq; a.H = p.H; a.rep = p.H / p.Hk; a.dv = p.dv; a.scale = p.scale;
+    a.g = g;
+    a.runs = c.runs; a.len = c.len;
+    a.status = (unsigned int*)ws;
+    a.runS = (float*)runs;
+    a.runG = a.runS + (size_t)p.seq.nseq * p.H * c.runs * p.dk * p.dv;
+    return a;
+}
+
+// All runs of a call: with more than one, first what each leaves.
+template <int MODE, bool REV>
+void launch_runs(const Params& a, const Problem& p, cudaStream_t st) {
+    const dim3 grid((unsigned)((size_t)p.seq.nseq * p.H), p.dv / NB, a.runs);
+    if (a.runs > 1) launch<1, REV>(a, p.dk, dim3(grid.x, grid.y, a.runs - 1), st);
+    launch<MODE, REV>(a, p.dk, grid, st);
 }
 
 }  // namespace
@@ -496,35 +605,33 @@ bool tc_supported(const Problem& p) {
     return p.dtype == GDN_BF16 && (p.dk == 64 || p.dk == 128) && (p.dv == 64 || p.dv == 128);
 }
 
-size_t tc_fwd_workspace(const Problem& p) {
-    const Cut c = cut_of(p);
-    if (c.runs == 1) return kStatusBytes;
-    const size_t chains = (size_t)p.seq.nseq * p.H;
-    return kStatusBytes + chains * c.runs * ((size_t)p.dk * p.dv * 4) + ((chains * c.runs * 4 + 255) & ~(size_t)255);
-}
+size_t tc_fwd_workspace(const Problem& p) { return kStatusBytes + runs_bytes(p, cut_of(p)); }
 
 bool launch_tc_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
                    void* o, float* hT, void* ws, cudaStream_t st) {
-    Params a{};
+    Params a = params_of(p, cut_of(p), g, (char*)ws + kStatusBytes, ws);
     if (!encode_head_map(&a.qmap, q, p.seq.rows, p.Hk, p.dk, CT) || !encode_head_map(&a.kmap, k, p.seq.rows, p.Hk, p.dk, CT) ||
         !encode_head_map(&a.vmap, v, p.seq.rows, p.H, p.dv, CT))
         return false;
-    const Cut c = cut_of(p);
-    const size_t chains = (size_t)p.seq.nseq * p.H;
-    a.seq = p.seq; a.H = p.H; a.rep = p.H / p.Hk; a.dv = p.dv; a.scale = p.scale;
-    a.g = g; a.h0 = h0; a.o = (__nv_bfloat16*)o; a.hT = hT;
-    a.runs = c.runs; a.len = c.len;
-    a.status = (unsigned int*)ws;
-    a.runS = (float*)((char*)ws + kStatusBytes);
-    a.runG = a.runS + chains * c.runs * p.dk * p.dv;
-    const dim3 grid((unsigned)chains, p.dv / NB, c.runs);
-    if (c.runs > 1) {
-        const dim3 maps(grid.x, grid.y, c.runs - 1);
-        if (p.dk == 64) launch<64, 1>(a, maps, st);
-        else launch<128, 1>(a, maps, st);
-    }
-    if (p.dk == 64) launch<64, 0>(a, grid, st);
-    else launch<128, 0>(a, grid, st);
+    a.h0 = h0; a.o = (__nv_bfloat16*)o; a.hT = hT;
+    launch_runs<0, false>(a, p, st);
+    return true;
+}
+
+size_t tc_states_workspace(const Problem& p) { return runs_bytes(p, cut_of(p)); }
+
+bool launch_tc_states(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
+                      const void* dO, const float* dhT, float* dh0, void* S, void* dS, float* cross, void* runs, void* ws,
+                      cudaStream_t st) {
+    Params a = params_of(p, cut_of(p), g, runs, ws), b = a;
+    if (!encode_head_map(&a.kmap, k, p.seq.rows, p.Hk, p.dk, CT) || !encode_head_map(&a.vmap, v, p.seq.rows, p.H, p.dv, CT) ||
+        !encode_head_map(&b.kmap, q, p.seq.rows, p.Hk, p.dk, CT) || !encode_head_map(&b.vmap, dO, p.seq.rows, p.H, p.dv, CT))
+        return false;
+    a.h0 = h0; a.image = (__nv_bfloat16*)S;
+    launch_runs<2, false>(a, p, st);
+    b.h0 = dhT; b.hT = dh0; b.image = (__nv_bfloat16*)dS;
+    b.other = (const __nv_bfloat16*)S; b.cross = cross;
+    launch_runs<2, true>(b, p, st);
     return true;
 }
 

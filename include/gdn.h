@@ -337,7 +337,8 @@ gdn_status gdn_recurrent_step(int N, int H, int dk, int dv, gdn_dtype dtype,
  * the last) are not read, and their rows of o, dq, dk, dv, dg are left as they
  * were.  A sequence whose offsets are not 0 <= cu[s] <= cu[s+1] <= T, or where
  * cu[s-1] > cu[s], is skipped and makes gdn_query_device_status on the workspace
- * return GDN_ERR_INVALID_ARG; sequences must not overlap.  nseq = 0 with a null
+ * return GDN_ERR_INVALID_ARG (the results of the call are then unspecified, though
+ * nothing outside the tensors is touched); sequences must not overlap.  nseq = 0 with a null
  * cu_seqlens is the plain batch.
  * Values: g <= 0 (documented, not checked); g = -inf is a reset.  The decay of a
  * pair of tokens is formed from an fp64 cumsum or token by token, the state and
