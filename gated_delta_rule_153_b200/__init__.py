@@ -12,7 +12,6 @@ states [B,H,dv,dk] fp32.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -693,38 +692,57 @@ def gdn_short_conv_bwd(x, w, dy, *, l2norm=True, workspace=None, stream=None):
 
 
 # ---- linear attention with a decay per head ----------------------------------
-@contextlib.contextmanager
-def _on(ref, stream, *others):
-    """The device of ``ref`` and, for the call's allocations, the stream it runs
-    on: what the call allocates then belongs to that stream.  Every tensor of
-    the call must be on the same device."""
+class _On:
+    """The device of a call's tensors and, when the caller names a stream, that
+    stream: what the call allocates then belongs to the stream it runs on.
+    Costs nothing where both are the current ones."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)     # sets its device too
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        import torch
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _want(t, name, dtype, shape, device):
+    """A contiguous CUDA tensor of this dtype and shape on this device."""
     import torch
-    for t in others:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"tensors on {ref.device} and {t.device} in one call")
-    with torch.cuda.device(ref.device):
-        if stream is None:
-            yield torch.cuda.current_stream()
-        else:
-            if stream.device != ref.device:
-                raise ValueError(f"stream of {stream.device} for tensors on {ref.device}")
-            with torch.cuda.stream(stream):
-                yield stream
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _given(t, name, like_shape, dtype, device):
+def _given(t, name, shape, dtype, device):
     """``t`` checked as an output, or a new tensor when it is None."""
     import torch
     if t is None:
-        return torch.empty(like_shape, dtype=dtype, device=device)
-    _need(t, name, dtype, like_shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want(t, name, dtype, shape, device)
     return t
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+    return t.numel() * t.element_size()
 
 
 def _scratch(nbytes, device, workspace):
@@ -747,34 +765,35 @@ def _decay_inputs(q, k, v, g, h0, cu_seqlens, scale):
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hk, dk]")
     B, T, Hk, dk = q.shape
-    _need(k, "k", q.dtype, (B, T, Hk, dk))
+    dev = q.device
+    _want(k, "k", q.dtype, q.shape, dev)
     _need(v, "v", q.dtype)
-    if v.dim() != 4 or tuple(v.shape[:2]) != (B, T):
-        raise ValueError("v must be [B, T, H, dv] matching q")
+    if v.dim() != 4 or v.shape[0] != B or v.shape[1] != T or v.device != dev:
+        raise ValueError(f"v must be [B, T, H, dv] matching q, on {dev}")
     H, dv = v.shape[2], v.shape[3]
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} value heads cannot share {Hk} key heads")
-    _need(g, "g", torch.float32, (B, T, H))
+    _want(g, "g", torch.float32, (B, T, H), dev)
     nseq = 0
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must be [nseq + 1] int32")
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2 or cu_seqlens.device != dev:
+            raise ValueError(f"cu_seqlens must be [nseq + 1] int32 on {dev}")
         if B != 1:
             raise ValueError("packed sequences take q [1, total_tokens, Hk, dk]")
-        nseq = cu_seqlens.numel() - 1
+        nseq = cu_seqlens.shape[0] - 1
     states = (nseq or B, H, dv, dk)
     if h0 is not None:
-        _need(h0, "h0", torch.float32, states)
-    return gdn_decay_dims(B, T, H, Hk, dk, dv, _dtype_code(q), float(scale)), nseq, states
+        _want(h0, "h0", torch.float32, states, dev)
+    return gdn_decay_dims(B, T, H, Hk, dk, dv, _dtype_code(q), scale), nseq, states
 
 
 def gdn_decay_fwd_workspace(dims: gdn_decay_dims, nseq: int = 0) -> int:
-    return int(lib().gdn_decay_fwd_workspace(ctypes.byref(dims), nseq))
+    return lib().gdn_decay_fwd_workspace(dims, nseq)
 
 
 def gdn_decay_bwd_workspace(dims: gdn_decay_dims, nseq: int = 0) -> int:
-    return int(lib().gdn_decay_bwd_workspace(ctypes.byref(dims), nseq))
+    return lib().gdn_decay_bwd_workspace(dims, nseq)
 
 
 def gdn_decay_fwd(q, k, v, g, h0=None, *, cu_seqlens=None, scale=1.0, output_final_state=True,
@@ -786,13 +805,15 @@ def gdn_decay_fwd(q, k, v, g, h0=None, *, cu_seqlens=None, scale=1.0, output_fin
     hT is None unless requested."""
     import torch
     dims, nseq, states = _decay_inputs(q, k, v, g, h0, cu_seqlens, scale)
-    with _on(q, stream, k, v, g, h0, cu_seqlens) as s:
-        o = _given(o, "o", tuple(v.shape), q.dtype, q.device)
+    dev = q.device
+    with _On(dev, stream) as s:
+        o = _given(o, "o", v.shape, q.dtype, dev)
         if output_final_state or hT is not None:
-            hT = _given(hT, "hT", states, torch.float32, q.device)
-        ws = _scratch(gdn_decay_fwd_workspace(dims, nseq), q.device, workspace)
-        st = lib().gdn_decay_fwd(ctypes.byref(dims), _ptr(cu_seqlens), nseq, _ptr(q), _ptr(k), _ptr(v),
-                                 _ptr(g), _ptr(h0), _ptr(o), _ptr(hT), _ptr(ws), _nbytes(ws), _stream(s))
+            hT = _given(hT, "hT", states, torch.float32, dev)
+        ws = _scratch(gdn_decay_fwd_workspace(dims, nseq), dev, workspace)
+        st = lib().gdn_decay_fwd(dims, _at(cu_seqlens), nseq, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                 g.data_ptr(), _at(h0), o.data_ptr(), _at(hT), ws.data_ptr(),
+                                 _nbytes(ws), s)
     _check(st, "gdn_decay_fwd")
     return o, hT
 
@@ -804,18 +825,19 @@ def gdn_decay_bwd(q, k, v, g, dO, h0=None, dhT=None, *, cu_seqlens=None, scale=1
     of preallocated results, filled in place."""
     import torch
     dims, nseq, states = _decay_inputs(q, k, v, g, h0, cu_seqlens, scale)
-    _need(dO, "dO", q.dtype, tuple(v.shape))
+    dev = q.device
+    _want(dO, "dO", q.dtype, v.shape, dev)
     if dhT is not None:
-        _need(dhT, "dhT", torch.float32, states)
-    with _on(q, stream, k, v, g, dO, h0, dhT, cu_seqlens) as s:
-        out = dict(out or {})
+        _want(dhT, "dhT", torch.float32, states, dev)
+    with _On(dev, stream) as s:
+        out = {} if out is None else dict(out)
         for n, ref in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dh0", h0)):
-            out[n] = None if ref is None else _given(out.get(n), n, tuple(ref.shape), ref.dtype, q.device)
-        ws = _scratch(gdn_decay_bwd_workspace(dims, nseq), q.device, workspace)
-        st = lib().gdn_decay_bwd(ctypes.byref(dims), _ptr(cu_seqlens), nseq, _ptr(q), _ptr(k), _ptr(v),
-                                 _ptr(g), _ptr(h0), _ptr(dO), _ptr(dhT), _ptr(out["dq"]),
-                                 _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dh0"]),
-                                 _ptr(ws), _nbytes(ws), _stream(s))
+            out[n] = None if ref is None else _given(out.get(n), n, ref.shape, ref.dtype, dev)
+        ws = _scratch(gdn_decay_bwd_workspace(dims, nseq), dev, workspace)
+        st = lib().gdn_decay_bwd(dims, _at(cu_seqlens), nseq, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                 g.data_ptr(), _at(h0), dO.data_ptr(), _at(dhT), out["dq"].data_ptr(),
+                                 out["dk"].data_ptr(), out["dv"].data_ptr(), out["dg"].data_ptr(),
+                                 _at(out["dh0"]), ws.data_ptr(), _nbytes(ws), s)
     _check(st, "gdn_decay_bwd")
     return out
 
@@ -828,19 +850,20 @@ def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
     if q.dim() != 3:
         raise ValueError("q must be [N, Hk, dk]")
     N, Hk, dk = q.shape
-    _need(k, "k", q.dtype, (N, Hk, dk))
+    dev = q.device
+    _want(k, "k", q.dtype, q.shape, dev)
     _need(v, "v", q.dtype)
-    if v.dim() != 3 or v.shape[0] != N:
-        raise ValueError("v must be [N, H, dv] matching q")
+    if v.dim() != 3 or v.shape[0] != N or v.device != dev:
+        raise ValueError(f"v must be [N, H, dv] matching q, on {dev}")
     H, dv = v.shape[1], v.shape[2]
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} value heads cannot share {Hk} key heads")
-    _need(g, "g", torch.float32, (N, H))
-    _need(state, "state", torch.float32, (N, H, dv, dk))
-    with _on(q, stream, k, v, g, state) as s:
-        o = _given(o, "o", (N, H, dv), q.dtype, q.device)
-        st = lib().gdn_decay_step(N, H, Hk, dk, dv, _dtype_code(q), float(scale), _ptr(q), _ptr(k),
-                                  _ptr(v), _ptr(g), _ptr(state), _ptr(o), _stream(s))
+    _want(g, "g", torch.float32, (N, H), dev)
+    _want(state, "state", torch.float32, (N, H, dv, dk), dev)
+    with _On(dev, stream) as s:
+        o = _given(o, "o", v.shape, q.dtype, dev)
+        st = lib().gdn_decay_step(N, H, Hk, dk, dv, _dtype_code(q), scale, q.data_ptr(), k.data_ptr(),
+                                  v.data_ptr(), g.data_ptr(), state.data_ptr(), o.data_ptr(), s)
     _check(st, "gdn_decay_step")
     return o
 
@@ -848,23 +871,24 @@ def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
 # ---- draft-tree attention over a paged cache ---------------------------------
 def _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len):
     import torch
-    _need(parent, "parent", torch.int32)
-    if parent.dim() != 2:
-        raise ValueError("parent must be [N, M] int32")
-    N, M = parent.shape
     _need(k, "k")
-    if k.dim() != 4 or tuple(k.shape[:2]) != (N, M):
+    dev = k.device
+    _need(parent, "parent", torch.int32)
+    if parent.dim() != 2 or parent.device != dev:
+        raise ValueError(f"parent must be [N, M] int32 on {dev}")
+    N, M = parent.shape
+    if k.dim() != 4 or k.shape[0] != N or k.shape[1] != M:
         raise ValueError("k must be [N, M, Hkv, d]")
     Hkv, d = k.shape[2], k.shape[3]
-    _need(v, "v", k.dtype, tuple(k.shape))
+    _want(v, "v", k.dtype, k.shape, dev)
     _need(k_cache, "k_cache", k.dtype)
-    if k_cache.dim() != 4 or tuple(k_cache.shape[2:]) != (Hkv, d):
-        raise ValueError("k_cache must be [pages, page, Hkv, d]")
-    _need(v_cache, "v_cache", k.dtype, tuple(k_cache.shape))
+    if k_cache.dim() != 4 or k_cache.shape[2] != Hkv or k_cache.shape[3] != d or k_cache.device != dev:
+        raise ValueError(f"k_cache must be [pages, page, Hkv, d] on {dev}")
+    _want(v_cache, "v_cache", k.dtype, k_cache.shape, dev)
     _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != N:
-        raise ValueError("block_table must be [N, width] int32")
-    _need(cache_len, "cache_len", torch.int32, (N,))
+    if block_table.dim() != 2 or block_table.shape[0] != N or block_table.device != dev:
+        raise ValueError(f"block_table must be [N, width] int32 on {dev}")
+    _want(cache_len, "cache_len", torch.int32, (N,), dev)
     return N, M, Hkv, d, k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
 
 
@@ -876,18 +900,18 @@ def gdn_tree_attn(parent, q, k, v, k_cache, v_cache, block_table, cache_len, *, 
     cache_len [N] int32.  window > 0: only positions less than ``window`` back.
     Returns o [N,M,Hq,d]."""
     N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len)
+    dev = k.device
     _need(q, "q", k.dtype)
-    if q.dim() != 4 or tuple(q.shape[:2]) != (N, M) or q.shape[3] != d:
-        raise ValueError("q must be [N, M, Hq, d] matching k")
-    Hq = q.shape[2]
-    with _on(q, stream, parent, k, v, k_cache, v_cache, block_table, cache_len) as s:
-        o = _given(o, "o", tuple(q.shape), q.dtype, q.device)
-        need = int(lib().gdn_tree_attn_workspace(N, M, Hq, Hkv, d, _dtype_code(q), page, width))
-        ws = _scratch(need, q.device, workspace)
-        st = lib().gdn_tree_attn(N, M, Hq, Hkv, d, _dtype_code(q), float(scale), int(window), _ptr(parent),
-                                 _ptr(q), _ptr(k), _ptr(v), pages, page, width, _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(block_table), _ptr(cache_len), _ptr(o), _ptr(ws),
-                                 _nbytes(ws), _stream(s))
+    if q.dim() != 4 or q.shape[0] != N or q.shape[1] != M or q.shape[3] != d or q.device != dev:
+        raise ValueError(f"q must be [N, M, Hq, d] matching k, on {dev}")
+    Hq, dt = q.shape[2], _dtype_code(q)
+    with _On(dev, stream) as s:
+        o = _given(o, "o", q.shape, q.dtype, dev)
+        ws = _scratch(lib().gdn_tree_attn_workspace(N, M, Hq, Hkv, d, dt, page, width), dev, workspace)
+        st = lib().gdn_tree_attn(N, M, Hq, Hkv, d, dt, scale, window, parent.data_ptr(), q.data_ptr(),
+                                 k.data_ptr(), v.data_ptr(), pages, page, width, k_cache.data_ptr(),
+                                 v_cache.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(),
+                                 o.data_ptr(), ws.data_ptr(), _nbytes(ws), s)
     _check(st, "gdn_tree_attn")
     return o
 
@@ -899,17 +923,18 @@ def gdn_tree_append(parent, accepted, k, v, k_cache, v_cache, block_table, cache
     the new lengths (``new_len`` may be ``cache_len``)."""
     import torch
     N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len)
-    _need(accepted, "accepted", torch.int32, (N,))
+    dev = k.device
+    _want(accepted, "accepted", torch.int32, (N,), dev)
     if status is not None:
         _need(status, "status", torch.int32)
-        if status.numel() < 1:
-            raise ValueError("status must hold a word")
-    with _on(k, stream, parent, accepted, v, k_cache, v_cache, block_table, cache_len, status) as s:
-        new_len = _given(new_len, "new_len", (N,), torch.int32, k.device)
-        st = lib().gdn_tree_append(N, M, Hkv, d, _dtype_code(k), _ptr(parent), _ptr(accepted), _ptr(k),
-                                   _ptr(v), pages, page, width, _ptr(k_cache), _ptr(v_cache),
-                                   _ptr(block_table), _ptr(cache_len), _ptr(new_len), _ptr(status),
-                                   _stream(s))
+        if status.numel() < 1 or status.device != dev:
+            raise ValueError(f"status must hold a word on {dev}")
+    with _On(dev, stream) as s:
+        new_len = _given(new_len, "new_len", (N,), torch.int32, dev)
+        st = lib().gdn_tree_append(N, M, Hkv, d, _dtype_code(k), parent.data_ptr(), accepted.data_ptr(),
+                                   k.data_ptr(), v.data_ptr(), pages, page, width, k_cache.data_ptr(),
+                                   v_cache.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(),
+                                   new_len.data_ptr(), _at(status), s)
     _check(st, "gdn_tree_append")
     return new_len
 
@@ -921,21 +946,20 @@ def _norm_inputs(x, z, w):
     if x.dim() < 2:
         raise ValueError("x must be [..., H, d]")
     H, d = x.shape[-2], x.shape[-1]
-    _need(z, "z", x.dtype, tuple(x.shape))
-    _need(w, "w", torch.float32)
-    if tuple(w.shape) not in ((d,), (H, d)):
-        raise ValueError(f"w must be [d] or [H, d] for x [..., {H}, {d}]")
-    return x.numel() // max(d, 1), H, d, 1 if w.dim() == 1 else H
+    _want(z, "z", x.dtype, x.shape, x.device)
+    shared = isinstance(w, torch.Tensor) and w.dim() == 1
+    _want(w, "w", torch.float32, (d,) if shared else (H, d), x.device)
+    return x.numel() // max(d, 1), H, d, 1 if shared else H
 
 
 def gdn_gated_norm_fwd(x, z, w, *, eps=1e-6, center=False, y=None, stream=None):
     """y = w * norm(x) * SiLU(z), the norm over the last axis of x [...,H,d]: RMS,
     or mean and variance with ``center``; w [d] or [H,d] fp32."""
     rows, H, d, wheads = _norm_inputs(x, z, w)
-    with _on(x, stream, z, w) as s:
-        y = _given(y, "y", tuple(x.shape), x.dtype, x.device)
-        st = lib().gdn_gated_norm_fwd(rows, H, d, wheads, _dtype_code(x), int(bool(center)), float(eps),
-                                      _ptr(x), _ptr(z), _ptr(w), _ptr(y), _stream(s))
+    with _On(x.device, stream) as s:
+        y = _given(y, "y", x.shape, x.dtype, x.device)
+        st = lib().gdn_gated_norm_fwd(rows, H, d, wheads, _dtype_code(x), bool(center), eps, x.data_ptr(),
+                                      z.data_ptr(), w.data_ptr(), y.data_ptr(), s)
     _check(st, "gdn_gated_norm_fwd")
     return y
 
@@ -944,15 +968,15 @@ def gdn_gated_norm_bwd(x, z, w, dy, *, eps=1e-6, center=False, dx=None, dz=None,
                        stream=None):
     """Gradients of <dy, y> for gdn_gated_norm_fwd: returns (dx, dz, dw)."""
     rows, H, d, wheads = _norm_inputs(x, z, w)
-    _need(dy, "dy", x.dtype, tuple(x.shape))
-    with _on(x, stream, z, w, dy) as s:
-        dx = _given(dx, "dx", tuple(x.shape), x.dtype, x.device)
-        dz = _given(dz, "dz", tuple(x.shape), x.dtype, x.device)
-        dw = _given(dw, "dw", tuple(w.shape), w.dtype, x.device)
-        need = int(lib().gdn_gated_norm_bwd_workspace(rows, H, d, _dtype_code(x)))
-        ws = _scratch(need, x.device, workspace)
-        st = lib().gdn_gated_norm_bwd(rows, H, d, wheads, _dtype_code(x), int(bool(center)), float(eps),
-                                      _ptr(x), _ptr(z), _ptr(w), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw),
-                                      _ptr(ws), _nbytes(ws), _stream(s))
+    dev, dt = x.device, _dtype_code(x)
+    _want(dy, "dy", x.dtype, x.shape, dev)
+    with _On(dev, stream) as s:
+        dx = _given(dx, "dx", x.shape, x.dtype, dev)
+        dz = _given(dz, "dz", x.shape, x.dtype, dev)
+        dw = _given(dw, "dw", w.shape, w.dtype, dev)
+        ws = _scratch(lib().gdn_gated_norm_bwd_workspace(rows, H, d, dt), dev, workspace)
+        st = lib().gdn_gated_norm_bwd(rows, H, d, wheads, dt, bool(center), eps, x.data_ptr(), z.data_ptr(),
+                                      w.data_ptr(), dy.data_ptr(), dx.data_ptr(), dz.data_ptr(),
+                                      dw.data_ptr(), ws.data_ptr(), _nbytes(ws), s)
     _check(st, "gdn_gated_norm_bwd")
     return dx, dz, dw

@@ -13,7 +13,7 @@
 // rows u, u + U, ... with U a multiple of the heads: neighbouring units read
 // neighbouring rows, and a unit's head, and so its slice of w, never changes.  A
 // unit therefore sums its dw in registers; a second kernel adds the units of a
-// head (of all heads, for a shared w) in a fixed order.
+// head (for a shared w, first within the CTA, then over the CTAs) in a fixed order.
 #include <math.h>
 
 #include <algorithm>
@@ -140,7 +140,19 @@ gated_norm_kernel(long long rows, int H, int wheads, long long U, float eps, con
         }
     }
     if constexpr (BWD) {
-        if (unit < U) {
+        if (wheads == 1) {  // one sum per CTA, its units in order
+            __shared__ float sum[R::UPC][D];
+#pragma unroll
+            for (int j = 0; j < R::CPL; ++j)
+                sum[threadIdx.x / R::LPR][(j / R::VEC * R::LPR + sub) * R::VEC + j % R::VEC] = dw[j];
+            __syncthreads();
+            for (int c = threadIdx.x; c < D; c += NT) {
+                float t = 0.f;
+#pragma unroll 8
+                for (int u = 0; u < R::UPC; ++u) t += sum[u][c];
+                part[(size_t)blockIdx.x * D + c] = t;
+            }
+        } else if (unit < U) {
 #pragma unroll
             for (int j = 0; j < R::CPL; ++j)
                 part[unit * D + (j / R::VEC * R::LPR + sub) * R::VEC + j % R::VEC] = dw[j];
@@ -148,13 +160,14 @@ gated_norm_kernel(long long rows, int H, int wheads, long long U, float eps, con
     }
 }
 
-// dw[h] = sum of the units' parts over u = h, h + heads, ... (heads = 1 for a
-// shared w), 32 sums in parallel per channel, joined in a fixed order.
+// dw[h] = sum of the parts u = h, h + heads, ... of U (per unit; for a shared w per CTA,
+// heads = 1), 32 sums in parallel per channel, joined in a fixed order.
 __global__ void __launch_bounds__(1024)
 gated_norm_dw_kernel(long long U, int heads, int D, const float* __restrict__ part, float* __restrict__ dw) {
     __shared__ float s[32][33];
     const int c = blockIdx.y * 32 + threadIdx.x, h = blockIdx.x;
     float sum = 0.f;
+#pragma unroll 4
     for (long long u = h + (long long)threadIdx.y * heads; u < U; u += 32ll * heads) sum += part[u * D + c];
     s[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
@@ -251,7 +264,9 @@ gdn_status gdn_gated_norm_bwd(long long rows, int H, int d, int wheads, gdn_dtyp
     cudaGetLastError();
     s = run<true>(rows, H, d, wheads, dtype, center, eps, x, z, w, dy, dx, dz, (float*)ws, st);
     if (s != GDN_OK) return s;
-    const long long U = units(rows, H, lanes_per_row(dtype, d));
+    const int lpr = lanes_per_row(dtype, d), upc = NT / lpr;
+    long long U = units(rows, H, lpr);
+    if (wheads == 1) U = (U + upc - 1) / upc;
     GDN_LAUNCH("gated_norm_dw", st, (gated_norm_dw_kernel<<<dim3((unsigned)wheads, d / 32), dim3(32, 32), 0, st>>>(
         U, wheads, d, (const float*)ws, dw)));
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
