@@ -16,6 +16,11 @@ import ctypes
 import os
 import threading
 
+try:  # needed by every call, though not to build the library
+    import torch
+except ImportError:
+    torch = None
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
 
@@ -695,23 +700,24 @@ def gdn_short_conv_bwd(x, w, dy, *, l2norm=True, workspace=None, stream=None):
 class _On:
     """The device of a call's tensors and, when the caller names a stream, that
     stream: what the call allocates then belongs to the stream it runs on.
-    Costs nothing where both are the current ones."""
+    Entering gives the stream's handle; where device and stream are the current
+    ones that is all it does."""
 
     def __init__(self, device, stream):
-        import torch
-        self.ctx = None
+        self.ctx, self.handle = None, None
         if stream is not None:
             if stream.device != device:
                 raise ValueError(f"stream of {stream.device} for tensors on {device}")
-            self.ctx = torch.cuda.stream(stream)     # sets its device too
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
+            self.ctx, self.handle = torch.cuda.stream(stream), stream.cuda_stream  # sets its device too
+        else:
+            if device.index != torch.cuda.current_device():
+                self.ctx = torch.cuda.device(device)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
 
     def __enter__(self):
-        import torch
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return self.handle
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -720,7 +726,6 @@ class _On:
 
 def _want(t, name, dtype, shape, device):
     """A contiguous CUDA tensor of this dtype and shape on this device."""
-    import torch
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
             and t.is_contiguous():
         return
@@ -730,10 +735,17 @@ def _want(t, name, dtype, shape, device):
 
 def _given(t, name, shape, dtype, device):
     """``t`` checked as an output, or a new tensor when it is None."""
-    import torch
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _want(t, name, dtype, shape, device)
+    return t
+
+
+def _like(t, name, ref):
+    """``t`` checked as an output of ``ref``'s kind, or a new one."""
+    if t is None:
+        return torch.empty_like(ref)
+    _want(t, name, ref.dtype, ref.shape, ref.device)
     return t
 
 
@@ -747,7 +759,6 @@ def _nbytes(t):
 
 def _scratch(nbytes, device, workspace):
     """The caller's workspace, checked, or a new one."""
-    import torch
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if not isinstance(workspace, torch.Tensor) or workspace.device != device:
@@ -760,7 +771,6 @@ def _scratch(nbytes, device, workspace):
 
 
 def _decay_inputs(q, k, v, g, h0, cu_seqlens, scale):
-    import torch
     _need(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hk, dk]")
@@ -803,11 +813,10 @@ def gdn_decay_fwd(q, k, v, g, h0=None, *, cu_seqlens=None, scale=1.0, output_fin
     [B,H,dv,dk] fp32.  With ``cu_seqlens`` (int32 on the device) B is 1, the row
     holds packed sequences and the states are [nseq,H,dv,dk].  Returns (o, hT);
     hT is None unless requested."""
-    import torch
     dims, nseq, states = _decay_inputs(q, k, v, g, h0, cu_seqlens, scale)
     dev = q.device
     with _On(dev, stream) as s:
-        o = _given(o, "o", v.shape, q.dtype, dev)
+        o = _like(o, "o", v)
         if output_final_state or hT is not None:
             hT = _given(hT, "hT", states, torch.float32, dev)
         ws = _scratch(gdn_decay_fwd_workspace(dims, nseq), dev, workspace)
@@ -823,7 +832,6 @@ def gdn_decay_bwd(q, k, v, g, dO, h0=None, dhT=None, *, cu_seqlens=None, scale=1
     """Backward of <dO,o> + <dhT,hT> for gdn_decay_fwd.  Returns a dict with dq,
     dk, dv (dtype of q), dg, dh0 (None when h0 is None).  ``out``: optional dict
     of preallocated results, filled in place."""
-    import torch
     dims, nseq, states = _decay_inputs(q, k, v, g, h0, cu_seqlens, scale)
     dev = q.device
     _want(dO, "dO", q.dtype, v.shape, dev)
@@ -832,7 +840,7 @@ def gdn_decay_bwd(q, k, v, g, dO, h0=None, dhT=None, *, cu_seqlens=None, scale=1
     with _On(dev, stream) as s:
         out = {} if out is None else dict(out)
         for n, ref in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dh0", h0)):
-            out[n] = None if ref is None else _given(out.get(n), n, ref.shape, ref.dtype, dev)
+            out[n] = None if ref is None else _like(out.get(n), n, ref)
         ws = _scratch(gdn_decay_bwd_workspace(dims, nseq), dev, workspace)
         st = lib().gdn_decay_bwd(dims, _at(cu_seqlens), nseq, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                  g.data_ptr(), _at(h0), dO.data_ptr(), _at(dhT), out["dq"].data_ptr(),
@@ -845,7 +853,6 @@ def gdn_decay_bwd(q, k, v, g, dO, h0=None, dhT=None, *, cu_seqlens=None, scale=1
 def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
     """One decode token of gdn_decay_fwd's recurrence, in place on ``state``
     [N,H,dv,dk] fp32: q, k [N,Hk,dk]; v [N,H,dv]; g [N,H] fp32.  Returns o."""
-    import torch
     _need(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [N, Hk, dk]")
@@ -861,7 +868,7 @@ def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
     _want(g, "g", torch.float32, (N, H), dev)
     _want(state, "state", torch.float32, (N, H, dv, dk), dev)
     with _On(dev, stream) as s:
-        o = _given(o, "o", v.shape, q.dtype, dev)
+        o = _like(o, "o", v)
         st = lib().gdn_decay_step(N, H, Hk, dk, dv, _dtype_code(q), scale, q.data_ptr(), k.data_ptr(),
                                   v.data_ptr(), g.data_ptr(), state.data_ptr(), o.data_ptr(), s)
     _check(st, "gdn_decay_step")
@@ -870,7 +877,6 @@ def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
 
 # ---- draft-tree attention over a paged cache ---------------------------------
 def _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len):
-    import torch
     _need(k, "k")
     dev = k.device
     _need(parent, "parent", torch.int32)
@@ -906,7 +912,7 @@ def gdn_tree_attn(parent, q, k, v, k_cache, v_cache, block_table, cache_len, *, 
         raise ValueError(f"q must be [N, M, Hq, d] matching k, on {dev}")
     Hq, dt = q.shape[2], _dtype_code(q)
     with _On(dev, stream) as s:
-        o = _given(o, "o", q.shape, q.dtype, dev)
+        o = _like(o, "o", q)
         ws = _scratch(lib().gdn_tree_attn_workspace(N, M, Hq, Hkv, d, dt, page, width), dev, workspace)
         st = lib().gdn_tree_attn(N, M, Hq, Hkv, d, dt, scale, window, parent.data_ptr(), q.data_ptr(),
                                  k.data_ptr(), v.data_ptr(), pages, page, width, k_cache.data_ptr(),
@@ -921,7 +927,6 @@ def gdn_tree_append(parent, accepted, k, v, k_cache, v_cache, block_table, cache
     """Appends the k and v rows of the root path of node accepted[n] (int32 [N];
     -1: nothing) to sequence n's pages, in place on k_cache and v_cache.  Returns
     the new lengths (``new_len`` may be ``cache_len``)."""
-    import torch
     N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len)
     dev = k.device
     _want(accepted, "accepted", torch.int32, (N,), dev)
@@ -930,7 +935,7 @@ def gdn_tree_append(parent, accepted, k, v, k_cache, v_cache, block_table, cache
         if status.numel() < 1 or status.device != dev:
             raise ValueError(f"status must hold a word on {dev}")
     with _On(dev, stream) as s:
-        new_len = _given(new_len, "new_len", (N,), torch.int32, dev)
+        new_len = _like(new_len, "new_len", cache_len)
         st = lib().gdn_tree_append(N, M, Hkv, d, _dtype_code(k), parent.data_ptr(), accepted.data_ptr(),
                                    k.data_ptr(), v.data_ptr(), pages, page, width, k_cache.data_ptr(),
                                    v_cache.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(),
@@ -941,7 +946,6 @@ def gdn_tree_append(parent, accepted, k, v, k_cache, v_cache, block_table, cache
 
 # ---- output norm and gate ----------------------------------------------------
 def _norm_inputs(x, z, w):
-    import torch
     _need(x, "x")
     if x.dim() < 2:
         raise ValueError("x must be [..., H, d]")
@@ -957,7 +961,7 @@ def gdn_gated_norm_fwd(x, z, w, *, eps=1e-6, center=False, y=None, stream=None):
     or mean and variance with ``center``; w [d] or [H,d] fp32."""
     rows, H, d, wheads = _norm_inputs(x, z, w)
     with _On(x.device, stream) as s:
-        y = _given(y, "y", x.shape, x.dtype, x.device)
+        y = _like(y, "y", x)
         st = lib().gdn_gated_norm_fwd(rows, H, d, wheads, _dtype_code(x), bool(center), eps, x.data_ptr(),
                                       z.data_ptr(), w.data_ptr(), y.data_ptr(), s)
     _check(st, "gdn_gated_norm_fwd")
@@ -971,9 +975,9 @@ def gdn_gated_norm_bwd(x, z, w, dy, *, eps=1e-6, center=False, dx=None, dz=None,
     dev, dt = x.device, _dtype_code(x)
     _want(dy, "dy", x.dtype, x.shape, dev)
     with _On(dev, stream) as s:
-        dx = _given(dx, "dx", x.shape, x.dtype, dev)
-        dz = _given(dz, "dz", x.shape, x.dtype, dev)
-        dw = _given(dw, "dw", w.shape, w.dtype, dev)
+        dx = _like(dx, "dx", x)
+        dz = _like(dz, "dz", x)
+        dw = _like(dw, "dw", w)
         ws = _scratch(lib().gdn_gated_norm_bwd_workspace(rows, H, d, dt), dev, workspace)
         st = lib().gdn_gated_norm_bwd(rows, H, d, wheads, dt, bool(center), eps, x.data_ptr(), z.data_ptr(),
                                       w.data_ptr(), dy.data_ptr(), dx.data_ptr(), dz.data_ptr(),
