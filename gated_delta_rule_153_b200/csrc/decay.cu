@@ -23,32 +23,33 @@
 // the states at each chunk's end, so the sums stay 64 tokens long: taken over
 // a whole sequence instead, their rounding would grow with its length.
 //
-// A row of R is covered by L = CD/16 lanes of 16 columns each, one or
-// two rows per thread, so R never leaves the registers; a tile of 32 tokens is staged in
-// shared memory as fp32.  What bounds it is the fp32 FMA rate: 3 operations
-// per state element and token (dk = dv = 128: 49 k per token-head and walk).
+// Tiles of 32 tokens are taken at once.  With G the cumsum of the gates from the tile's
+// start, D_ts the decay between tokens t and s, and R what enters the tile,
+//     out_t = c (f_t R x_t + sum_s D_ts (w_s.x_t) y_s),   R <- e^{G_last} R + sum_s h_s y_s w_s^T
+// over s <= t, with f = e^G and h = e^{G_last - G} forwards, and over s >= t, with the two
+// exchanged, backwards.  All of it is small matrix products in fp32 on CUDA cores, from
+// shared memory in 2 x 4 and 4 x 4 register tiles; a CTA holds 32 rows of R, and the next
+// tile's values are on their way to registers meanwhile.  What bounds it is the issue of
+// fp32 FMAs and their shared-memory loads, one tile after the other along a chain.
 #include <math.h>
 
 #include <type_traits>
 
 #include "common.cuh"
 #include "decay.h"
+#include "decay_tc.cuh"
 
 namespace gdn {
 namespace decay {
 namespace {
 
-constexpr int TT = 32;          // tokens per staged tile
+constexpr int TT = 32;          // tokens per tile
 constexpr int WT = 128;         // threads per CTA
+constexpr int RB = 32;          // rows of R per CTA
 constexpr int AC = 64;          // tokens per chunk of the gate gradient
 
 // A gate of -inf (or one so low that e^g is zero in fp32) is a reset.
 GDN_DEV float decay_of(float g) { return expf(g); }
-
-template <int CD>
-constexpr int rows_per_thread() { return CD >= 64 ? 2 : 1; }
-template <int CD>
-constexpr int rows_per_cta() { return (WT / 32) * (32 / (CD / 16)) * rows_per_thread<CD>(); }
 
 struct Operand {
     const void* p;
@@ -75,161 +76,279 @@ struct Walk {
     unsigned int* status;
 };
 
+// Four consecutive values.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    using Raw = float4;
+    GDN_DEV static float4 of(float4 v) { return v; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+    using Raw = uint2;
+    GDN_DEV static float4 of(uint2 v) {
+        const float2 a = unpack_bf16(v.x), b = unpack_bf16(v.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+};
+GDN_DEV void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+GDN_DEV void put4(__nv_bfloat16* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+template <int CD>
+struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in different banks
+    float x[TT][CD + 4], w[TT][CD + 4], y[TT][RB + 4], z[TT][RB + 4], p[TT][TT + 4];
+    float r[CD][RB + 4];
+    float2 g[TT];
+    float f[TT], h[TT], own[TT], red[WT / 32];
+};
+
 template <int CD, typename T, bool REV>
 __global__ void __launch_bounds__(WT)
 decay_walk_kernel(const Walk p) {
-    constexpr int L = CD / 16, RPW = 32 / L, RPT = rows_per_thread<CD>(), RB = rows_per_cta<CD>(),
-                  NW = WT / 32;
-    __shared__ __align__(16) float sx[TT][CD], sw[TT][CD];
-    __shared__ float sy[TT][RB], sz[TT][RB], sa[TT], sdot[NW][TT], sred[NW];
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
+    extern __shared__ __align__(16) unsigned char raw[];
+    WalkSmem<CD>& s = *reinterpret_cast<WalkSmem<CD>*>(raw);
+    using F = Four<T>;
+    constexpr int NX = TT * CD / 4 / WT > 0 ? TT * CD / 4 / WT : 1;  // groups of four per thread and tile
+    constexpr int NC = CD / 16;                                      // columns of R per thread
+    const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sub = lane % L, grp = lane / L;
     long long tok0;
     int n;
-    if (!span_of(p.seq, s, tok0, n)) {
+    if (!span_of(p.seq, seq, tok0, n)) {
         if (tid == 0) atomicOr(p.status, 2u);
         return;
     }
-    const size_t sh = (size_t)s * p.H + h;
-    const long long slot0 = tok0 / AC + s;
-    int row[RPT];
-    float R[RPT][16];
-#pragma unroll
-    for (int q = 0; q < RPT; ++q) {
-        row[q] = (warp * RPT + q) * RPW + grp;  // within the block
-        const int r = r0 + row[q];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int c = 4 * (sub + L * (e / 4)) + e % 4;
-            R[q][e] = 0.f;
-            if (p.init && r < p.RD)
-                R[q][e] = p.init_t ? p.init[(sh * CD + c) * p.RD + r] : p.init[(sh * p.RD + r) * CD + c];
-        }
+    const size_t sh = (size_t)seq * p.H + h;
+    const long long slot0 = tok0 / AC + seq;
+    // R, column-major
+    for (int e = tid; e < CD * RB; e += WT) {
+        const int c = p.init_t ? e / RB : e % CD, r = p.init_t ? e % RB : e / CD, row = r0 + r;
+        s.r[c][r] = !p.init || row >= p.RD ? 0.f : p.init_t ? p.init[(sh * CD + c) * p.RD + row] : p.init[(sh * p.RD + row) * CD + c];
     }
     const int tiles = (n + TT - 1) / TT;
+    typename F::Raw px[NX], pw[NX], py[2], pz[2];
+    float pg = 0.f;
+    const bool has_z = p.dots != nullptr;
+    auto fetch = [&](int tile) {
+        const int m = min(TT, n - tile * TT);
+        const long long t0 = tok0 + (long long)tile * TT;
+        const typename F::Raw zero{};
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
+            const bool in = t < m;
+            px[i] = in ? *reinterpret_cast<const typename F::Raw*>((const T*)p.x.p + row_of(p.x, t0 + t, h) + c) : zero;
+            pw[i] = in ? *reinterpret_cast<const typename F::Raw*>((const T*)p.w.p + row_of(p.w, t0 + t, h) + c) : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = 4 * (tid + WT * i), t = e / RB, r = e % RB;
+            const bool in = t < m && r0 + r < p.RD;
+            py[i] = in ? *reinterpret_cast<const typename F::Raw*>((const T*)p.y.p + row_of(p.y, t0 + t, h) + r0 + r) : zero;
+            pz[i] = in && has_z ? *reinterpret_cast<const typename F::Raw*>((const T*)p.z.p + row_of(p.z, t0 + t, h) + r0 + r) : zero;
+        }
+        if (warp == 0) pg = lane < m ? p.g[(size_t)(t0 + lane) * p.H + h] : 0.f;
+    };
+    if (tiles > 0) fetch(REV ? tiles - 1 : 0);
     for (int it = 0; it < tiles; ++it) {
         const int tile = REV ? tiles - 1 - it : it;
         const int m = min(TT, n - tile * TT);
         const long long t0 = tok0 + (long long)tile * TT;
+        const int end = tile * TT + m;
+        const bool border = end % AC == 0 || end == n;  // the tile ends a chunk
+        const long long slot = slot0 + (end - 1) / AC;
         __syncthreads();
-        for (int e = tid; e < m * CD; e += WT) {
-            const int t = e / CD, c = e % CD;
-            sx[t][c] = to_f(((const T*)p.x.p)[row_of(p.x, t0 + t, h) + c]);
-            sw[t][c] = to_f(((const T*)p.w.p)[row_of(p.w, t0 + t, h) + c]);
+        if (TT * CD / 4 >= WT || tid < TT * CD / 4) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
+                *reinterpret_cast<float4*>(&s.x[t][c]) = F::of(px[i]);
+                *reinterpret_cast<float4*>(&s.w[t][c]) = F::of(pw[i]);
+            }
         }
-        for (int e = tid; e < m * RB; e += WT) {
-            const int t = e / RB, r = e % RB;
-            const bool in = r0 + r < p.RD;
-            sy[t][r] = in ? p.c_y * to_f(((const T*)p.y.p)[row_of(p.y, t0 + t, h) + r0 + r]) : 0.f;
-            if (p.dots) sz[t][r] = in ? to_f(((const T*)p.z.p)[row_of(p.z, t0 + t, h) + r0 + r]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = 4 * (tid + WT * i), t = e / RB, r = e % RB;
+            const float4 v = F::of(py[i]);
+            *reinterpret_cast<float4*>(&s.y[t][r]) = make_float4(p.c_y * v.x, p.c_y * v.y, p.c_y * v.z, p.c_y * v.w);
+            *reinterpret_cast<float4*>(&s.z[t][r]) = F::of(pz[i]);
         }
-        if (tid < m) {
-            // backwards the decay applied before token t is that of token t + 1
-            const long long t = t0 + tid + (REV ? 1 : 0);
-            sa[tid] = t < tok0 + n ? decay_of(p.g[(size_t)t * p.H + h]) : 1.f;
+        if (warp == 0) {  // the gates' cumsum, in two floats
+            const float y = pg < -277.f ? -277.f : pg, hi = y * 1.44269502f;
+            float2 c = make_float2(hi, fmaf(y, 1.44269502f, -hi) + y * 1.92596299e-8f);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float2 u = make_float2(__shfl_up_sync(0xffffffffu, c.x, o), __shfl_up_sync(0xffffffffu, c.y, o));
+                if (lane >= o) c = add2(c, u);
+            }
+            const float2 last = make_float2(__shfl_sync(0xffffffffu, c.x, 31), __shfl_sync(0xffffffffu, c.y, 31));
+            const float a = start_decay(c), b = pair_decay(last, c);
+            s.g[lane] = c;
+            s.f[lane] = REV ? b : a;
+            s.h[lane] = REV ? a : b;
         }
         __syncthreads();
-        for (int i = 0; i < m; ++i) {
-            const int t = REV ? m - 1 - i : i;
-            const int pos = tile * TT + t;
-            const float a = sa[t];
+        if (it + 1 < tiles) fetch(REV ? tile - 1 : tile + 1);
+        {   // p[t][u] = D_tu (w_u . x_t), its diagonal apart; a thread: 2 x 4
+            const int t = 2 * (tid / 8), u = 4 * (tid % 8);
+            float a[2][4] = {};
+#pragma unroll 4
+            for (int c = 0; c < CD; c += 4) {
+                float4 xv[2], wv[4];
 #pragma unroll
-            for (int q = 0; q < RPT; ++q)
+                for (int i = 0; i < 2; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[t + i][c]);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) R[q][e] *= a;
-            if (REV && p.cross && ((pos + 1) % AC == 0 || pos + 1 == n)) {
-                // R is dS^T at the end of this chunk: dot it with the state there
-                const long long slot = slot0 + pos / AC;
-                float d = 0.f;
+                for (int j = 0; j < 4; ++j) wv[j] = *reinterpret_cast<const float4*>(&s.w[u + j][c]);
 #pragma unroll
-                for (int q = 0; q < RPT; ++q) {
-                    const int r = r0 + row[q];
-                    if (r >= p.RD) continue;
-                    const float* A = p.anchor + (((size_t)slot * p.H + h) * p.RD + r) * CD;
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) d += R[q][e] * A[4 * (sub + L * (e / 4)) + e % 4];
+                    for (int j = 0; j < 4; ++j)
+                        a[i][j] += xv[i].x * wv[j].x + xv[i].y * wv[j].y + xv[i].z * wv[j].z + xv[i].w * wv[j].w;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float4 v;
+                float* q = &v.x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int tt = t + i, uu = u + j;
+                    if (tt == uu) s.own[tt] = a[i][j];
+                    const bool in = REV ? uu > tt : uu < tt;
+                    q[j] = in ? a[i][j] * (REV ? pair_decay(s.g[uu], s.g[tt]) : pair_decay(s.g[tt], s.g[uu])) : 0.f;
                 }
-                d = warp_sum(d);
-                if (lane == 0) sred[warp] = d;
-                __syncthreads();
-                if (tid == 0) {
-                    float all = 0.f;
-                    for (int w = 0; w < NW; ++w) all += sred[w];
-                    p.cross[((size_t)blockIdx.y * chunk_slots(p.seq, AC) + slot) * p.H + h] = all;
-                }
-                __syncthreads();
+                *reinterpret_cast<float4*>(&s.p[t + i][u]) = v;
             }
-            float acc[RPT], wx = 0.f, w[16];
+        }
+        __syncthreads();
+        {   // out; a thread: 2 tokens x 4 rows
+            const int t = 2 * (tid / 8), r = 4 * (tid % 8);
+            float a[2][4] = {};
+#pragma unroll 2
+            for (int c = 0; c < CD; c += 4) {
+                float4 xv[2], rv[4];
 #pragma unroll
-            for (int q = 0; q < RPT; ++q) acc[q] = 0.f;
+                for (int i = 0; i < 2; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[t + i][c]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 x4 = *reinterpret_cast<const float4*>(&sx[t][4 * (sub + L * j)]);
-                const float4 w4 = *reinterpret_cast<const float4*>(&sw[t][4 * (sub + L * j)]);
-                const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-                w[4 * j] = w4.x; w[4 * j + 1] = w4.y; w[4 * j + 2] = w4.z; w[4 * j + 3] = w4.w;
+                for (int j = 0; j < 4; ++j) rv[j] = *reinterpret_cast<const float4*>(&s.r[c + j][r]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    wx += w[4 * j + e] * x[e];
+                for (int i = 0; i < 2; ++i) {
+                    const float q[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
 #pragma unroll
-                    for (int q = 0; q < RPT; ++q) acc[q] += R[q][4 * j + e] * x[e];
+                    for (int j = 0; j < 4; ++j) {
+                        a[i][0] += q[j] * rv[j].x; a[i][1] += q[j] * rv[j].y;
+                        a[i][2] += q[j] * rv[j].z; a[i][3] += q[j] * rv[j].w;
+                    }
                 }
             }
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) {
-                wx += __shfl_xor_sync(0xffffffffu, wx, o);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int q = 0; q < RPT; ++q) acc[q] += __shfl_xor_sync(0xffffffffu, acc[q], o);
-            }
-            float dot = 0.f;
+                for (int j = 0; j < 4; ++j) a[i][j] *= s.f[t + i];
+#pragma unroll 2
+            for (int u = 0; u < TT; u += 4) {
+                float4 pv[2], yv[4];
 #pragma unroll
-            for (int q = 0; q < RPT; ++q) {
-                const float y = sy[t][row[q]];
-                if (p.dots && sub == 0) dot += sz[t][row[q]] * acc[q];
-                if (sub == 0 && r0 + row[q] < p.RD) {
-                    const float v = p.c_out * (acc[q] + y * wx);
-                    const size_t at = ((size_t)(t0 + t) * p.H + h) * p.RD + r0 + row[q];
-                    if (p.out_f32) ((float*)p.out)[at] = v;
-                    else ((T*)p.out)[at] = from_f<T>(v);
+                for (int i = 0; i < 2; ++i) pv[i] = *reinterpret_cast<const float4*>(&s.p[t + i][u]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) yv[j] = *reinterpret_cast<const float4*>(&s.y[u + j][r]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float q[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        a[i][0] += q[j] * yv[j].x; a[i][1] += q[j] * yv[j].y;
+                        a[i][2] += q[j] * yv[j].z; a[i][3] += q[j] * yv[j].w;
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) R[q][e] += y * w[e];
             }
-            if (p.dots) {
-                dot = warp_sum(dot);
-                if (lane == 0) sdot[warp][t] = p.c_out * dot;
-            }
-            if (!REV && p.anchor && ((pos + 1) % AC == 0 || pos + 1 == n)) {
-                const long long slot = slot0 + pos / AC;
 #pragma unroll
-                for (int q = 0; q < RPT; ++q) {
-                    const int r = r0 + row[q];
-                    if (r >= p.RD) continue;
-                    float* A = p.anchor + (((size_t)slot * p.H + h) * p.RD + r) * CD;
+            for (int i = 0; i < 2; ++i) {
+                const int tt = t + i;
+                const size_t row = (size_t)(t0 + tt) * p.H + h;
+                if (has_z) {
+                    const float4 zv = *reinterpret_cast<const float4*>(&s.z[tt][r]);
+                    float d = zv.x * a[i][0] + zv.y * a[i][1] + zv.z * a[i][2] + zv.w * a[i][3];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) A[4 * (sub + L * (e / 4)) + e % 4] = R[q][e];
+                    for (int o = 4; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if (tid % 8 == 0 && tt < m) p.dots[(size_t)blockIdx.y * p.seq.rows * p.H + row] = p.c_out * d;
+                }
+                if (tt < m && r0 + r < p.RD) {
+                    const float4 yv = *reinterpret_cast<const float4*>(&s.y[tt][r]);
+                    const float q = s.own[tt];
+                    const float4 v = make_float4(p.c_out * (a[i][0] + q * yv.x), p.c_out * (a[i][1] + q * yv.y),
+                                                 p.c_out * (a[i][2] + q * yv.z), p.c_out * (a[i][3] + q * yv.w));
+                    if (p.out_f32) put4((float*)p.out + row * p.RD + r0 + r, v);
+                    else put4((T*)p.out + row * p.RD + r0 + r, v);
                 }
             }
         }
-        if (p.dots) {
-            __syncthreads();
-            if (tid < m) {
-                float d = 0.f;
-                for (int w = 0; w < NW; ++w) d += sdot[w][tid];
-                p.dots[((size_t)blockIdx.y * p.seq.rows + t0 + tid) * p.H + h] = d;
+        const int c0 = tid / 8 * NC, r = 4 * (tid % 8);  // this thread's columns and rows of R
+        if (REV && p.cross && border) {
+            // R is dS^T at the end of this chunk: dot it with the state there
+            float d = 0.f;
+            if (r0 + r < p.RD) {
+                const float* A = p.anchor + (((size_t)slot * p.H + h) * p.RD + r0 + r) * CD + c0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) d += s.r[c0 + c][r + j] * A[(size_t)j * CD + c];
+            }
+            d = warp_sum(d);
+            if (lane == 0) s.red[warp] = d;
+        }
+        __syncthreads();
+        if (REV && p.cross && border && tid == 0) {
+            float d = 0.f;
+            for (int w = 0; w < WT / 32; ++w) d += s.red[w];
+            p.cross[((size_t)blockIdx.y * chunk_slots(p.seq, AC) + slot) * p.H + h] = d;
+        }
+        {   // R; a thread: NC columns x 4 rows
+            const float total = start_decay(s.g[TT - 1]);
+            float a[NC][4];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(&s.r[c0 + c][r]);
+                a[c][0] = total * v.x; a[c][1] = total * v.y; a[c][2] = total * v.z; a[c][3] = total * v.w;
+            }
+#pragma unroll 4
+            for (int u = 0; u < TT; ++u) {
+                const float4 yv = *reinterpret_cast<const float4*>(&s.y[u][r]);
+                const float f = s.h[u], q[4] = {f * yv.x, f * yv.y, f * yv.z, f * yv.w};
+                float w[NC];
+                if constexpr (NC >= 4) {
+#pragma unroll
+                    for (int c = 0; c < NC; c += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(&s.w[u][c0 + c]);
+                        w[c] = v.x; w[c + 1] = v.y; w[c + 2] = v.z; w[c + 3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) w[c] = s.w[u][c0 + c];
+                }
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[c][j] += w[c] * q[j];
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                *reinterpret_cast<float4*>(&s.r[c0 + c][r]) = make_float4(a[c][0], a[c][1], a[c][2], a[c][3]);
+                if (!REV && p.anchor && border && r0 + r < p.RD) {
+                    float* A = p.anchor + (((size_t)slot * p.H + h) * p.RD + r0 + r) * CD + c0 + c;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) A[(size_t)j * CD] = a[c][j];
+                }
             }
         }
     }
     if (p.last) {
-        const float a = REV && n > 0 ? decay_of(p.g[(size_t)tok0 * p.H + h]) : 1.f;
-#pragma unroll
-        for (int q = 0; q < RPT; ++q) {
-            const int r = r0 + row[q];
-            if (r >= p.RD) continue;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                p.last[(sh * p.RD + r) * CD + 4 * (sub + L * (e / 4)) + e % 4] = a * R[q][e];
+        __syncthreads();
+        for (int e = tid; e < CD * RB; e += WT) {
+            const int r = e / CD, c = e % CD;
+            if (r0 + r < p.RD) p.last[(sh * p.RD + r0 + r) * CD + c] = s.r[c][r];
         }
     }
 }
@@ -294,8 +413,10 @@ template <typename T, bool REV>
 void launch_walk(const Walk& w, int CD, cudaStream_t st) {
     auto go = [&](auto cd, const char* name) {
         constexpr int C = decltype(cd)::value;
-        const dim3 grid((unsigned)((long long)w.seq.nseq * w.H), (w.RD + rows_per_cta<C>() - 1) / rows_per_cta<C>());
-        GDN_LAUNCH(name, st, (decay_walk_kernel<C, T, REV><<<grid, WT, 0, st>>>(w)));
+        const dim3 grid((unsigned)((long long)w.seq.nseq * w.H), (w.RD + RB - 1) / RB);
+        const int smem = sizeof(WalkSmem<C>);
+        cudaFuncSetAttribute(decay_walk_kernel<C, T, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        GDN_LAUNCH(name, st, (decay_walk_kernel<C, T, REV><<<grid, WT, smem, st>>>(w)));
     };
     const char* name = REV ? "decay_walk_rev" : "decay_walk";
     switch (CD) {
@@ -306,10 +427,7 @@ void launch_walk(const Walk& w, int CD, cudaStream_t st) {
     }
 }
 
-int row_blocks(int RD, int CD) {
-    const int rb = CD == 16 ? rows_per_cta<16>() : CD == 32 ? rows_per_cta<32>() : CD == 64 ? rows_per_cta<64>() : rows_per_cta<128>();
-    return (RD + rb - 1) / rb;
-}
+int row_blocks(int RD) { return (RD + RB - 1) / RB; }
 
 struct BwdLayout {
     size_t anchor, dotq, dotk, cross, dq, dk, end;
@@ -318,7 +436,7 @@ BwdLayout bwd_layout(const Problem& p) {
     BwdLayout l{};
     size_t o = kStatusBytes;
     auto take = [&](size_t bytes) { size_t r = o; o += (bytes + 255) & ~(size_t)255; return r; };
-    const size_t slots = (size_t)chunk_slots(p.seq, AC), nb = row_blocks(p.dk, p.dv), rows = p.seq.rows;
+    const size_t slots = (size_t)chunk_slots(p.seq, AC), nb = row_blocks(p.dk), rows = p.seq.rows;
     l.anchor = take(slots * p.H * p.dk * p.dv * 4);
     l.dotq = take(nb * rows * p.H * 4);
     l.dotk = take(nb * rows * p.H * 4);
@@ -373,7 +491,7 @@ void run_bwd(const Problem& p, const void* q, const void* k, const void* v, cons
     launch_walk<T, true>(u, p.dk, st);
     const unsigned chunks = spread(p, (p.seq.cu ? p.seq.rows : p.seq.len) / (4 * AC) + 1);
     GDN_LAUNCH("decay_gate", st, (decay_gate_kernel<<<dim3((unsigned)((long long)p.seq.nseq * p.H), chunks), 128, 0, st>>>(
-        p.seq, p.H, row_blocks(p.dk, p.dv), g, (const float*)(base + l.dotq), (const float*)(base + l.dotk),
+        p.seq, p.H, row_blocks(p.dk), g, (const float*)(base + l.dotq), (const float*)(base + l.dotk),
         (const float*)(base + l.cross), dg)));
     if (rep > 1) {
         launch_group_sum(p, p.dk, (const float*)(base + l.dq), dq, st);
