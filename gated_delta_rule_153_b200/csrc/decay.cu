@@ -28,11 +28,12 @@
 //     out_t = c (f_t R x_t + sum_s D_ts (w_s.x_t) y_s),   R <- e^{G_last} R + sum_s h_s y_s w_s^T
 // over s <= t, with f = e^G and h = e^{G_last - G} forwards, and over s >= t, with the two
 // exchanged, backwards.  All of it is small matrix products in fp32 on CUDA cores, from
-// shared memory in 2 x 4 and 4 x 4 register tiles; a CTA holds 32 rows of R, and the next
-// tile's values are on their way to registers meanwhile.  What bounds it is the issue of
-// fp32 FMAs and their shared-memory loads, one tile after the other along a chain.
+// shared memory in register tiles of up to 16 x 4; a CTA holds 64 rows of R.  What bounds it is the issue of
+// fp32 FMAs and, twice as long, the shared-memory loads that feed them (a 16-byte load
+// takes four cycles of the SM's 128 bytes per cycle, whatever its lanes share).
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -45,7 +46,7 @@ namespace {
 
 constexpr int TT = 32;          // tokens per tile
 constexpr int WT = 128;         // threads per CTA
-constexpr int RB = 32;          // rows of R per CTA
+constexpr int RB = 64;          // rows of R per CTA
 constexpr int AC = 64;          // tokens per chunk of the gate gradient
 
 // A gate of -inf (or one so low that e^g is zero in fp32) is a reset.
@@ -73,6 +74,10 @@ struct Walk {
     float* anchor;          // [slot][H][RD][CD] states at chunk ends: written forwards, read backwards
     float* dots;            // [row block][token][H]: sum over this CTA's rows of z . out' (own pair left out)
     float* cross;           // [row block][slot][H]: <S_e, dS_e> over this CTA's rows
+    // Few chains are cut into runs of `len` tiles: first what each run adds to a zero R
+    // and its decay (MAP), then all runs at once, each from what the ones before leave.
+    int runs, len;
+    float *runR, *runA;     // [chain][run][RD][CD] and [chain][run]
     unsigned int* status;
 };
 
@@ -105,14 +110,15 @@ struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in dif
     float f[TT], h[TT], own[TT], red[WT / 32];
 };
 
-template <int CD, typename T, bool REV>
+template <int CD, typename T, bool REV, bool MAP>
 __global__ void __launch_bounds__(WT)
 decay_walk_kernel(const Walk p) {
     extern __shared__ __align__(16) unsigned char raw[];
     WalkSmem<CD>& s = *reinterpret_cast<WalkSmem<CD>*>(raw);
     using F = Four<T>;
     constexpr int NX = TT * CD / 4 / WT > 0 ? TT * CD / 4 / WT : 1;  // groups of four per thread and tile
-    constexpr int NC = CD / 16;                                      // columns of R per thread
+    constexpr int NC = CD / 8;                                       // columns of R per thread
+    constexpr int NY = TT * RB / 4 / WT;
     const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long tok0;
@@ -123,58 +129,69 @@ decay_walk_kernel(const Walk p) {
     }
     const size_t sh = (size_t)seq * p.H + h;
     const long long slot0 = tok0 / AC + seq;
-    // R, column-major
+    const int tiles = (n + TT - 1) / TT;
+    const int i0 = blockIdx.z * p.len, i1 = min(tiles, i0 + p.len);  // this run, in the order of the walk
+    // the run that ends the chain (the first of an empty one) writes the last state
+    const bool ends = i1 == tiles && (blockIdx.z == 0 || i0 < tiles);
+    if (MAP ? i1 >= tiles : i0 >= tiles && !ends) return;
+    // R, column-major; from run 1 on with what the runs before this one leave
+#pragma unroll 8
     for (int e = tid; e < CD * RB; e += WT) {
         const int c = p.init_t ? e / RB : e % CD, r = p.init_t ? e % RB : e / CD, row = r0 + r;
-        s.r[c][r] = !p.init || row >= p.RD ? 0.f : p.init_t ? p.init[(sh * CD + c) * p.RD + row] : p.init[(sh * p.RD + row) * CD + c];
+        s.r[c][r] = MAP || !p.init || row >= p.RD ? 0.f : __ldg(p.init + (p.init_t ? (sh * CD + c) * p.RD + row : (sh * p.RD + row) * CD + c));
     }
-    const int tiles = (n + TT - 1) / TT;
-    typename F::Raw px[NX], pw[NX], py[2], pz[2];
-    float pg = 0.f;
-    const bool has_z = p.dots != nullptr;
-    auto fetch = [&](int tile) {
-        const int m = min(TT, n - tile * TT);
-        const long long t0 = tok0 + (long long)tile * TT;
-        const typename F::Raw zero{};
-#pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
-            const bool in = t < m;
-            px[i] = in ? *reinterpret_cast<const typename F::Raw*>((const T*)p.x.p + row_of(p.x, t0 + t, h) + c) : zero;
-            pw[i] = in ? *reinterpret_cast<const typename F::Raw*>((const T*)p.w.p + row_of(p.w, t0 + t, h) + c) : zero;
+    if (!MAP && blockIdx.z > 0) {
+        __syncthreads();
+        for (int q = 0; q < blockIdx.z; ++q) {
+            const float f = __ldg(p.runA + sh * p.runs + q), *from = p.runR + ((sh * p.runs + q) * p.RD + r0) * CD;
+#pragma unroll 8
+            for (int e = tid; e < CD * RB; e += WT) {
+                const int c = e % CD, r = e / CD;
+                if (r0 + r < p.RD) s.r[c][r] = f * s.r[c][r] + __ldg(from + (size_t)r * CD + c);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = 4 * (tid + WT * i), t = e / RB, r = e % RB;
-            const bool in = t < m && r0 + r < p.RD;
-            py[i] = in ? *reinterpret_cast<const typename F::Raw*>((const T*)p.y.p + row_of(p.y, t0 + t, h) + r0 + r) : zero;
-            pz[i] = in && has_z ? *reinterpret_cast<const typename F::Raw*>((const T*)p.z.p + row_of(p.z, t0 + t, h) + r0 + r) : zero;
-        }
-        if (warp == 0) pg = lane < m ? p.g[(size_t)(t0 + lane) * p.H + h] : 0.f;
-    };
-    if (tiles > 0) fetch(REV ? tiles - 1 : 0);
-    for (int it = 0; it < tiles; ++it) {
+    }
+    float all = 1.f;  // the decay of the run so far
+    const bool has_z = !MAP && p.dots != nullptr;
+    for (int it = i0; it < i1; ++it) {
         const int tile = REV ? tiles - 1 - it : it;
         const int m = min(TT, n - tile * TT);
         const long long t0 = tok0 + (long long)tile * TT;
         const int end = tile * TT + m;
         const bool border = end % AC == 0 || end == n;  // the tile ends a chunk
         const long long slot = slot0 + (end - 1) / AC;
-        __syncthreads();
-        if (TT * CD / 4 >= WT || tid < TT * CD / 4) {
+        const int r = 4 * (tid % 16);  // this thread's rows of R
+        const typename F::Raw zero{};
+        auto get = [&](const Operand& o, int t, int c, bool in) {
+            return in ? __ldg(reinterpret_cast<const typename F::Raw*>((const T*)o.p + row_of(o, t0 + t, h) + c)) : zero;
+        };
+        const float pg = warp == 0 && lane < m ? __ldg(p.g + (size_t)(t0 + lane) * p.H + h) : 0.f;
+        typename F::Raw vx[NX], vw[NX], vy[NY], vz[NY];  // all on their way before any is put down
 #pragma unroll
-            for (int i = 0; i < NX; ++i) {
-                const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
-                *reinterpret_cast<float4*>(&s.x[t][c]) = F::of(px[i]);
-                *reinterpret_cast<float4*>(&s.w[t][c]) = F::of(pw[i]);
-            }
+        for (int i = 0; i < NX; ++i) {
+            const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
+            if (!MAP) vx[i] = get(p.x, t, c, t < m);
+            vw[i] = get(p.w, t, c, t < m);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = 4 * (tid + WT * i), t = e / RB, r = e % RB;
-            const float4 v = F::of(py[i]);
+        for (int i = 0; i < NY; ++i) {
+            const int t = tid / 16 + 8 * i;
+            vy[i] = get(p.y, t, r0 + r, t < m && r0 + r < p.RD);
+            if (has_z) vz[i] = get(p.z, t, r0 + r, t < m && r0 + r < p.RD);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
+            if (!MAP) *reinterpret_cast<float4*>(&s.x[t][c]) = F::of(vx[i]);
+            *reinterpret_cast<float4*>(&s.w[t][c]) = F::of(vw[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NY; ++i) {
+            const int t = tid / 16 + 8 * i;
+            const float4 v = F::of(vy[i]);
             *reinterpret_cast<float4*>(&s.y[t][r]) = make_float4(p.c_y * v.x, p.c_y * v.y, p.c_y * v.z, p.c_y * v.w);
-            *reinterpret_cast<float4*>(&s.z[t][r]) = F::of(pz[i]);
+            if (has_z) *reinterpret_cast<float4*>(&s.z[t][r]) = F::of(vz[i]);
         }
         if (warp == 0) {  // the gates' cumsum, in two floats
             const float y = pg < -277.f ? -277.f : pg, hi = y * 1.44269502f;
@@ -191,102 +208,107 @@ decay_walk_kernel(const Walk p) {
             s.h[lane] = REV ? a : b;
         }
         __syncthreads();
-        if (it + 1 < tiles) fetch(REV ? tile - 1 : tile + 1);
-        {   // p[t][u] = D_tu (w_u . x_t), its diagonal apart; a thread: 2 x 4
-            const int t = 2 * (tid / 8), u = 4 * (tid % 8);
-            float a[2][4] = {};
-#pragma unroll 4
-            for (int c = 0; c < CD; c += 4) {
-                float4 xv[2], wv[4];
+        if constexpr (!MAP) {
+            {   // p[t][u] = D_tu (w_u . x_t) for t = tid / 8 + 16 i, u = tid % 8 + 8 j (neighbouring
+                // lanes read neighbouring rows, which are in different banks), its diagonal apart
+                const int ta = tid / 8, ua = tid % 8;
+                float a[2][4] = {};
+#pragma unroll 2
+                for (int c = 0; c < CD; c += 4) {
+                    float4 xv[2], wv[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[t + i][c]);
+                    for (int i = 0; i < 2; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[ta + 16 * i][c]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) wv[j] = *reinterpret_cast<const float4*>(&s.w[u + j][c]);
+                    for (int j = 0; j < 4; ++j) wv[j] = *reinterpret_cast<const float4*>(&s.w[ua + 8 * j][c]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            a[i][j] = fmaf(xv[i].x, wv[j].x, a[i][j]);
+                            a[i][j] = fmaf(xv[i].y, wv[j].y, a[i][j]);
+                            a[i][j] = fmaf(xv[i].z, wv[j].z, a[i][j]);
+                            a[i][j] = fmaf(xv[i].w, wv[j].w, a[i][j]);
+                        }
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        a[i][j] += xv[i].x * wv[j].x + xv[i].y * wv[j].y + xv[i].z * wv[j].z + xv[i].w * wv[j].w;
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = ta + 16 * i, u = ua + 8 * j;
+                        if (t == u) s.own[t] = a[i][j];
+                        const bool in = REV ? u > t : u < t;
+                        s.p[t][u] = in ? a[i][j] * (REV ? pair_decay(s.g[u], s.g[t]) : pair_decay(s.g[t], s.g[u])) : 0.f;
+                    }
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float4 v;
-                float* q = &v.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int tt = t + i, uu = u + j;
-                    if (tt == uu) s.own[tt] = a[i][j];
-                    const bool in = REV ? uu > tt : uu < tt;
-                    q[j] = in ? a[i][j] * (REV ? pair_decay(s.g[uu], s.g[tt]) : pair_decay(s.g[tt], s.g[uu])) : 0.f;
-                }
-                *reinterpret_cast<float4*>(&s.p[t + i][u]) = v;
-            }
-        }
-        __syncthreads();
-        {   // out; a thread: 2 tokens x 4 rows
-            const int t = 2 * (tid / 8), r = 4 * (tid % 8);
-            float a[2][4] = {};
+            __syncthreads();
+            // out: 4 tokens x 4 rows
+            const int tb = 4 * (tid / 16);
+            float a[4][4] = {};
+            auto add = [&](float (&o)[4], float q, const float4& v) {
+                o[0] = fmaf(q, v.x, o[0]);
+                o[1] = fmaf(q, v.y, o[1]);
+                o[2] = fmaf(q, v.z, o[2]);
+                o[3] = fmaf(q, v.w, o[3]);
+            };
 #pragma unroll 2
             for (int c = 0; c < CD; c += 4) {
-                float4 xv[2], rv[4];
+                float4 xv[4], rv[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[t + i][c]);
+                for (int i = 0; i < 4; ++i) {
+                    xv[i] = *reinterpret_cast<const float4*>(&s.x[tb + i][c]);
+                    rv[i] = *reinterpret_cast<const float4*>(&s.r[c + i][r]);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) rv[j] = *reinterpret_cast<const float4*>(&s.r[c + j][r]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float q[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[i][0] += q[j] * rv[j].x; a[i][1] += q[j] * rv[j].y;
-                        a[i][2] += q[j] * rv[j].z; a[i][3] += q[j] * rv[j].w;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    add(a[i], xv[i].x, rv[0]);
+                    add(a[i], xv[i].y, rv[1]);
+                    add(a[i], xv[i].z, rv[2]);
+                    add(a[i], xv[i].w, rv[3]);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i) {
+                const float f = s.f[tb + i];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[i][j] *= s.f[t + i];
+                for (int j = 0; j < 4; ++j) a[i][j] *= f;
+            }
 #pragma unroll 2
             for (int u = 0; u < TT; u += 4) {
-                float4 pv[2], yv[4];
+                float4 pv[4], yv[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) pv[i] = *reinterpret_cast<const float4*>(&s.p[t + i][u]);
+                for (int i = 0; i < 4; ++i) {
+                    pv[i] = *reinterpret_cast<const float4*>(&s.p[tb + i][u]);
+                    yv[i] = *reinterpret_cast<const float4*>(&s.y[u + i][r]);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) yv[j] = *reinterpret_cast<const float4*>(&s.y[u + j][r]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float q[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[i][0] += q[j] * yv[j].x; a[i][1] += q[j] * yv[j].y;
-                        a[i][2] += q[j] * yv[j].z; a[i][3] += q[j] * yv[j].w;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    add(a[i], pv[i].x, yv[0]);
+                    add(a[i], pv[i].y, yv[1]);
+                    add(a[i], pv[i].z, yv[2]);
+                    add(a[i], pv[i].w, yv[3]);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tt = t + i;
-                const size_t row = (size_t)(t0 + tt) * p.H + h;
+            for (int i = 0; i < 4; ++i) {
+                const int t = tb + i;
+                const size_t row = (size_t)(t0 + t) * p.H + h;
                 if (has_z) {
-                    const float4 zv = *reinterpret_cast<const float4*>(&s.z[tt][r]);
+                    const float4 zv = *reinterpret_cast<const float4*>(&s.z[t][r]);
                     float d = zv.x * a[i][0] + zv.y * a[i][1] + zv.z * a[i][2] + zv.w * a[i][3];
 #pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                    if (tid % 8 == 0 && tt < m) p.dots[(size_t)blockIdx.y * p.seq.rows * p.H + row] = p.c_out * d;
+                    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if (tid % 16 == 0 && t < m) p.dots[(size_t)blockIdx.y * p.seq.rows * p.H + row] = p.c_out * d;
                 }
-                if (tt < m && r0 + r < p.RD) {
-                    const float4 yv = *reinterpret_cast<const float4*>(&s.y[tt][r]);
-                    const float q = s.own[tt];
-                    const float4 v = make_float4(p.c_out * (a[i][0] + q * yv.x), p.c_out * (a[i][1] + q * yv.y),
-                                                 p.c_out * (a[i][2] + q * yv.z), p.c_out * (a[i][3] + q * yv.w));
+                if (t < m && r0 + r < p.RD) {
+                    add(a[i], s.own[t], *reinterpret_cast<const float4*>(&s.y[t][r]));
+                    const float4 v = make_float4(p.c_out * a[i][0], p.c_out * a[i][1], p.c_out * a[i][2], p.c_out * a[i][3]);
                     if (p.out_f32) put4((float*)p.out + row * p.RD + r0 + r, v);
                     else put4((T*)p.out + row * p.RD + r0 + r, v);
                 }
             }
         }
-        const int c0 = tid / 8 * NC, r = 4 * (tid % 8);  // this thread's columns and rows of R
-        if (REV && p.cross && border) {
+        const int c0 = tid / 16 * NC;  // this thread's columns of R
+        if (!MAP && REV && p.cross && border) {
             // R is dS^T at the end of this chunk: dot it with the state there
             float d = 0.f;
             if (r0 + r < p.RD) {
@@ -299,14 +321,15 @@ decay_walk_kernel(const Walk p) {
             d = warp_sum(d);
             if (lane == 0) s.red[warp] = d;
         }
-        __syncthreads();
-        if (REV && p.cross && border && tid == 0) {
+        if (!MAP) __syncthreads();
+        if (!MAP && REV && p.cross && border && tid == 0) {
             float d = 0.f;
             for (int w = 0; w < WT / 32; ++w) d += s.red[w];
             p.cross[((size_t)blockIdx.y * chunk_slots(p.seq, AC) + slot) * p.H + h] = d;
         }
+        const float total = start_decay(s.g[TT - 1]);
+        all *= total;
         {   // R; a thread: NC columns x 4 rows
-            const float total = start_decay(s.g[TT - 1]);
             float a[NC][4];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -331,12 +354,12 @@ decay_walk_kernel(const Walk p) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) a[c][j] += w[c] * q[j];
+                    for (int j = 0; j < 4; ++j) a[c][j] = fmaf(w[c], q[j], a[c][j]);
             }
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 *reinterpret_cast<float4*>(&s.r[c0 + c][r]) = make_float4(a[c][0], a[c][1], a[c][2], a[c][3]);
-                if (!REV && p.anchor && border && r0 + r < p.RD) {
+                if (!MAP && !REV && p.anchor && border && r0 + r < p.RD) {
                     float* A = p.anchor + (((size_t)slot * p.H + h) * p.RD + r0 + r) * CD + c0 + c;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) A[(size_t)j * CD] = a[c][j];
@@ -344,13 +367,15 @@ decay_walk_kernel(const Walk p) {
             }
         }
     }
-    if (p.last) {
+    float* const to = MAP ? p.runR + ((sh * p.runs + blockIdx.z) * p.RD) * CD : p.last && ends ? p.last + sh * p.RD * CD : nullptr;
+    if (to) {
         __syncthreads();
         for (int e = tid; e < CD * RB; e += WT) {
             const int r = e / CD, c = e % CD;
-            if (r0 + r < p.RD) p.last[(sh * p.RD + r0 + r) * CD + c] = s.r[c][r];
+            if (r0 + r < p.RD) to[(size_t)(r0 + r) * CD + c] = s.r[c][r];
         }
     }
+    if (MAP && tid == 0 && blockIdx.y == 0) p.runA[sh * p.runs + blockIdx.z] = all;
 }
 
 // dg of one chunk per warp: the suffix sums of q.dq' - k.dk' and the chunk end's <S, dS>.
@@ -413,10 +438,15 @@ template <typename T, bool REV>
 void launch_walk(const Walk& w, int CD, cudaStream_t st) {
     auto go = [&](auto cd, const char* name) {
         constexpr int C = decltype(cd)::value;
-        const dim3 grid((unsigned)((long long)w.seq.nseq * w.H), (w.RD + RB - 1) / RB);
+        dim3 grid((unsigned)((long long)w.seq.nseq * w.H), (w.RD + RB - 1) / RB, w.runs);
         const int smem = sizeof(WalkSmem<C>);
-        cudaFuncSetAttribute(decay_walk_kernel<C, T, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        GDN_LAUNCH(name, st, (decay_walk_kernel<C, T, REV><<<grid, WT, smem, st>>>(w)));
+        if (w.runs > 1) {
+            const dim3 maps(grid.x, grid.y, w.runs - 1);
+            cudaFuncSetAttribute(decay_walk_kernel<C, T, REV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            GDN_LAUNCH("decay_map", st, (decay_walk_kernel<C, T, REV, true><<<maps, WT, smem, st>>>(w)));
+        }
+        cudaFuncSetAttribute(decay_walk_kernel<C, T, REV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        GDN_LAUNCH(name, st, (decay_walk_kernel<C, T, REV, false><<<grid, WT, smem, st>>>(w)));
     };
     const char* name = REV ? "decay_walk_rev" : "decay_walk";
     switch (CD) {
@@ -429,14 +459,52 @@ void launch_walk(const Walk& w, int CD, cudaStream_t st) {
 
 int row_blocks(int RD) { return (RD + RB - 1) / RB; }
 
+// Runs per chain, of whole chunks: 1 when the chains fill the device.  Two launches
+// and the first one's pass over the states cost about four tiles, a tile of it a third
+// of one of the walk.
+struct Cut {
+    int runs, len;
+};
+Cut cut(const Problem& p, int RD) {
+    const int tiles = ((p.seq.cu ? p.seq.rows : p.seq.len) + TT - 1) / TT;
+    const long long ctas = (long long)p.seq.nseq * p.H * row_blocks(RD);
+    auto waves = [](long long n) { return (double)((n + 295) / 296); };  // two CTAs per SM
+    Cut best{1, std::max(tiles, 1)};
+    double cost = tiles * waves(ctas);
+    for (int r = 2; r <= 16; ++r) {
+        int len = (tiles + r - 1) / r;
+        len += len % 2;  // whole chunks of the gate gradient
+        const int runs = (tiles + len - 1) / len;
+        if (runs < 2) break;
+        const double c = len * (waves(ctas * runs) + waves(ctas * (runs - 1)) / 3) + 4;
+        if (c < 0.9 * cost) {
+            cost = c;
+            best = Cut{runs, len};
+        }
+    }
+    return best;
+}
+size_t runs_bytes(const Problem& p, const Cut& c) {
+    if (c.runs == 1) return 0;
+    const size_t chains = (size_t)p.seq.nseq * p.H;
+    return chains * c.runs * (size_t)p.dk * p.dv * 4 + ((chains * c.runs * 4 + 255) & ~(size_t)255);
+}
+void set_runs(Walk& w, const Problem& p, const Cut& c, void* at) {
+    w.runs = c.runs;
+    w.len = c.len;
+    w.runR = (float*)at;
+    w.runA = w.runR + (size_t)p.seq.nseq * p.H * c.runs * p.dk * p.dv;
+}
+
 struct BwdLayout {
-    size_t anchor, dotq, dotk, cross, dq, dk, end;
+    size_t runs, anchor, dotq, dotk, cross, dq, dk, end;
 };
 BwdLayout bwd_layout(const Problem& p) {
     BwdLayout l{};
     size_t o = kStatusBytes;
     auto take = [&](size_t bytes) { size_t r = o; o += (bytes + 255) & ~(size_t)255; return r; };
     const size_t slots = (size_t)chunk_slots(p.seq, AC), nb = row_blocks(p.dk), rows = p.seq.rows;
+    l.runs = take(std::max(runs_bytes(p, cut(p, p.dk)), runs_bytes(p, cut(p, p.dv))));
     l.anchor = take(slots * p.H * p.dk * p.dv * 4);
     l.dotq = take(nb * rows * p.H * 4);
     l.dotk = take(nb * rows * p.H * 4);
@@ -468,6 +536,7 @@ void run_bwd(const Problem& p, const void* q, const void* k, const void* v, cons
     w.g = g; w.seq = p.seq; w.H = p.H; w.status = (unsigned int*)ws;
     w.anchor = (float*)(base + l.anchor);
     w.out_f32 = rep > 1;
+    set_runs(w, p, cut(p, p.dk), base + l.runs);
     // dq, with the states at the chunk ends kept
     w.x = od; w.w = ov; w.y = ok; w.z = oq;
     w.init = h0; w.init_t = true; w.c_out = p.scale; w.c_y = 1.f; w.RD = p.dk;
@@ -487,6 +556,7 @@ void run_bwd(const Problem& p, const void* q, const void* k, const void* v, cons
     u.x = ok; u.w = oq; u.y = od;
     u.init = dhT; u.c_out = 1.f; u.c_y = p.scale; u.RD = p.dv;
     u.last = dh0;
+    set_runs(u, p, cut(p, p.dv), base + l.runs);
     u.out = dv;
     launch_walk<T, true>(u, p.dk, st);
     const unsigned chunks = spread(p, (p.seq.cu ? p.seq.rows : p.seq.len) / (4 * AC) + 1);
@@ -501,12 +571,13 @@ void run_bwd(const Problem& p, const void* q, const void* k, const void* v, cons
 
 template <typename T>
 void run_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
-             void* o, float* hT, unsigned int* status, cudaStream_t st) {
+             void* o, float* hT, void* ws, cudaStream_t st) {
     const int rep = p.H / p.Hk;
     Walk w{};
-    w.g = g; w.seq = p.seq; w.H = p.H; w.status = status;
+    w.g = g; w.seq = p.seq; w.H = p.H; w.status = (unsigned int*)ws;
     w.x = Operand{q, p.Hk, rep, p.dk}; w.w = Operand{k, p.Hk, rep, p.dk}; w.y = Operand{v, p.H, 1, p.dv};
     w.init = h0; w.last = hT; w.out = o; w.c_out = p.scale; w.c_y = 1.f; w.RD = p.dv;
+    set_runs(w, p, cut(p, p.dv), (char*)ws + kStatusBytes);
     launch_walk<T, false>(w, p.dk, st);
 }
 
@@ -593,12 +664,14 @@ void launch_group_sum(const Problem& p, int d, const float* part, void* out, cud
         GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<<<grid, 256, 0, st>>>(p.seq, p.Hk, p.H / p.Hk, d, part, (float*)out)));
 }
 
+size_t simt_fwd_workspace(const Problem& p) { return kStatusBytes + runs_bytes(p, cut(p, p.dv)); }
+
 size_t simt_bwd_workspace(const Problem& p) { return bwd_layout(p).end; }
 
 void launch_simt_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g,
-                     const float* h0, void* o, float* hT, unsigned int* status, cudaStream_t st) {
-    if (p.dtype == GDN_BF16) run_fwd<__nv_bfloat16>(p, q, k, v, g, h0, o, hT, status, st);
-    else run_fwd<float>(p, q, k, v, g, h0, o, hT, status, st);
+                     const float* h0, void* o, float* hT, void* ws, cudaStream_t st) {
+    if (p.dtype == GDN_BF16) run_fwd<__nv_bfloat16>(p, q, k, v, g, h0, o, hT, ws, st);
+    else run_fwd<float>(p, q, k, v, g, h0, o, hT, ws, st);
 }
 
 void launch_simt_bwd(const Problem& p, const void* q, const void* k, const void* v, const float* g,

@@ -46,9 +46,10 @@ __device__ __forceinline__ bool span_of(const Seqs& q, int s, long long& tok0, i
 #endif
 
 // fp32 arithmetic on CUDA cores, any supported dims (decay.cu).
+size_t simt_fwd_workspace(const Problem& p);
 size_t simt_bwd_workspace(const Problem& p);
 void launch_simt_fwd(const Problem& p, const void* q, const void* k, const void* v, const float* g,
-                     const float* h0, void* o, float* hT, unsigned int* status, cudaStream_t st);
+                     const float* h0, void* o, float* hT, void* ws, cudaStream_t st);
 void launch_decay_step(int N, int H, int Hk, int dk, int dv, gdn_dtype dtype, float scale, const void* q,
                        const void* k, const void* v, const float* g, float* state, void* o,
                        cudaStream_t st);

@@ -46,7 +46,7 @@ gdn_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
 
 gdn_status launched() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
-size_t fwd_need(const Problem& p) { return tc_supported(p) ? tc_fwd_workspace(p) : kStatusBytes; }
+size_t fwd_need(const Problem& p) { return tc_supported(p) ? tc_fwd_workspace(p) : simt_fwd_workspace(p); }
 size_t bwd_need(const Problem& p) { return tc_supported(p) ? tc_bwd_workspace(p) : simt_bwd_workspace(p); }
 
 // The workspace queries take no offsets: any non-null pointer stands for them.
@@ -86,7 +86,7 @@ gdn_status gdn_decay_fwd(const gdn_decay_dims* d, const int* cu_seqlens, int nse
     if (tc_supported(p)) {
         if (!launch_tc_fwd(p, q, k, v, g, h0, o, hT, ws, st)) return GDN_ERR_CUDA;
     } else {
-        launch_simt_fwd(p, q, k, v, g, h0, o, hT, (unsigned int*)ws, st);
+        launch_simt_fwd(p, q, k, v, g, h0, o, hT, ws, st);
     }
     return launched();
 }
