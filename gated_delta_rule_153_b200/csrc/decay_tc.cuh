@@ -14,6 +14,23 @@ namespace decay {
 
 constexpr int CT = 128;  // tokens per chunk of the tensor-core kernels
 
+// Two fp32 operations in one instruction.
+GDN_DEV void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+GDN_DEV void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+GDN_DEV void add2f(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // 2^x; results below 2^-126 are zero.
 GDN_DEV float ex2(float x) {
     float y;
@@ -82,27 +99,22 @@ GDN_DEV void split_bf16(uint32_t (&t)[TERMS], float x, float y) {
         t[i] = pack_bf16(x, y);
         if (i + 1 < TERMS) {
             const float2 f = unpack_bf16(t[i]);
-            x -= f.x;
-            y -= f.y;
+            add2f(x, y, x, y, -f.x, -f.y);
         }
     }
 }
 
-// A bounded wait in few instructions: these kernels run five roles' loops side by
-// side, and their footprint in the instruction cache counts.  Each try is given
-// a microsecond, a million of them are a second at most.  The caller reports a
-// wait that gave up once, after its loop.
+// A bounded wait (1 s) in few instructions: these kernels run five roles' loops side by
+// side, and their footprint in the instruction cache counts.  The caller reports a wait
+// that gave up once, after its loop.
 GDN_DEV bool wait_for(uint64_t* bar, uint32_t parity) {
-    uint32_t ok, n = 0;
-    const uint32_t at = smem_u32(bar);
-    do {
-        asm volatile(
-            "{\n .reg .pred p;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok) : "r"(at), "r"(parity), "r"(1000) : "memory");
-    } while (!ok && ++n < 1000000);
-    return ok != 0;
+    uint64_t t0 = 0;
+    while (!mbar_try(bar, parity)) {
+        const uint64_t t = globaltimer();
+        if (!t0) t0 = t;
+        if (t - t0 > kWaitNs) return false;
+    }
+    return true;
 }
 
 // One lane of a converged warp, chosen so that the compiler knows the branch to

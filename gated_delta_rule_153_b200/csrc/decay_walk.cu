@@ -23,8 +23,8 @@
 // would stay in the state, which is kept and returned in fp32.
 //
 // Roles: warps 0-7 turn A into P and combine O (thread = query token); warps 8-15
-// split V and own the state (thread = key channel, half of the value channels);
-// warp 16 issues the loads, warp 17 the products, warp 18 forms the gates' cumsum.
+// own the state (thread = key channel, half of the value channels); warp 16 issues
+// the loads, warp 17 the products, warp 18 forms the gates' cumsum, the last four split V.
 // K and V tiles go through a two-stage ring; Q, which A and X are done with early
 // in a chunk, has one place.
 //
@@ -46,8 +46,12 @@ namespace {
 
 constexpr int NB = 64;               // value channels per CTA
 constexpr int PANEL = CT * 128;      // bytes of a 128-row, 64-channel tile
-constexpr int kEpi = 8, kState = 8;  // warps of the two epilogue groups
-constexpr int kThreads = 32 * (kEpi + kState + 3);
+constexpr int kEpi = 8, kState = 8;  // warps that make P and O, and that own the state
+// Warps that split V: four of their own in MODE 0, else the eight that P and O leave idle.
+template <int MODE>
+constexpr int kSplit = MODE == 0 ? 4 : kEpi;
+template <int MODE>
+constexpr int kThreads = 32 * (kEpi + kState + 3 + (MODE == 0 ? 4 : MODE == 2 ? 1 : 0));
 constexpr int NST = 2;
 
 template <int DK>
@@ -59,9 +63,9 @@ struct alignas(1024) Smem {
     unsigned char Vt[3][PANEL];  // decayed V, three bf16 terms
     unsigned char S[DK * 128];   // the entering state in bf16, [key channel][64 value channels]
     Gates gate[NST];
-    float col[kEpi][96];         // per warp of P: decays from token j to the end of the block before its own
+    float col[kEpi][CT];         // per warp of P: the column factors of its decays
     uint64_t full[NST], gfull[NST], gfree[NST];
-    uint64_t s_free, q_full, a_done, p_ready, vt_ready, n_done, s_ready, x_done, o_done, o_free, drain;
+    uint64_t img_ready, img_free, q_full, a_done, p_ready, vt_ready, n_done, s_ready, x_done, o_done, o_free, drain;
     uint32_t tmem;
 };
 
@@ -86,7 +90,7 @@ struct Params {
 constexpr uint32_t TA = 0, TP = 128, TX = 192, TY = 256, TN = 320, kCols = 512;
 
 template <int DK, int MODE, bool REV>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<MODE>, 1)
 decay_tc_walk_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem<DK>& s = *reinterpret_cast<Smem<DK>*>(align1k(raw));
@@ -115,13 +119,14 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.gfull[i], 32);
-            mbar_init(&s.gfree[i], MODE == 0 ? kEpi + kState : kState);
+            mbar_init(&s.gfree[i], (MODE == 0 ? kEpi : 0) + kState + kSplit<MODE>);
         }
         mbar_init(&s.q_full, 1);
-        mbar_init(&s.s_free, 1);
+        mbar_init(&s.img_ready, kState);
+        mbar_init(&s.img_free, 1);
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
-        mbar_init(&s.vt_ready, kState);
+        mbar_init(&s.vt_ready, kSplit<MODE>);
         mbar_init(&s.n_done, 1);
         mbar_init(&s.s_ready, kState);
         mbar_init(&s.x_done, 1);
@@ -138,6 +143,52 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     int done = 0;  // chunks this warp went through: fewer than nc after a wait that gave up
     const uint32_t trow = tm + ((uint32_t)(32 * (warp & 3)) << 16);
 
+    // ---- V of each chunk, decayed, in three bf16 terms: thread = token, a share of the channels ----
+    auto split = [&](int w) {
+        constexpr int PIECES = 32 / kSplit<MODE>;  // 16-byte pieces of this thread's row of V
+        const int r = 32 * (w & 3) + lane, part = w >> 2;
+        for (int c = 0; c < nc; ++c) {
+            const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
+            if (!warp_wait(&s.gfull[st], (c / NST) & 1)) break;
+            // forwards what token r adds decays to the chunk's end, backwards from its start
+            const float2 ge = s.gate[st].G[CT - 1], gr = s.gate[st].G[r];
+            const float wt = r < L ? (REV ? p.scale * start_decay(gr) : pair_decay(ge, gr)) : 0.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.gfree[st]);
+            if (!warp_wait(&s.full[st], (c / NST) & 1)) break;
+            if (c > 0 && !warp_wait(&s.n_done, (c - 1) & 1)) break;  // N(c-1) is done with the terms before
+#pragma unroll 1
+            for (int q = 0; q < PIECES; ++q) {
+                const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q));
+                uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
+                if (r >= L) {  // rows past the chunk's tokens become zero, in V and K too
+                    v = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
+                }
+                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                uint32_t t[4][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 f = unpack_bf16(in[e]);
+                    mul2(f.x, f.y, f.x, f.y, wt, wt);
+                    split_bf16<3>(t[e], f.x, f.y);
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
+            }
+            if (r >= L) {
+#pragma unroll 1
+                for (int q = part; q < DK / 8; q += kSplit<MODE> / 4)
+                    *reinterpret_cast<uint4*>(s.st[st].K[q >> 3] + 2 * swz<64>(r, 8 * (q & 7))) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.vt_ready);
+            ++done;
+        }
+    };
+
     if (warp < kEpi) {
         if constexpr (MODE == 0) {
             // ---- P, then O: thread = query token --------------------------------
@@ -147,51 +198,62 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
                 const Gates& G = s.gate[st];
                 if (!warp_wait(&s.gfull[st], (c / NST) & 1)) break;
-                // decays between blocks factor at the end of the block before this row's: both
-                // factors are at most 1.  Those of the columns are shared by the warp's rows.
-                const float2 gi = G.G[i];
-                float rf = 0.f, *const col = s.col[warp];
+                // Decays factor about a base token b, e^{G_i - G_b} e^{G_b - G_j}: for the blocks
+                // before this row's the end of the block before, so that both factors are at
+                // most 1; for its own block the middle, where they stay within fp32 unless
+                // half the block decays by more than 2^100.  The column factors are shared by
+                // the warp's rows.
+                const float2 gi = G.G[i], gm = G.G[32 * blk + 15];
+                const float first = diff2(G.G[32 * blk], gm), last_ = diff2(gm, G.G[32 * blk + 31]);
+                const bool wide = !(first < 100.f && last_ < 100.f);  // the same for the whole warp
+                float* const col = s.col[warp];
+                float rf = 0.f;
+                __syncwarp();
                 if (blk) {
                     const float2 gb = G.G[32 * blk - 1];
                     rf = p.scale * pair_decay(gi, gb);
-                    __syncwarp();
 #pragma unroll 1
                     for (int j = lane; j < 32 * blk; j += 32) col[j] = pair_decay(gb, G.G[j]);
-                    __syncwarp();
                 }
+                const float rd = p.scale * ex2(diff2(gi, gm));
+                col[32 * blk + lane] = ex2(diff2(gm, gi));
+                __syncwarp();
                 const float ein = p.scale * start_decay(gi);
                 const uint32_t tp = trow + TP;
                 if (!warp_wait(&s.a_done, c & 1)) break;
                 tc5::fence_after();
 #pragma unroll 1
-                for (int J = half; J < 2 * blk; J += 2) {  // the blocks before this row's
+                for (int J = half; J < 2 * blk + 2; J += 2) {  // 16 columns
                     float a[16];
                     uint32_t pk[8];
                     tc5::ld16(a, trow + TA + 16 * J);
                     tc5::wait_ld();
+                    const bool diag = J >= 2 * blk;
+                    const float f = diag ? rd : rf;
+                    if (diag && wide) {  // pair by pair
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float d = p.scale * pair_decay(gi, G.G[16 * J + q]);
+                            a[q] = 16 * J + q <= i ? a[q] * d : 0.f;
+                        }
+                    } else {
                     const float4* cf = reinterpret_cast<const float4*>(col + 16 * J);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float4 f = cf[q];
-                        pk[2 * q] = pack_bf16(a[4 * q] * (rf * f.x), a[4 * q + 1] * (rf * f.y));
-                        pk[2 * q + 1] = pack_bf16(a[4 * q + 2] * (rf * f.z), a[4 * q + 3] * (rf * f.w));
+                        float4 w = cf[q];
+                        mul2(w.x, w.y, w.x, w.y, f, f);
+                        mul2(w.z, w.w, w.z, w.w, f, f);
+                        mul2(a[4 * q], a[4 * q + 1], a[4 * q], a[4 * q + 1], w.x, w.y);
+                        mul2(a[4 * q + 2], a[4 * q + 3], a[4 * q + 2], a[4 * q + 3], w.z, w.w);
                     }
-                    tc5::st8(tp + 8 * J, pk);
-                }
-                {   // the diagonal block
-                    const int j0 = 32 * blk + 16 * half;
-                    float a[16];
-                    uint32_t pk[8];
-                    tc5::ld16(a, trow + TA + j0);
-                    tc5::wait_ld();
+                    if (diag) {
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float d = p.scale * pair_decay(gi, G.G[j0 + q]);
-                        a[q] = j0 + q <= i ? a[q] * d : 0.f;
+                        for (int q = 0; q < 16; ++q) a[q] = 16 * J + q <= i ? a[q] : 0.f;
+                    }
                     }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) pk[q] = pack_bf16(a[2 * q], a[2 * q + 1]);
-                    tc5::st8(tp + j0 / 2, pk);
+                    tc5::st8(tp + 8 * J, pk);
                 }
                 {
                     const uint32_t zero[8] = {};
@@ -227,8 +289,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     }
                     uint32_t w[8], mine[4], got[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = pack_bf16(ein * x[2 * e] + y[2 * e], ein * x[2 * e + 1] + y[2 * e + 1]);
+                    for (int e = 0; e < 8; ++e) {
+                        fma2(x[2 * e], x[2 * e + 1], ein, ein, x[2 * e], x[2 * e + 1], y[2 * e], y[2 * e + 1]);
+                        w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         mine[e] = odd ? w[4 + e] : w[e];
@@ -243,23 +307,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 ++done;
             }
         }
-        if constexpr (MODE == 2) {
-            // ---- the states' images to memory ------------------------------------
-            if (tid == 0) {
-                for (int c = 0; c < nc; ++c) {
-                    if (!wait_for(&s.s_ready, c & 1)) break;
-                    unsigned char* to = reinterpret_cast<unsigned char*>(p.image) +
-                                        ((slot0 + chunk_of(c)) * p.H + h) * (2 * gridDim.y * (size_t)(DK * 128)) + vb * (size_t)(DK * 128);
-                    bulk_s2g(to, s.Q, DK * 128);
-                    bulk_s2g(to + gridDim.y * (size_t)(DK * 128), (unsigned char*)s.Q + DK * 128, DK * 128);
-                    bulk_commit();
-                    bulk_wait_read<0>();
-                    mbar_arrive(&s.s_free);
-                    ++done;
-                }
-                bulk_wait<0>();
-            }
-        }
+        if constexpr (MODE != 0) split(warp);
     } else if (warp < kEpi + kState) {
         // ---- the state: thread = key channel r, value channels 32 half .. +31 ------
         // (and, to split V, thread = token r of the same channels)
@@ -287,7 +335,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 tc5::wait_ld();
                 const float a = x ? 1.f : total;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[e] = a * S[e] + N[e];
+                for (int e = 0; e < 32; e += 2) fma2(S[e], S[e + 1], a, a, S[e], S[e + 1], N[e], N[e + 1]);
             }
             tc5::fence_before();
         };
@@ -307,19 +355,25 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                                        pack_bf16(S[8 * q + 4], S[8 * q + 5]), pack_bf16(S[8 * q + 6], S[8 * q + 7]));
                 }
                 fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.s_ready);
             }
+            // N(c-1) is in the registers (and, MODE 0, S where X finds it)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.s_ready);
+            if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
+            total = start_decay(s.gate[st].G[CT - 1]);
+            decay *= total;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.gfree[st]);
             if constexpr (MODE == 2) {
-                const size_t img = (((slot0 + chunk_of(c)) * p.H + h) * 2 * gridDim.y + vb) * slab;
                 if (REV) {
                     // <S, dS> of the chunk: this thread's part of both
+                    const size_t img = (((slot0 + chunk_of(c)) * p.H + h) * 2 * gridDim.y + vb) * slab;
                     float d = 0.f;
                     if (own) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const uint4 a = *reinterpret_cast<const uint4*>(p.other + img + swz<64>(r, 32 * half + 8 * q));
-                            const uint4 b = *reinterpret_cast<const uint4*>(p.other + img + gridDim.y * slab + swz<64>(r, 32 * half + 8 * q));
+                            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.other + img + swz<64>(r, 32 * half + 8 * q)));
+                            const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.other + img + gridDim.y * slab + swz<64>(r, 32 * half + 8 * q)));
                             const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -329,9 +383,9 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                         }
                     }
                     d = warp_sum(d);
-                    if (lane == 0) s.col[warp - kEpi][c & 1] = d;
+                    if (lane == 0) s.col[warp - kEpi][c & 1] = total * d;
                 }
-                if (c > 0 && !(ok = warp_wait(&s.s_free, (c - 1) & 1))) break;
+                if (c > 0 && !(ok = warp_wait(&s.img_free, (c - 1) & 1))) break;
                 if (own) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -345,54 +399,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.s_ready);
-            }
-            if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
-            const float2 ge = s.gate[st].G[CT - 1];
-            // forwards what token r adds decays to the chunk's end, backwards from its start
-            const float2 gr = s.gate[st].G[r];
-            const float wt = r < L ? (REV ? p.scale * start_decay(gr) : pair_decay(ge, gr)) : 0.f;
-            total = start_decay(ge);
-            decay *= total;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.gfree[st]);
-            if (!(ok = warp_wait(&s.full[st], (c / NST) & 1))) break;
-            // decayed V in three terms; rows past the chunk's tokens become zero in V and K too
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t at = 2 * swz<64>(r, 32 * half + 8 * q);
-                uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
-                if (r >= L) {
-                    v = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
-                }
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t t[4][3];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack_bf16(in[e]);
-                    split_bf16<3>(t[e], wt * f.x, wt * f.y);
-                }
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
-            }
-            if (r >= L) {
-#pragma unroll 1
-                for (int q = 0; q < DK / 16; ++q) {
-                    const int ch = half * (DK / 16) + q;  // 16-byte piece of the K row
-                    *reinterpret_cast<uint4*>(s.st[st].K[ch >> 3] + 2 * swz<64>(r, 8 * (ch & 7))) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.vt_ready);
-            if (MODE == 2 && REV && warp == kEpi) {
-                // every state warp has left its part before its s_ready, which this one's wait follows
-                if (!(ok = warp_wait(&s.s_ready, c & 1))) break;
-                float d = lane < kState ? s.col[lane][c & 1] : 0.f;
-                d = warp_sum(d);
-                if (lane == 0) p.cross[(vb * (size_t)chunk_slots(p.seq, CT) + slot0 + chunk_of(c)) * p.H + h] = total * d;
+                if (lane == 0) mbar_arrive(&s.img_ready);
             }
             ++done;
         }
@@ -487,6 +494,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
             }
             // N(c); with 64 key channels lanes 64-127 read the V tile behind K and are ignored
+            if (MODE != 0 && !warp_wait(&s.s_ready, c & 1)) break;
             if (!warp_wait(&s.vt_ready, c & 1)) break;
             tc5::fence_after();
             if (elect_one()) {
@@ -509,6 +517,30 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         }
         if (elect_one()) tc5::commit(&s.drain);  // no product may be in flight when the CTA ends
         warp_wait(&s.drain, 0);
+    } else if (MODE == 0 && warp > kEpi + kState + 2) {
+        split(warp - (kEpi + kState + 3));
+    } else if (MODE == 2 && warp > kEpi + kState + 2) {
+        // ---- the states' images to memory, and the sums of <S, dS> -------------------
+        for (int c = 0; c < nc; ++c) {
+            if (!warp_wait(&s.img_ready, c & 1)) break;
+            if (REV) {
+                float d = lane < kState ? s.col[lane][c & 1] : 0.f;
+                d = warp_sum(d);
+                if (lane == 0) p.cross[(vb * (size_t)chunk_slots(p.seq, CT) + slot0 + chunk_of(c)) * p.H + h] = d;
+            }
+            if (lane == 0) {
+                unsigned char* to = reinterpret_cast<unsigned char*>(p.image) +
+                                    ((slot0 + chunk_of(c)) * p.H + h) * (2 * gridDim.y * (size_t)(DK * 128)) + vb * (size_t)(DK * 128);
+                bulk_s2g(to, s.Q, DK * 128);
+                bulk_s2g(to + gridDim.y * (size_t)(DK * 128), (unsigned char*)s.Q + DK * 128, DK * 128);
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&s.img_free);
+            }
+            __syncwarp();
+            ++done;
+        }
+        if (lane == 0) bulk_wait<0>();
     } else {
         // ---- gates: the next chunk's values are on their way while this one's wait ----
         float x[4];
@@ -525,7 +557,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             ++done;
         }
     }
-    if (lane == 0 && done < nc && (MODE == 0 || warp >= kEpi || (MODE == 2 && warp == 0))) atomicOr(p.status, 1u);
+    if (lane == 0 && done < nc) atomicOr(p.status, 1u);
     tc5::fence_before();
     __syncthreads();
     if (warp == kEpi + kState + 1) {
@@ -567,7 +599,7 @@ void launch(const Params& a, int dk, dim3 grid, cudaStream_t st) {
         const int smem = sizeof(Smem<DK>) + 1024;
         cudaFuncSetAttribute(decay_tc_walk_kernel<DK, MODE, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         GDN_LAUNCH(MODE == 0 ? "decay_tc_walk" : MODE == 1 ? "decay_tc_map" : "decay_tc_states", st,
-                   (decay_tc_walk_kernel<DK, MODE, REV><<<grid, kThreads, smem, st>>>(a)));
+                   (decay_tc_walk_kernel<DK, MODE, REV><<<grid, kThreads<MODE>, smem, st>>>(a)));
     };
     if (dk == 64) go(std::integral_constant<int, 64>{});
     else go(std::integral_constant<int, 128>{});
