@@ -38,16 +38,25 @@ template <int DK, int DV>
 struct alignas(1024) Smem {
     unsigned char Q[DK / 64][PANEL], K[DK / 64][PANEL], V[DV / 64][PANEL], Y[DV / 64][PANEL];  // Y = dO
     unsigned char S[2][DV / 64][DK * 128];  // the two terms of S, then of dS
+    // Results on their way out: dq, then dk and dv.  At the largest dims they go by way of S: dq
+    // through its second term, between its last use and the arrival of dS's, dk and dv
+    // through both, between dS and the next chunk's S, which only the second
+    // products of that chunk need.
+    static constexpr bool kOwnOut = DK + DV < 256;
+    unsigned char O[kOwnOut ? (DK + DV) / 64 : 1][kOwnOut ? PANEL : 16];
+    GDN_DEV unsigned char* out_q() { return kOwnOut ? O[0] : S[1][0]; }
+    GDN_DEV unsigned char* out_k() { return kOwnOut ? O[0] : S[0][0]; }
+    GDN_DEV unsigned char* out_v() { return out_k() + DK / 64 * PANEL; }
     Gates gate[2];
     float r[2][4][CT], c[2][4][CT], a[2][4][CT], b[2][4][CT];  // [chunk parity][column quarter][token]
     float col[kEpi][2][16];
-    uint64_t t_full, kv_full, s_full, gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, e3r, e3, o_done, e4, gfree[2],
+    uint64_t t_full, kv_full, s_full[2], gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, e3r, e3, o_done, e4, gfree[2],
         drain;
     uint32_t tmem;
 };
 
 struct Params {
-    CUtensorMap qmap, kmap, vmap, ymap;
+    CUtensorMap qmap, kmap, vmap, ymap, dqmap, dkmap, dvmap;
     Seqs seq;
     int H, Hk, rep;
     float scale;
@@ -116,7 +125,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long slots = chunk_slots(p.seq, CT), units = slots * p.H;
     if (tid == 0) {
-        for (uint64_t* b : {&s.t_full, &s.kv_full, &s.s_full, &s.a_done, &s.x_done, &s.q_done, &s.a2_done, &s.x2_done, &s.o_done, &s.drain})
+        for (uint64_t* b : {&s.t_full, &s.kv_full, &s.s_full[0], &s.s_full[1], &s.a_done, &s.x_done, &s.q_done, &s.a2_done, &s.x2_done, &s.o_done, &s.drain})
             mbar_init(b, 1);
         for (uint64_t* b : {&s.zeroed, &s.e1, &s.e2, &s.e3r, &s.e3, &s.e4}) mbar_init(b, kEpi);
         for (int i = 0; i < 2; ++i) {
@@ -248,30 +257,40 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             if (lane == 0) mbar_arrive(&s.e1);
             const bool up = (i & ~1) < L, dn = (i | 1) < L;
             const size_t row = (size_t)(ch.tok + i) * p.H + h, row0 = (size_t)(ch.tok + (i & ~1)) * p.H + h;
-            auto put = [&](void* out, uint32_t col, int n, int d) {  // a quarter of n columns of this lane's row
+            // A quarter of this lane's row of a result, n of its d columns: to the tile the
+            // controller's TMA store takes (to == null: straight to memory, in fp32 for
+            // the parts of shared key heads, or row by row for a short chunk)
+            auto put = [&](unsigned char* to, void* out, uint32_t col, int n, int d) {
 #pragma unroll 1
                 for (int z = 0; z < n / 16; ++z) {
+                    const int c0 = qt * n + 16 * z;
                     float v[16];
-                    tc5::ld16(v, trow + col + qt * n + 16 * z);
+                    uint32_t w[8];
+                    tc5::ld16(v, trow + col + c0);
                     tc5::wait_ld();
-                    if (p.rep > 1 && out != p.dv) {
-                        float* at = (float*)out + row * d + qt * n + 16 * z;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                    if (to) {
+                        unsigned char* at = to + (c0 >> 6) * PANEL;
+                        *reinterpret_cast<uint4*>(at + 2 * swz<64>(i, c0 & 63)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(at + 2 * swz<64>(i, (c0 & 63) + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (p.rep > 1 && out != p.dv) {
+                        float* at = (float*)out + row * d + c0;
                         if (i < L) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 *reinterpret_cast<float4*>(at + 4 * e) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                         }
                     } else {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                        store_rows<8>((__nv_bfloat16*)out + row0 * d + qt * n + 16 * z, (size_t)p.H * d, w, up, dn);
+                        store_rows<8>((__nv_bfloat16*)out + row0 * d + c0, (size_t)p.H * d, w, up, dn);
                     }
                 }
             };
+            const bool whole = L == CT, tiles = whole && p.rep == 1;
             if (!(ok = warp_wait(&s.q_done, ph))) break;
             tc5::fence_after();
-            put(p.dq, TX, QK, DK);
+            put(tiles ? s.out_q() : nullptr, p.dq, TX, QK, DK);
+            fence_async_smem();
             tc5::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.e2);
@@ -380,8 +399,9 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             if (lane == 0) mbar_arrive(&s.e3);
             if (!(ok = warp_wait(&s.o_done, ph))) break;
             tc5::fence_after();
-            put(p.dk, TX, QK, DK);
-            put(p.dv, TV, QV, DV);
+            put(tiles ? s.out_k() : nullptr, p.dk, TX, QK, DK);
+            put(whole ? s.out_v() : nullptr, p.dv, TV, QV, DV);
+            fence_async_smem();
             tc5::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.e4);
@@ -428,24 +448,25 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             }
             __syncwarp();
         };
-        auto load_s = [&](long long u, const unsigned char* from) {
+        auto load_s = [&](long long u, const unsigned char* from, int term) {
             if (elect_one()) {
-                mbar_arrive_expect(&s.s_full, SB);
-                bulk_g2s(s.S, from + (size_t)u * SB, SB, &s.s_full);
+                mbar_arrive_expect(&s.s_full[term], SB / 2);
+                bulk_g2s(s.S[term], from + (size_t)u * SB + term * (SB / 2), SB / 2, &s.s_full[term]);
             }
             __syncwarp();
         };
         long long u = next_unit(blockIdx.x, ch);
-        int nt = 0, nkv = 0, ns = 0;  // loads issued of each kind
+        int nt = 0, nkv = 0, ns[2] = {0, 0};  // loads issued of each kind
         if (u < units) {
             load_qy(u, ch); ++nt;
             load_kv(u, ch); ++nkv;
-            load_s(u, p.S); ++ns;
+            load_s(u, p.S, 0); ++ns[0];
+            load_s(u, p.S, 1); ++ns[1];
         }
+        Chunk nx;
+        long long un = u < units ? next_unit(u + gridDim.x, nx) : units;
         for (; ok && u < units; ++x) {
             const int ph = x & 1;
-            Chunk nx;
-            const long long un = next_unit(u + gridDim.x, nx);
             // first half
             if (!(ok = warp_wait(&s.t_full, ph)) || !(ok = warp_wait(&s.kv_full, ph)) || !(ok = warp_wait(&s.zeroed, ph))) break;
             tc5::fence_after();
@@ -457,9 +478,34 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                 tc5::commit(&s.a_done);
             }
             __syncwarp();
-            // dO S goes where dk of the chunk before was
-            if (x > 0 && !(ok = warp_wait(&s.e4, ph ^ 1))) break;
-            if (!(ok = warp_wait(&s.s_full, 0))) break;
+            if (!s.kOwnOut && x > 0) {  // S, where dk and dv of the chunk before were
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+                load_s(u, p.S, 0);
+                load_s(u, p.S, 1);
+                ++ns[0];
+                ++ns[1];
+            }
+            // the next chunk's operands to L2 meanwhile: their places here come free late, and
+            // all SMs would then wait for DRAM at once
+            if (un < units && lane == 0) {
+                const int hn = (int)(un % p.H), kn = hn / p.rep, tn = (int)nx.tok;
+#pragma unroll 1
+                for (int y = 0; y < DK / 64; ++y) {
+                    tma_prefetch_3d(&p.qmap, 64 * y, kn, tn);
+                    tma_prefetch_3d(&p.kmap, 64 * y, kn, tn);
+                }
+#pragma unroll 1
+                for (int y = 0; y < DV / 64; ++y) {
+                    tma_prefetch_3d(&p.vmap, 64 * y, hn, tn);
+                    tma_prefetch_3d(&p.ymap, 64 * y, hn, tn);
+                }
+                bulk_prefetch_l2(p.S + (size_t)un * SB, SB);
+                bulk_prefetch_l2(p.dS + (size_t)un * SB, SB);
+            }
+            __syncwarp();
+            // (dO S goes where dk of the chunk before was: its e4 came before these loads)
+            if (!(ok = warp_wait(&s.s_full[0], 0)) || !(ok = warp_wait(&s.s_full[1], 0))) break;
             tc5::fence_after();
             if (elect_one()) {
 #pragma unroll 1
@@ -471,10 +517,16 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             }
             __syncwarp();
             if (!(ok = warp_wait(&s.x_done, ph))) break;
-            load_s(u, p.dS);
-            ++ns;
+            load_s(u, p.dS, 0);
+            ++ns[0];
+            if (s.kOwnOut) {
+                load_s(u, p.dS, 1);
+                ++ns[1];
+            }
             if (!(ok = warp_wait(&s.e1, ph))) break;
             tc5::fence_after();
+            if (s.kOwnOut && lane == 0) bulk_wait_read<0>();  // dq goes where dk and dv of the chunk before were
+            __syncwarp();
             if (elect_one()) {
 #pragma unroll 2
                 for (int k = 0; k < CT / 16; ++k) tc5::mma_ts(tm + TX, tm + TP + 8 * k, tK + k * KROWS, ID_KT, true);
@@ -489,23 +541,42 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             __syncwarp();
             // V dS goes where dq is read, K dS^T where its operand was
             if (!(ok = warp_wait(&s.e2, ph))) break;
-            if (!(ok = warp_wait(&s.s_full, 1))) break;
+            const int h = (int)(u % p.H), tok = (int)ch.tok;
+            const bool whole = ch.L == CT, tiles = whole && p.rep == 1;
+            if (lane == 0 && tiles) {
+#pragma unroll
+                for (int y = 0; y < DK / 64; ++y) tma_store_3d(&p.dqmap, 64 * y, h, tok, s.out_q() + y * PANEL);
+                bulk_commit();
+                if (!s.kOwnOut) bulk_wait_read<0>();
+            }
+            __syncwarp();
+            if (!s.kOwnOut) {
+                load_s(u, p.dS, 1);
+                ++ns[1];
+            }
+            if (!(ok = warp_wait(&s.s_full[0], 1))) break;
             tc5::fence_after();
             if (elect_one()) {
-#pragma unroll 1
-                for (int t = 0; t < 2; ++t)
 #pragma unroll 2
-                    for (int k = 0; k < DV / 16; ++k)
-                        tc5::mma(tm + TX, dV + cols(k, KPANEL), dS + t * STERM + cols(k, SPANEL), ID_K, t + k > 0);
+                for (int k = 0; k < DV / 16; ++k) tc5::mma(tm + TX, dV + cols(k, KPANEL), dS + cols(k, SPANEL), ID_K, k > 0);
 #pragma unroll 2
                 for (int k = 0; k < DK / 16; ++k) tc5::mma(tm + TV, dK + cols(k, KPANEL), tS + k * KROWS, ID_VT, k > 0);
+            }
+            __syncwarp();
+            if (!(ok = warp_wait(&s.s_full[1], 1))) break;
+            tc5::fence_after();
+            if (elect_one()) {
+#pragma unroll 2
+                for (int k = 0; k < DV / 16; ++k) tc5::mma(tm + TX, dV + cols(k, KPANEL), dS + STERM + cols(k, SPANEL), ID_K, true);
                 tc5::commit(&s.x2_done);
             }
             __syncwarp();
             if (!(ok = warp_wait(&s.x2_done, ph))) break;
-            if (un < units) {
-                load_s(un, p.S);
-                ++ns;
+            if (s.kOwnOut && un < units) {
+                load_s(un, p.S, 0);
+                load_s(un, p.S, 1);
+                ++ns[0];
+                ++ns[1];
             }
             if (!(ok = warp_wait(&s.e3, ph))) break;  // K's rows are read by then too
             tc5::fence_after();
@@ -521,18 +592,37 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                 tc5::commit(&s.o_done);
             }
             __syncwarp();
+            Chunk n2;
+            const long long u2 = un < units ? next_unit(un + gridDim.x, n2) : units;
             if (!(ok = warp_wait(&s.o_done, ph))) break;
             if (un < units) {
                 load_qy(un, nx);
                 ++nt;
             }
+            if (!(ok = warp_wait(&s.e4, ph))) break;
+            if (lane == 0) {
+                if (tiles) {
+#pragma unroll
+                    for (int y = 0; y < DK / 64; ++y) tma_store_3d(&p.dkmap, 64 * y, h, tok, s.out_k() + y * PANEL);
+                }
+                if (whole) {
+#pragma unroll
+                    for (int y = 0; y < DV / 64; ++y) tma_store_3d(&p.dvmap, 64 * y, h, tok, s.out_v() + y * PANEL);
+                }
+                bulk_commit();
+            }
+            __syncwarp();
             u = un;
+            un = u2;
             ch = nx;
+            nx = n2;
         }
         // no copy and no product may be in flight when the CTA ends
         if (nt) warp_wait(&s.t_full, (nt - 1) & 1);
         if (nkv) warp_wait(&s.kv_full, (nkv - 1) & 1);
-        if (ns) warp_wait(&s.s_full, (ns - 1) & 1);
+        for (int t = 0; t < 2; ++t)
+            if (ns[t]) warp_wait(&s.s_full[t], (ns[t] - 1) & 1);
+        if (lane == 0) bulk_wait<0>();
         if (elect_one()) tc5::commit(&s.drain);
         warp_wait(&s.drain, 0);
     } else {
@@ -650,6 +740,9 @@ bool launch_tc_bwd(const Problem& p, const void* q, const void* k, const void* v
         !encode_head_map(&a.vmap, v, p.seq.rows, p.H, p.dv, CT) || !encode_head_map(&a.ymap, dO, p.seq.rows, p.H, p.dv, CT))
         return false;
     const bool parts = p.H != p.Hk;
+    if (!encode_head_map(&a.dvmap, dv, p.seq.rows, p.H, p.dv, CT)) return false;
+    if (!parts && (!encode_head_map(&a.dqmap, dq, p.seq.rows, p.H, p.dk, CT) || !encode_head_map(&a.dkmap, dk, p.seq.rows, p.H, p.dk, CT)))
+        return false;
     a.seq = p.seq; a.H = p.H; a.Hk = p.Hk; a.rep = p.H / p.Hk; a.scale = p.scale; a.g = g;
     a.S = (unsigned char*)base + l.S; a.dS = (unsigned char*)base + l.dS; a.cross = (float*)(base + l.cross);
     a.dq = parts ? (void*)(base + l.dq) : dq;

@@ -32,6 +32,14 @@ GDN_DEV void tma_load_3d(void* smem, const CUtensorMap* map, int x, int y, int z
         : "memory");
 }
 
+// Box (x, y, z) of a 3-D map from shared memory to global (bulk-group completion).
+GDN_DEV void tma_store_3d(const CUtensorMap* map, int x, int y, int z, const void* smem) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem))
+                 : "memory");
+}
+
 // Both 64-channel halves of rows z .. z+63 of head y into a Tma128 tile.
 GDN_DEV void tma_load_tile(__nv_bfloat16* tile, const CUtensorMap* map, int head, int token,
                            uint64_t* bar) {
