@@ -726,11 +726,31 @@ class _On:
 
 def _want(t, name, dtype, shape, device):
     """A contiguous CUDA tensor of this dtype and shape on this device."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
-            and t.is_contiguous():
-        return
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     _need(t, name, dtype, shape)
     raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+_CODES = {}  # torch dtypes of q, k, v and the like, filled on first use
+
+
+def _lead(t, name, dims):
+    """The first tensor of a call: (dtype code, device, shape)."""
+    try:
+        code, shape = _CODES[t.dtype], t.shape
+        if len(shape) == dims and t.is_cuda and t.is_contiguous():
+            return code, t.device, shape
+    except (KeyError, AttributeError):
+        pass
+    _need(t, name)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    _CODES[t.dtype] = _dtype_code(t)
+    return _CODES[t.dtype], t.device, t.shape
 
 
 def _given(t, name, shape, dtype, device):
@@ -771,16 +791,11 @@ def _scratch(nbytes, device, workspace):
 
 
 def _decay_inputs(q, k, v, g, h0, cu_seqlens, scale):
-    _need(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, T, Hk, dk]")
-    B, T, Hk, dk = q.shape
-    dev = q.device
+    code, dev, (B, T, Hk, dk) = _lead(q, "q", 4)
     _want(k, "k", q.dtype, q.shape, dev)
-    _need(v, "v", q.dtype)
-    if v.dim() != 4 or v.shape[0] != B or v.shape[1] != T or v.device != dev:
-        raise ValueError(f"v must be [B, T, H, dv] matching q, on {dev}")
-    H, dv = v.shape[2], v.shape[3]
+    _, vdev, (Bv, Tv, H, dv) = _lead(v, "v", 4)
+    if Bv != B or Tv != T or v.dtype is not q.dtype or vdev != dev:
+        raise ValueError(f"v must be {q.dtype} [B, T, H, dv] matching q, on {dev}")
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} value heads cannot share {Hk} key heads")
     _want(g, "g", torch.float32, (B, T, H), dev)
@@ -795,7 +810,7 @@ def _decay_inputs(q, k, v, g, h0, cu_seqlens, scale):
     states = (nseq or B, H, dv, dk)
     if h0 is not None:
         _want(h0, "h0", torch.float32, states, dev)
-    return gdn_decay_dims(B, T, H, Hk, dk, dv, _dtype_code(q), scale), nseq, states
+    return gdn_decay_dims(B, T, H, Hk, dk, dv, code, scale), nseq, states
 
 
 def gdn_decay_fwd_workspace(dims: gdn_decay_dims, nseq: int = 0) -> int:
@@ -853,23 +868,18 @@ def gdn_decay_bwd(q, k, v, g, dO, h0=None, dhT=None, *, cu_seqlens=None, scale=1
 def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
     """One decode token of gdn_decay_fwd's recurrence, in place on ``state``
     [N,H,dv,dk] fp32: q, k [N,Hk,dk]; v [N,H,dv]; g [N,H] fp32.  Returns o."""
-    _need(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [N, Hk, dk]")
-    N, Hk, dk = q.shape
-    dev = q.device
+    code, dev, (N, Hk, dk) = _lead(q, "q", 3)
     _want(k, "k", q.dtype, q.shape, dev)
-    _need(v, "v", q.dtype)
-    if v.dim() != 3 or v.shape[0] != N or v.device != dev:
-        raise ValueError(f"v must be [N, H, dv] matching q, on {dev}")
-    H, dv = v.shape[1], v.shape[2]
+    _, vdev, (Nv, H, dv) = _lead(v, "v", 3)
+    if Nv != N or v.dtype is not q.dtype or vdev != dev:
+        raise ValueError(f"v must be {q.dtype} [N, H, dv] matching q, on {dev}")
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} value heads cannot share {Hk} key heads")
     _want(g, "g", torch.float32, (N, H), dev)
     _want(state, "state", torch.float32, (N, H, dv, dk), dev)
     with _On(dev, stream) as s:
         o = _like(o, "o", v)
-        st = lib().gdn_decay_step(N, H, Hk, dk, dv, _dtype_code(q), scale, q.data_ptr(), k.data_ptr(),
+        st = lib().gdn_decay_step(N, H, Hk, dk, dv, code, scale, q.data_ptr(), k.data_ptr(),
                                   v.data_ptr(), g.data_ptr(), state.data_ptr(), o.data_ptr(), s)
     _check(st, "gdn_decay_step")
     return o
@@ -877,25 +887,17 @@ def gdn_decay_step(q, k, v, g, state, *, scale=1.0, o=None, stream=None):
 
 # ---- draft-tree attention over a paged cache ---------------------------------
 def _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len):
-    _need(k, "k")
-    dev = k.device
-    _need(parent, "parent", torch.int32)
-    if parent.dim() != 2 or parent.device != dev:
-        raise ValueError(f"parent must be [N, M] int32 on {dev}")
-    N, M = parent.shape
-    if k.dim() != 4 or k.shape[0] != N or k.shape[1] != M:
-        raise ValueError("k must be [N, M, Hkv, d]")
-    Hkv, d = k.shape[2], k.shape[3]
+    code, dev, (N, M, Hkv, d) = _lead(k, "k", 4)
+    _want(parent, "parent", torch.int32, (N, M), dev)
     _want(v, "v", k.dtype, k.shape, dev)
-    _need(k_cache, "k_cache", k.dtype)
-    if k_cache.dim() != 4 or k_cache.shape[2] != Hkv or k_cache.shape[3] != d or k_cache.device != dev:
-        raise ValueError(f"k_cache must be [pages, page, Hkv, d] on {dev}")
+    _, cdev, (pages, page, Hc, dc) = _lead(k_cache, "k_cache", 4)
+    if Hc != Hkv or dc != d or k_cache.dtype is not k.dtype or cdev != dev:
+        raise ValueError(f"k_cache must be {k.dtype} [pages, page, Hkv, d] on {dev}")
     _want(v_cache, "v_cache", k.dtype, k_cache.shape, dev)
-    _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != N or block_table.device != dev:
-        raise ValueError(f"block_table must be [N, width] int32 on {dev}")
+    width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
+    _want(block_table, "block_table", torch.int32, (N, width), dev)
     _want(cache_len, "cache_len", torch.int32, (N,), dev)
-    return N, M, Hkv, d, k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
+    return code, dev, N, M, Hkv, d, pages, page, width
 
 
 def gdn_tree_attn(parent, q, k, v, k_cache, v_cache, block_table, cache_len, *, scale=1.0, window=0,
@@ -905,12 +907,10 @@ def gdn_tree_attn(parent, q, k, v, k_cache, v_cache, block_table, cache_len, *, 
     [N,M,Hkv,d]; k_cache, v_cache [pages,page,Hkv,d]; block_table [N,width] and
     cache_len [N] int32.  window > 0: only positions less than ``window`` back.
     Returns o [N,M,Hq,d]."""
-    N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len)
-    dev = k.device
-    _need(q, "q", k.dtype)
-    if q.dim() != 4 or q.shape[0] != N or q.shape[1] != M or q.shape[3] != d or q.device != dev:
-        raise ValueError(f"q must be [N, M, Hq, d] matching k, on {dev}")
-    Hq, dt = q.shape[2], _dtype_code(q)
+    dt, dev, N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table,
+                                                            cache_len)
+    Hq = q.shape[2] if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
+    _want(q, "q", k.dtype, (N, M, Hq, d), dev)
     with _On(dev, stream) as s:
         o = _like(o, "o", q)
         ws = _scratch(lib().gdn_tree_attn_workspace(N, M, Hq, Hkv, d, dt, page, width), dev, workspace)
@@ -927,8 +927,8 @@ def gdn_tree_append(parent, accepted, k, v, k_cache, v_cache, block_table, cache
     """Appends the k and v rows of the root path of node accepted[n] (int32 [N];
     -1: nothing) to sequence n's pages, in place on k_cache and v_cache.  Returns
     the new lengths (``new_len`` may be ``cache_len``)."""
-    N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len)
-    dev = k.device
+    code, dev, N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table,
+                                                              cache_len)
     _want(accepted, "accepted", torch.int32, (N,), dev)
     if status is not None:
         _need(status, "status", torch.int32)
@@ -936,7 +936,7 @@ def gdn_tree_append(parent, accepted, k, v, k_cache, v_cache, block_table, cache
             raise ValueError(f"status must hold a word on {dev}")
     with _On(dev, stream) as s:
         new_len = _like(new_len, "new_len", cache_len)
-        st = lib().gdn_tree_append(N, M, Hkv, d, _dtype_code(k), parent.data_ptr(), accepted.data_ptr(),
+        st = lib().gdn_tree_append(N, M, Hkv, d, code, parent.data_ptr(), accepted.data_ptr(),
                                    k.data_ptr(), v.data_ptr(), pages, page, width, k_cache.data_ptr(),
                                    v_cache.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(),
                                    new_len.data_ptr(), _at(status), s)
