@@ -21,18 +21,20 @@
 
 #include "checks.h"
 #include "common.cuh"
+#include "decay_tc.cuh"
 #include "mma.cuh"
 
 namespace gdn {
 namespace {
 
+using decay::add2f;
+using decay::fma2;
+using decay::mul2;
+
 constexpr int NT = 256;
 
-template <typename T>
-GDN_DEV void load16(float* v, const T* p);
-template <>
-GDN_DEV void load16<__nv_bfloat16>(float* v, const __nv_bfloat16* p) {
-    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
+// 16 bytes of a row, as loaded and as fp32.
+GDN_DEV void widen(float* v, const uint4& r, __nv_bfloat16) {
     const uint32_t x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -41,11 +43,14 @@ GDN_DEV void load16<__nv_bfloat16>(float* v, const __nv_bfloat16* p) {
         v[2 * i + 1] = f.y;
     }
 }
-template <>
-GDN_DEV void load16<float>(float* v, const float* p) {
-    const float4 r = __ldcs(reinterpret_cast<const float4*>(p));
-    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+GDN_DEV void widen(float* v, const uint4& r, float) {
+    v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
 }
+// 1 / (1 + e^-z).  For bf16 the fast exponential and quotient, whose error (2^-18 where
+// the result is not small) is far below the rounding of the result.
+GDN_DEV float sigmoid(float z, float) { return 1.f / (1.f + expf(-z)); }
+GDN_DEV float sigmoid(float z, __nv_bfloat16) { return __fdividef(1.f, 1.f + __expf(-z)); }
 GDN_DEV void store16(__nv_bfloat16* p, const float* v) {
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                                                    pack_bf16(v[6], v[7])));
@@ -69,7 +74,7 @@ struct Row {
 };
 
 template <typename T, int D, bool CENTER, bool BWD>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 4)
 gated_norm_kernel(long long rows, int H, int wheads, long long U, float eps, const T* __restrict__ x,
                   const T* __restrict__ z, const float* __restrict__ w, const T* __restrict__ dy,
                   T* __restrict__ out, T* __restrict__ dz, float* __restrict__ part) {
@@ -83,53 +88,79 @@ gated_norm_kernel(long long rows, int H, int wheads, long long U, float eps, con
         wr[j] = w[wh * D + (j / R::VEC * R::LPR + sub) * R::VEC + j % R::VEC];
         dw[j] = 0.f;
     }
+    uint4 nx[R::NV], nz[R::NV], ng[R::NV];
+    auto fetch = [&](long long r) {
+        const bool in = unit < U && r < rows;
+#pragma unroll
+        for (int p = 0; p < R::NV; ++p) {
+            const size_t at = (size_t)(in ? r : 0) * D + (p * R::LPR + sub) * R::VEC;
+            nx[p] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+            nz[p] = __ldcs(reinterpret_cast<const uint4*>(z + at));
+            if constexpr (BWD) ng[p] = __ldcs(reinterpret_cast<const uint4*>(dy + at));
+        }
+    };
     // every lane of a warp runs the same number of turns: the shuffles need them all
     const long long first = (long long)blockIdx.x * R::UPC + (threadIdx.x / 32) * (32 / R::LPR);
+    if (first < rows) fetch(unit);
     for (long long base = 0; base + first < rows; base += U) {
         const long long r = base + unit;
         const bool in = unit < U && r < rows;
         float xv[R::CPL], zv[R::CPL], g[R::CPL];
 #pragma unroll
         for (int p = 0; p < R::NV; ++p) {
-            const size_t at = (size_t)(in ? r : 0) * D + (p * R::LPR + sub) * R::VEC;
-            load16<T>(xv + p * R::VEC, x + at);
-            load16<T>(zv + p * R::VEC, z + at);
-            if constexpr (BWD) load16<T>(g + p * R::VEC, dy + at);
+            widen(xv + p * R::VEC, nx[p], T());
+            widen(zv + p * R::VEC, nz[p], T());
+            if constexpr (BWD) widen(g + p * R::VEC, ng[p], T());
         }
-        float mean = 0.f;
+        if (base + U + first < rows) fetch(r + U);  // the next turn's rows are on their way
         if constexpr (CENTER) {
+            float mean = 0.f;
 #pragma unroll
             for (int j = 0; j < R::CPL; ++j) mean += xv[j];
-            mean = row_sum<R::LPR>(mean) * (1.f / D);
-        }
-        float sq = 0.f;
+            mean = row_sum<R::LPR>(mean) * (-1.f / D);
 #pragma unroll
-        for (int j = 0; j < R::CPL; ++j) {
-            xv[j] -= mean;
-            sq += xv[j] * xv[j];
+            for (int j = 0; j < R::CPL; j += 2) add2f(xv[j], xv[j + 1], xv[j], xv[j + 1], mean, mean);
         }
-        const float rs = 1.f / sqrtf(row_sum<R::LPR>(sq) * (1.f / D) + eps);
-        float eh = 0.f, es = 0.f;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < R::CPL; ++j) {
-            const float h = xv[j] * rs, sg = 1.f / (1.f + expf(-zv[j])), act = zv[j] * sg;
+        for (int j = 0; j < R::CPL; j += 2) fma2(s0, s1, xv[j], xv[j + 1], xv[j], xv[j + 1], s0, s1);
+        const float rs = rsqrtf(row_sum<R::LPR>(s0 + s1) * (1.f / D) + eps);
+        float e0 = 0.f, e1 = 0.f, t0 = 0.f, t1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < R::CPL; j += 2) {  // (pairs: two operations to an instruction)
+            float h0, h1, a0, a1;
+            const float g0 = sigmoid(zv[j], T()), g1 = sigmoid(zv[j + 1], T());
+            mul2(h0, h1, xv[j], xv[j + 1], rs, rs);
+            mul2(a0, a1, zv[j], zv[j + 1], g0, g1);
             if constexpr (BWD) {
-                const float gh = g[j] * h, e = g[j] * wr[j] * act;
-                if (in) dw[j] += gh * act;
-                zv[j] = gh * wr[j] * sg * (1.f + zv[j] * (1.f - sg));
-                eh += e * h;
-                es += e;
-                xv[j] = h;
-                g[j] = e;
+                float w0, w1, p0, p1, q0, q1;
+                mul2(w0, w1, g[j], g[j + 1], wr[j], wr[j + 1]);           // dy w
+                mul2(p0, p1, g[j], g[j + 1], h0, h1);                     // dy h
+                if (in) fma2(dw[j], dw[j + 1], p0, p1, a0, a1, dw[j], dw[j + 1]);
+                // s'(z) = sigmoid + s (1 - sigmoid)
+                fma2(q0, q1, a0, a1, -g0, -g1, a0, a1);
+                add2f(q0, q1, q0, q1, g0, g1);
+                mul2(p0, p1, w0, w1, h0, h1);
+                mul2(zv[j], zv[j + 1], p0, p1, q0, q1);
+                mul2(w0, w1, w0, w1, a0, a1);                             // e
+                fma2(e0, e1, w0, w1, h0, h1, e0, e1);
+                if constexpr (CENTER) add2f(t0, t1, t0, t1, w0, w1);
+                xv[j] = h0; xv[j + 1] = h1;
+                g[j] = w0; g[j + 1] = w1;
             } else {
-                xv[j] = wr[j] * h * act;
+                mul2(h0, h1, h0, h1, wr[j], wr[j + 1]);
+                mul2(xv[j], xv[j + 1], h0, h1, a0, a1);
             }
         }
         if constexpr (BWD) {
-            eh = row_sum<R::LPR>(eh) * (1.f / D);
-            es = CENTER ? row_sum<R::LPR>(es) * (1.f / D) : 0.f;
+            const float eh = row_sum<R::LPR>(e0 + e1) * (-1.f / D);
+            const float es = CENTER ? row_sum<R::LPR>(t0 + t1) * (-1.f / D) : 0.f;
 #pragma unroll
-            for (int j = 0; j < R::CPL; ++j) xv[j] = (g[j] - xv[j] * eh - es) * rs;
+            for (int j = 0; j < R::CPL; j += 2) {
+                fma2(xv[j], xv[j + 1], xv[j], xv[j + 1], eh, eh, g[j], g[j + 1]);
+                if constexpr (CENTER) add2f(xv[j], xv[j + 1], xv[j], xv[j + 1], es, es);
+                mul2(xv[j], xv[j + 1], xv[j], xv[j + 1], rs, rs);
+            }
         }
         if (!in) continue;
 #pragma unroll
@@ -175,10 +206,10 @@ gated_norm_dw_kernel(long long U, int heads, int D, const float* __restrict__ pa
     if (threadIdx.x == 0) dw[h * D + blockIdx.y * 32 + threadIdx.y] = t;
 }
 
-// Units of a call: as many as fill the device twice over, in whole turns of
-// the heads, and no more than there are rows.
+// Units of a call: four CTAs per SM, in whole turns of the heads, and no more than
+// there are rows.
 long long units(long long rows, int H, int lpr) {
-    const long long fill = 148ll * 16 * (NT / lpr) / 2;
+    const long long fill = 148ll * 4 * (NT / lpr);
     return std::max<long long>(std::min(rows, fill) / H, 1) * H;
 }
 
