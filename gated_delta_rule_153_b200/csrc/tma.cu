@@ -35,12 +35,13 @@ bool encode_token_map(CUtensorMap* map, const void* base, int B, int T, int H, i
            CUDA_SUCCESS;
 }
 
-bool encode_head_map(CUtensorMap* map, const void* base, long long rows, int heads, int d, int box_rows) {
+bool encode_head_map(CUtensorMap* map, const void* base, long long rows, int heads, int d, int box_rows,
+                     int box_heads) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -69,7 +69,7 @@ bool encode_token_map(CUtensorMap* map, const void* base, int B, int T, int H,
                       int box_cols = 64, int box_rows = 64);
 
 // Host: the map of a [rows, heads, d] bf16 tensor (rows: tokens, or cache
-// positions) in 128-byte-swizzled boxes of box_rows x 64 channels of one head.
-bool encode_head_map(CUtensorMap* map, const void* base, long long rows, int heads, int d, int box_rows);
+// positions) in 128-byte-swizzled boxes of box_rows x box_heads x 64 channels.
+bool encode_head_map(CUtensorMap* map, const void* base, long long rows, int heads, int d, int box_rows, int box_heads = 1);
 
 }  // namespace gdn

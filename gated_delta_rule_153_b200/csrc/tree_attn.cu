@@ -55,7 +55,10 @@ GDN_DEV int parent_of(const int* parent, int i, unsigned int* status) {
 // of every unit is one step of work, and the steps of the whole call, in order, are
 // cut evenly over one CTA per SM, so that sequences of any lengths fill the
 // device.  A CTA whose share starts or ends within a unit leaves a partial result
-// (maximum, sum, weighted sum) for a second kernel.
+// (maximum, sum, weighted sum) in the workspace; the last CTA of a unit to do so,
+// told by a counter, joins them, in the order of the steps whoever that is.  With units
+// for less than half of the SMs, each unit instead gets a number of CTAs of its own:
+// no CTA then works on two, which would be most of its time.
 //
 // Per tile:  S = Q K^T (tcgen05, 128 x 128 x d, lane = row),  P = e^{S - m} as a
 // bf16 A operand over S in tensor memory,  O += P V.  Two groups of four softmax
@@ -73,29 +76,34 @@ constexpr int kThreads = 32 * (kSoft + 2);
 
 template <int D>
 struct alignas(1024) Smem {
-    unsigned char Q[D / 64][PANEL];  // at a segment's end: maxima and sums of the groups
+    unsigned char Q[D / 64][PANEL];
     unsigned char K[NST][D / 64][PANEL], V[NST][D / 64][PANEL];
+    float2 ml[128];                  // a segment's end: one group's maxima and sums, then both factors
     int parent[kMaxNodes];
     // 16-row pieces of a step's tile that hold cached rows; twice the stages, as the
     // loader may be that far ahead of the softmax warps
     uint32_t have[2 * NST];
-    uint64_t k_full[NST], v_full[NST], k_free[NST], v_free[NST], s_ready[2], p_ready[2], o_done[2], q_ready, seg_done, meet, drain;
+    uint64_t k_full[NST], v_full[NST], k_free[NST], v_free[NST], s_ready[2], p_ready[2], o_done[2], q_full, seg_done, meet, drain;
     long long warp_sum[kSoft + 2];
     int n0;
     long long before, total;
+    int last[2], b0[2], b1[2];  // the units left at the end: whether joined here, and their CTAs
     uint32_t tmem;
 };
 
 struct Params {
-    CUtensorMap kmap, vmap, knode, vnode;
+    CUtensorMap qmap, kmap, vmap, knode, vnode;
     Cache c;
     int N, M, Hq, Hkv, group, row_tiles, window;
     float scale;
+    int q_tma;                       // Q rows by TMA: a tile is whole nodes, and the scale is positive
     const int* parent;
     const __nv_bfloat16* q;
     __nv_bfloat16* o;
-    float* part;                     // [CTA][2][rows][D + 2]: sum, then m and l
-    int part_rows;
+    float* part;                     // [CTA][2][D / 4][rows][4] weighted sums, then [rows][2] m and l
+    int part_rows, part_floats;      // rows of a part, and its size (whole 16-byte pieces)
+    unsigned int* count;             // per unit: parts left so far
+    int split;                       // CTAs per unit, or 0: the steps cut evenly over all CTAs
     unsigned int* status;
 };
 
@@ -150,7 +158,7 @@ GDN_DEV long long share_start(long long total, long long parts, long long b) { r
 // All threads: total steps, and the sequence that holds step `at` with the steps
 // before it (s.n0, s.before).  Every thread sums a run of sequences.
 template <class S>
-GDN_DEV void locate(S& s, const Params& p, long long (*at_of)(long long, int, int), int b, int ctas) {
+GDN_DEV void locate(S& s, const Params& p, int b, int ctas) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.N + kThreads - 1) / kThreads, a = min(p.N, tid * per), e = min(p.N, a + per);
     const int units = p.Hkv * p.row_tiles;
@@ -171,7 +179,7 @@ GDN_DEV void locate(S& s, const Params& p, long long (*at_of)(long long, int, in
     }
     all *= units;
     before *= units;
-    const long long at = at_of(all, b, ctas);
+    const long long at = share_start(all, shares(all, ctas), b);
     if (at >= before && at < before + mine * units) {
         int n = a;
         for (;; ++n) {
@@ -185,7 +193,21 @@ GDN_DEV void locate(S& s, const Params& p, long long (*at_of)(long long, int, in
     if (tid == 0) s.total = all;
     __syncthreads();
 }
-GDN_DEV long long cta_start(long long total, int b, int ctas) { return share_start(total, shares(total, ctas), b); }
+// The share that holds step `at`.
+GDN_DEV int owner_of(long long total, long long parts, long long at) {
+    long long b = at * parts / total;
+    while (share_start(total, parts, b + 1) <= at) ++b;
+    while (share_start(total, parts, b) > at) --b;
+    return (int)b;
+}
+// Sixteen values of a row in bf16.
+GDN_DEV void put16(__nv_bfloat16* to, const float (&u)[16]) {
+    uint32_t h[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) h[q] = pack_bf16(u[2 * q], u[2 * q + 1]);
+    *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(to + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+}
 
 GDN_DEV unsigned char* align1k(unsigned char* p) {
     return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -215,22 +237,34 @@ tree_attn_kernel(const __grid_constant__ Params p) {
             mbar_init(&s.p_ready[g], kSoft / 2);
             mbar_init(&s.o_done[g], 1);
         }
-        mbar_init(&s.q_ready, kSoft);
+        mbar_init(&s.q_full, p.q_tma ? 1 : kSoft);
         mbar_init(&s.seg_done, kSoft);
         mbar_init(&s.meet, kSoft);
         mbar_init(&s.drain, 1);
         fence_mbar_init();
     }
     if (warp == kSoft + 1) tc5::alloc(&s.tmem, 512);
-    locate(s, p, [](long long total, int i, int n) { return cta_start(total, i, n); }, b, ctas);
+    if (!p.split) locate(s, p, b, ctas);
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, s.tmem, 0);
-    const long long parts = shares(s.total, ctas);
-    Walk w{share_start(s.total, parts, b), b < parts ? share_start(s.total, parts, b + 1) : 0, s.before, s.n0, {}};
-    if (b < parts) w.span = span_of(p, w.n);
-    else w.end = w.at;
+    const long long parts = p.split ? 0 : shares(s.total, ctas);
+    Walk w{0, 0, 0, 0, {}};
+    int pieces = 0;  // split: CTAs that share this one's unit
+    if (p.split) {
+        const int unit = b / p.split, units = p.Hkv * p.row_tiles, q = b % p.split;
+        w.n = unit / units;
+        w.span = span_of(p, w.n);
+        pieces = max(1, min(p.split, w.span.steps / 2));
+        if (q < pieces) {
+            w.at = (long long)(unit % units) * w.span.steps + w.span.steps * q / pieces;
+            w.end = (long long)(unit % units) * w.span.steps + w.span.steps * (q + 1) / pieces;
+        }
+    } else if (b < parts) {
+        w = Walk{share_start(s.total, parts, b), share_start(s.total, parts, b + 1), s.before, s.n0, {}};
+        w.span = span_of(p, w.n);
+    }
     // tensor-memory columns of a group: S (P over it, as bf16 pairs), O
     constexpr uint32_t TG = 256, TO = 128;
     int x = 0;      // steps so far: the group and the phases of its barriers follow from it
@@ -242,7 +276,11 @@ tree_attn_kernel(const __grid_constant__ Params p) {
         const uint32_t tg = tm + ((uint32_t)(32 * (warp & 3)) << 16) + TG * grp;
         const float sc = p.scale == 0.f ? 1.4426950408889634f : fabsf(p.scale) * 1.4426950408889634f;
         const int R = p.M * p.group;
-        int met = 0;
+        struct {
+            Segment g;
+            long long u0;  // the unit's first step
+        } left[2];
+        int lefts = 0, met = 0;
         auto meet = [&]() {  // the softmax warps come together (within the bounds of a wait)
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.meet);
@@ -252,21 +290,34 @@ tree_attn_kernel(const __grid_constant__ Params p) {
             const int row = g.rt * 128 + r, node = row / p.group, head = g.kh * p.group + row % p.group;
             const bool live = row < R;
             const bool busy = g.rt * 128 + 32 * (warp & 3) < R;  // this warp has rows
-            // Q of the unit (its sign with the scale's; zero for a zero scale and past the rows)
             const size_t qrow = (((size_t)g.n * p.M + (live ? node : 0)) * p.Hq + (live ? head : 0)) * D;
-            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u, keep = p.scale == 0.f || !live ? 0u : 0xffffffffu;
-#pragma unroll 1
-            for (int j = 0; j < D / 16; ++j) {
-                const int ch = grp * (D / 16) + j;  // 16-byte piece of the row
-                uint4 v = *reinterpret_cast<const uint4*>(p.q + qrow + 8 * ch);
-                v = make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep);
-                *reinterpret_cast<uint4*>(s.Q[ch >> 3] + 2 * swz<64>(r, 8 * (ch & 7))) = v;
+            if (!p.q_tma) {
+                // Q of the unit (its sign with the scale's; zero for a zero scale and past the rows):
+                // D / 8 lanes to a row, all of a warp's 16 rows on their way at once.  Every S
+                // of the Q before is done: this warp has waited for all of them.
+                constexpr int LR = D / 8, RPI = 32 / LR;
+                const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+                uint4 v[16 / RPI];
+#pragma unroll
+                for (int j = 0; j < 16 / RPI; ++j) {
+                    const int y = g.rt * 128 + 16 * warp + RPI * j + lane / LR;
+                    v[j] = make_uint4(0, 0, 0, 0);
+                    if (y < R && p.scale != 0.f)
+                        v[j] = __ldg(reinterpret_cast<const uint4*>(
+                            p.q + (((size_t)g.n * p.M + y / p.group) * p.Hq + g.kh * p.group + y % p.group) * D + 8 * (lane % LR)));
+                }
+#pragma unroll
+                for (int j = 0; j < 16 / RPI; ++j) {
+                    const int y = 16 * warp + RPI * j + lane / LR, ch = lane % LR;
+                    *reinterpret_cast<uint4*>(s.Q[ch >> 3] + 2 * swz<64>(y, 8 * (ch & 7))) =
+                        make_uint4(v[j].x ^ flip, v[j].y ^ flip, v[j].z ^ flip, v[j].w ^ flip);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.q_full);
             }
             if (tid < p.M) s.parent[tid] = parent_of(p.parent + (size_t)g.n * p.M, tid, p.status);
-            fence_async_smem();
-            tc5::fence_before();
             if (!meet()) break;
-            if (lane == 0) mbar_arrive(&s.q_ready);
             // what this row sees: cached positions from `lo`, nodes in `anc`
             unsigned long long anc = 0;
             int depth = 0;
@@ -401,19 +452,34 @@ tree_attn_kernel(const __grid_constant__ Params p) {
             }
             if (!ok) break;
             tc5::fence_after();
-            float* ml = reinterpret_cast<float*>(s.Q[0]);  // every product of this Q is done
-            ml[grp * 256 + r] = m;
-            ml[grp * 256 + 128 + r] = any ? l : 0.f;
-            if (!meet()) break;
-            const float m0 = ml[r], l0 = ml[128 + r], m1 = ml[256 + r], l1 = ml[384 + r];
-            const float mx = fmaxf(m0, m1);
-            const float f0 = l0 > 0.f ? ex2(m0 - mx) : 0.f, f1 = l1 > 0.f ? ex2(m1 - mx) : 0.f;
-            const float lt = l0 * f0 + l1 * f1;
+            // m and l of both groups; the factors of their sums (a group without a step has
+            // nothing in its O)
+            float mx = 0.f, lt = 0.f, f0, f1;
             const bool whole = g.t0 == 0 && g.t1 == g.span.steps;
+            if (grp == 1) s.ml[r] = make_float2(m, any ? l : 0.f);
+            if (!meet()) break;
+            if (grp == 0) {
+                const float2 o = s.ml[r];
+                const float l0 = any ? l : 0.f;
+                mx = fmaxf(m, o.x);
+                f0 = l0 != 0.f ? ex2(m - mx) : 0.f;  // (a NaN goes on)
+                f1 = o.y != 0.f ? ex2(o.x - mx) : 0.f;
+                lt = l0 * f0 + o.y * f1;
+                if (whole) {
+                    f0 *= 1.f / lt;
+                    f1 *= 1.f / lt;
+                }
+                s.ml[r] = make_float2(f0, f1);
+            }
+            if (!meet()) break;
+            if (grp == 1) {
+                const float2 o = s.ml[r];
+                f0 = o.x;
+                f1 = o.y;
+            }
             if (busy) {
-                const float inv = whole ? 1.f / lt : 1.f;
                 // a CTA that starts within the unit leaves its part in place 0, else in 1
-                float* part = p.part + (((size_t)b * 2 + (g.t0 > 0 ? 0 : 1)) * p.part_rows + r) * (D + 2);
+                float* part = p.part + ((size_t)b * 2 + (g.t0 > 0 ? 0 : 1)) * p.part_floats;
                 __nv_bfloat16* out = p.o + qrow;
                 const uint32_t t0 = tg - TG * grp + TO, t1 = t0 + TG;
 #pragma unroll 1
@@ -423,32 +489,101 @@ tree_attn_kernel(const __grid_constant__ Params p) {
                     tc5::ld16(u, t0 + c0);
                     tc5::ld16(v, t1 + c0);
                     tc5::wait_ld();
-                    // a group without a step has nothing in its O
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) u[q] = ((f0 > 0.f ? f0 * u[q] : 0.f) + (f1 > 0.f ? f1 * v[q] : 0.f)) * inv;
+                    for (int q = 0; q < 16; ++q) u[q] = (f0 != 0.f ? f0 * u[q] : 0.f) + (f1 != 0.f ? f1 * v[q] : 0.f);
                     if (!live) continue;
                     if (whole) {
-                        uint32_t h[8];
+                        put16(out + c0, u);
+                    } else {  // a warp's rows side by side
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) h[q] = pack_bf16(u[2 * q], u[2 * q + 1]);
-                        *reinterpret_cast<uint4*>(out + c0) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4*>(out + c0 + 8) = make_uint4(h[4], h[5], h[6], h[7]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<float2*>(part + c0 + 2 * q) = make_float2(u[2 * q], u[2 * q + 1]);
+                        for (int q = 0; q < 16; q += 4)
+                            *reinterpret_cast<float4*>(part + ((size_t)(c0 + q) / 4 * p.part_rows + r) * 4) =
+                                make_float4(u[q], u[q + 1], u[q + 2], u[q + 3]);
                     }
                 }
-                if (!whole && live && grp == 0) *reinterpret_cast<float2*>(part + D) = make_float2(mx, lt);
+                if (!whole && live && grp == 0)
+                    *reinterpret_cast<float2*>(part + (size_t)D * p.part_rows + 2 * r) = make_float2(mx, lt);
+            }
+            if (!whole) {  // to be told at the end
+                left[lefts].g = g;
+                left[lefts++].u0 = w.at - g.t1;
             }
             tc5::fence_before();
-            if (!meet()) break;  // before the next Q goes over the sums
+            __syncwarp();
             if (lane == 0) mbar_arrive(&s.seg_done);
             ++segs;
+        }
+        // ---- the units of which this CTA had a part: told, and joined if it was the last ----
+        // (at the end, when the parts' stores have long been on their way)
+        if (ok && lefts) {
+            __threadfence();
+            if (meet()) {
+                if (tid < lefts) {
+                    const Segment& y = left[tid].g;
+                    const int b0 = p.split ? b / p.split * p.split : owner_of(s.total, parts, left[tid].u0);
+                    const int b1 = p.split ? b0 + pieces - 1 : owner_of(s.total, parts, left[tid].u0 + y.span.steps - 1);
+                    s.b0[tid] = b0;
+                    s.b1[tid] = b1;
+                    s.last[tid] = atomicAdd(p.count + ((size_t)y.n * p.Hkv + y.kh) * p.row_tiles + y.rt, 1u) == (unsigned)(b1 - b0);
+                }
+                meet();
+            }
+        }
+        for (int i = 0; ok && i < lefts; ++i) {
+            const Segment& y = left[i].g;
+            const int row = y.rt * 128 + r;
+            if (!s.last[i] || row >= R) continue;
+            __threadfence();
+            // half of the channels of each part in turn, all on their way at once
+            float mj = -INFINITY, lj = 0.f, u[D / 2];
+#pragma unroll
+            for (int q = 0; q < D / 2; ++q) u[q] = 0.f;
+#pragma unroll 1
+            for (int c = s.b0[i]; c <= s.b1[i]; ++c) {
+                // the first of a unit's CTAs left its part in place 1, the others in place 0
+                const float* at = p.part + ((size_t)c * 2 + (c > s.b0[i] ? 0 : 1)) * p.part_floats;
+                const float2 o = __ldcg(reinterpret_cast<const float2*>(at + (size_t)D * p.part_rows + 2 * r));
+                at += ((size_t)(grp * (D / 8)) * p.part_rows + r) * 4;
+                float4 v[D / 8];
+#pragma unroll
+                for (int q = 0; q < D / 8; ++q) v[q] = __ldcg(reinterpret_cast<const float4*>(at + (size_t)q * 4 * p.part_rows));
+                if (o.y == 0.f) continue;  // (a part without a visible key has nothing in its sums)
+                const float mn = fmaxf(mj, o.x), f = ex2(o.x - mn), e = lj != 0.f ? ex2(mj - mn) : 0.f;
+                mj = mn;
+                lj = e * lj + f * o.y;
+#pragma unroll
+                for (int q = 0; q < D / 8; ++q) {
+                    u[4 * q] = e * u[4 * q] + f * v[q].x; u[4 * q + 1] = e * u[4 * q + 1] + f * v[q].y;
+                    u[4 * q + 2] = e * u[4 * q + 2] + f * v[q].z; u[4 * q + 3] = e * u[4 * q + 3] + f * v[q].w;
+                }
+            }
+            const float inv = 1.f / lj;
+            __nv_bfloat16* out = p.o + (((size_t)y.n * p.M + row / p.group) * p.Hq + y.kh * p.group + row % p.group) * D + grp * (D / 2);
+#pragma unroll
+            for (int q = 0; q < D / 2; q += 16) {
+                float w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = inv * u[q + e];
+                put16(out + q, w);
+            }
         }
     } else if (warp == kSoft) {
         // ---- loads: a lane per page -------------------------------------------------
         const int pages = KT / p.c.page;
+        // Q follows the first step's keys and values, once the S before it are done
+        auto load_q = [&]() {
+            if (!p.q_tma) return true;
+            if (x > 0 && !(ok = warp_wait(&s.k_free[(x - 1) % NST], ((x - 1) / NST) & 1))) return false;
+            if (lane == 0) {
+                mbar_arrive_expect(&s.q_full, D / 64 * PANEL);
+#pragma unroll
+                for (int y = 0; y < D / 64; ++y)
+                    tma_load_3d(s.Q[y], &p.qmap, 64 * y, g.kh * p.group, g.n * p.M + g.rt * (128 / p.group), &s.q_full);
+            }
+            __syncwarp();
+            ++segs;
+            return true;
+        };
         while (ok && w.next(p, g)) {
             for (int t = g.t0; t < g.t1; ++t, ++x) {
                 const int st = x % NST, use = x / NST;
@@ -465,6 +600,7 @@ tree_attn_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                         for (int y = 0; y < D / 64; ++y) tma_load_3d(s.V[st][y], &p.vnode, 64 * y, g.kh, g.n * p.M, &s.v_full[st]);
                     }
+                    if (t == g.t0 && !load_q()) { ++x; break; }
                     continue;
                 }
                 const int pos = (g.span.first + t) * KT + lane * p.c.page;
@@ -501,8 +637,10 @@ tree_attn_kernel(const __grid_constant__ Params p) {
                     for (int y = 0; y < D / 64; ++y) tma_load_3d(s.V[st][y] + at, &p.vmap, 64 * y, g.kh, pg * p.c.page, &s.v_full[st]);
                 }
                 __syncwarp();
+                if (t == g.t0 && !load_q()) { ++x; break; }
             }
         }
+        if (p.q_tma && segs) warp_wait(&s.q_full, (segs - 1) & 1);
         // no copy may be in flight when the CTA ends (a stage that a wait gave up on makes this
         // one give up as well: its copies are in by then)
         for (int y = max(0, x - NST); y < x; ++y) {
@@ -515,8 +653,7 @@ tree_attn_kernel(const __grid_constant__ Params p) {
         constexpr uint64_t KROWS = (16 * 128) >> 4, KCOLS = 32 >> 4, KPANEL = PANEL >> 4;
         const uint64_t dQ = tc5::kmajor<KT>(smem_u32(s.Q), 0);
         while (ok && w.next(p, g)) {
-            if (segs > 0 && !(ok = warp_wait(&s.seg_done, (segs - 1) & 1))) break;
-            if (!(ok = warp_wait(&s.q_ready, segs & 1))) break;
+            if (!(ok = warp_wait(&s.q_full, segs & 1))) break;
             const int x0 = x, x1 = x + (g.t1 - g.t0);
             for (; x <= x1; ++x) {
                 if (x < x1) {
@@ -539,6 +676,8 @@ tree_attn_kernel(const __grid_constant__ Params p) {
                 }
                 if (x > x0) {
                     const int y = x - 1, st = y % NST;
+                    // the O of the segment before has been read
+                    if (y == x0 && segs > 0 && !(ok = warp_wait(&s.seg_done, (segs - 1) & 1))) break;
                     if (!(ok = warp_wait(&s.v_full[st], (y / NST) & 1))) break;
                     if (!(ok = warp_wait(&s.p_ready[y & 1], (y >> 1) & 1))) break;
                     tc5::fence_after();
@@ -570,85 +709,15 @@ tree_attn_kernel(const __grid_constant__ Params p) {
     }
 }
 
-// Units that more than one CTA worked on: their parts, joined in order.  A CTA per
-// unit and 16 rows, a warp per row.
-constexpr int JT = 256, JR = 16;
-template <int D>
-__global__ void __launch_bounds__(JT)
-tree_attn_join_kernel(const __grid_constant__ Params p, int ctas) {
-    const int u = blockIdx.x, units = p.Hkv * p.row_tiles, n = u / units;
-    // steps before sequence n: summed as in the first kernel
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long before = 0, all = 0;
-    for (int i = tid; i < p.N; i += JT) {
-        const int st = span_of(p, i).steps;
-        all += st;
-        if (i < n) before += st;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    __shared__ long long part_all[JT / 32], part_before[JT / 32];
-    if (lane == 0) {
-        part_all[warp] = all;
-        part_before[warp] = before;
-    }
-    __syncthreads();
-    all = before = 0;
-    for (int i = 0; i < JT / 32; ++i) {
-        all += part_all[i];
-        before += part_before[i];
-    }
-    const long long total = all * units, parts = shares(total, ctas);
-    const int steps = span_of(p, n).steps;
-    const long long u0 = before * units + (long long)(u % units) * steps, u1 = u0 + steps;
-    // the CTAs that hold its first and last step
-    auto owner = [&](long long at) {
-        long long b = at * parts / total;
-        while (share_start(total, parts, b + 1) <= at) ++b;
-        while (share_start(total, parts, b) > at) --b;
-        return (int)b;
-    };
-    const int b0 = owner(u0), b1 = owner(u1 - 1);
-    if (b0 == b1) return;  // one CTA had all of it and wrote the result
-    const int kh = (u % units) / p.row_tiles, rt = u % p.row_tiles, R = p.M * p.group;
-    for (int r = blockIdx.y * JR + warp; r < (blockIdx.y + 1) * JR && rt * 128 + r < R; r += JT / 32) {
-        auto part_of = [&](int b) {
-            return p.part + (((size_t)b * 2 + (share_start(total, parts, b) > u0 ? 0 : 1)) * p.part_rows + r) * (D + 2);
-        };
-        float m = -INFINITY;
-        for (int b = b0; b <= b1; ++b) m = fmaxf(m, part_of(b)[D]);
-        float l = 0.f, acc[D / 32];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-        for (int b = b0; b <= b1; ++b) {
-            const float* q = part_of(b);
-            const float f = q[D + 1] > 0.f ? ex2(q[D] - m) : 0.f;
-            l += f * q[D + 1];
-#pragma unroll
-            for (int e = 0; e < D / 64; ++e) {
-                const float2 v = *reinterpret_cast<const float2*>(q + 64 * e + 2 * lane);
-                acc[2 * e] += f * v.x;
-                acc[2 * e + 1] += f * v.y;
-            }
-        }
-        const int row = rt * 128 + r, node = row / p.group, head = kh * p.group + row % p.group;
-        __nv_bfloat16* out = p.o + (((size_t)n * p.M + node) * p.Hq + head) * D;
-        const float inv = 1.f / l;
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e)
-            *reinterpret_cast<uint32_t*>(out + 64 * e + 2 * lane) = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    }
-}
-
 constexpr int kCtas = 148;  // one per SM
 
-size_t part_bytes(int M, int group, int d) {
-    const int rows = M * group < 128 ? M * group : 128;
-    return (size_t)kCtas * 2 * rows * (d + 2) * 4;
+// Workspace: the status word, the units' counters, the parts.
+size_t count_bytes(int N, int M, int Hq, int Hkv) {
+    return ((size_t)N * Hkv * ((M * (Hq / Hkv) + 127) / 128) * 4 + 255) & ~(size_t)255;
 }
+int part_rows(int M, int group) { return M * group < 128 ? M * group : 128; }
+int part_floats(int M, int group, int d) { return (part_rows(M, group) * (d + 2) + 3) & ~3; }
+size_t part_bytes(int M, int group, int d) { return (size_t)kCtas * 2 * part_floats(M, group, d) * 4; }
 
 template <int D>
 bool launch_attn(Params& a, const void* k, const void* v, cudaStream_t st) {
@@ -658,10 +727,13 @@ bool launch_attn(Params& a, const void* k, const void* v, cudaStream_t st) {
         !encode_head_map(&a.knode, k, (long long)a.N * a.M, a.Hkv, D, KT / 2) ||
         !encode_head_map(&a.vnode, v, (long long)a.N * a.M, a.Hkv, D, KT / 2))
         return false;
+    a.q_tma = a.scale > 0.f && 128 % a.group == 0;
+    if (a.q_tma && !encode_head_map(&a.qmap, a.q, (long long)a.N * a.M, a.Hq, D, 128 / a.group, a.group)) return false;
     const int smem = sizeof(Smem<D>) + 1024;
     cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    GDN_LAUNCH("tree_attn", st, (tree_attn_kernel<D><<<kCtas, kThreads, smem, st>>>(a)));
-    GDN_LAUNCH("tree_attn_join", st, (tree_attn_join_kernel<D><<<dim3((unsigned)(a.N * a.Hkv * a.row_tiles), (a.part_rows + JR - 1) / JR), JT, 0, st>>>(a, kCtas)));
+    const long long units = (long long)a.N * a.Hkv * a.row_tiles;
+    a.split = units * 2 <= kCtas ? (int)(kCtas / units) : 0;
+    GDN_LAUNCH("tree_attn", st, (tree_attn_kernel<D><<<a.split ? (unsigned)(units * a.split) : kCtas, kThreads, smem, st>>>(a)));
     return true;
 }
 
@@ -734,7 +806,7 @@ extern "C" {
 
 size_t gdn_tree_attn_workspace(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, int page, int width) {
     if (check(N, M, Hq, Hkv, d, dtype, 1, page, width) != GDN_OK) return 0;
-    return kStatusBytes + part_bytes(M, Hq / Hkv, d);
+    return kStatusBytes + count_bytes(N, M, Hq, Hkv) + part_bytes(M, Hq / Hkv, d);
 }
 
 gdn_status gdn_tree_attn(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, float scale, int window,
@@ -757,7 +829,8 @@ gdn_status gdn_tree_attn(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, 
         return GDN_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     cudaGetLastError();
-    if (cudaMemsetAsync(ws, 0, sizeof(unsigned int), st) != cudaSuccess) return GDN_ERR_CUDA;
+    const size_t counts = count_bytes(N, M, Hq, Hkv);
+    if (cudaMemsetAsync(ws, 0, kStatusBytes + counts, st) != cudaSuccess) return GDN_ERR_CUDA;
     const Cache c{(const __nv_bfloat16*)k_cache, (const __nv_bfloat16*)v_cache, block_table, cache_len, pages, page, width};
     Params a{};
     a.c = c;
@@ -765,8 +838,10 @@ gdn_status gdn_tree_attn(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, 
     a.row_tiles = (M * a.group + 127) / 128;
     a.window = window; a.scale = scale; a.parent = parent;
     a.q = (const __nv_bfloat16*)q; a.o = (__nv_bfloat16*)o;
-    a.part = (float*)((char*)ws + kStatusBytes);
-    a.part_rows = M * a.group < 128 ? M * a.group : 128;
+    a.count = (unsigned int*)((char*)ws + kStatusBytes);
+    a.part = (float*)((char*)ws + kStatusBytes + counts);
+    a.part_rows = part_rows(M, a.group);
+    a.part_floats = part_floats(M, a.group, d);
     a.status = (unsigned int*)ws;
     const bool fine = d == 64 ? launch_attn<64>(a, k, v, st) : launch_attn<128>(a, k, v, st);
     if (!fine) return GDN_ERR_CUDA;

@@ -75,7 +75,8 @@ def check(x, dev, scale, window=0, o=None):
 
 CASES = [([0], 1, 1, 1, 64, 16), ([1, 0, 5], 3, 2, 1, 128, 16), ([130, 127, 128], 5, 4, 2, 64, 32),
          ([33, 300], 16, 8, 2, 128, 64), ([257], 64, 4, 4, 128, 128), ([40, 129], 33, 6, 1, 64, 16),
-         ([515, 3], 1, 16, 2, 128, 64), ([200], 64, 16, 2, 64, 128)]
+         ([515, 3], 1, 16, 2, 128, 64), ([200], 64, 16, 2, 64, 128), ([1300, 900, 1111], 1, 5, 5, 64, 16),
+         ([900, 10], 3, 3, 1, 128, 32), ([640], 50, 6, 2, 64, 64)]
 
 
 @pytest.mark.parametrize("case", CASES)
@@ -89,6 +90,18 @@ def test_matches_oracle(dev, case, kind):
 def test_sliding_window(dev, window):
     x = poison(make([300, 64, 0, 131], 12, 4, 2, 64, 32, kind="kary", seed=2))
     check(x, dev, 0.125, window)
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0])
+def test_scales_that_are_not_positive(dev, scale):
+    check(poison(make([300, 5], 9, 4, 2, 64, 32, seed=12)), dev, scale)
+
+
+@pytest.mark.parametrize("N,M,Hq,Hkv", [(40, 3, 4, 4), (75, 1, 2, 1), (160, 2, 2, 2)])
+def test_many_sequences(dev, N, M, Hq, Hkv):
+    """Units for half the SMs and more: CTAs work on several, sequences of all lengths."""
+    lens = [(37 * n) % 300 for n in range(N)]
+    check(poison(make(lens, M, Hq, Hkv, 64, 32, kind="chain", seed=13)), dev, 0.125)
 
 
 def test_large_scores(dev):
