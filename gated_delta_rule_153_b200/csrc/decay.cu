@@ -416,21 +416,40 @@ decay_gate_kernel(Seqs q, int H, int nb, const float* __restrict__ g, const floa
     }
 }
 
-// Gradients of shared key heads: the sum over a group's value heads, in order.
+GDN_DEV void store8(float* to, const float (&x)[8]) {
+    reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+GDN_DEV void store8(__nv_bfloat16* to, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// Gradients of shared key heads: the sum over a group's value heads, in order.  One
+// thread per 8 channels of a row, dq and dk in one launch; bound by the reading of the
+// fp32 parts.
 template <typename T>
 __global__ void __launch_bounds__(256)
-decay_group_sum_kernel(Seqs q, int Hk, int rep, int d, const float* __restrict__ part, T* __restrict__ out) {
+decay_group_sum_kernel(Seqs q, int Hk, int rep, int d, const float* __restrict__ part_q, const float* __restrict__ part_k,
+                       T* __restrict__ dq, T* __restrict__ dk) {
     long long tok0;
     int n;
     if (!span_of(q, blockIdx.x, tok0, n)) return;
-    const size_t total = (size_t)n * Hk * d;
+    const float* part = blockIdx.z ? part_k : part_q;
+    T* out = blockIdx.z ? dk : dq;
+    const int sh = __ffs(d) - 4;  // d / 8 pieces per row, a power of two
+    const size_t total = ((size_t)n * Hk) << sh;
     for (size_t e = (size_t)blockIdx.y * 256 + threadIdx.x; e < total; e += (size_t)gridDim.y * 256) {
-        const size_t row = e / d;  // token * Hk + key head
-        const size_t c = e % d;
-        const float* src = part + ((size_t)tok0 * Hk + row) * rep * d + c;
-        float sum = 0.f;
-        for (int r = 0; r < rep; ++r) sum += src[(size_t)r * d];
-        out[((size_t)tok0 * Hk + row) * d + c] = from_f<T>(sum);
+        const size_t row = (size_t)tok0 * Hk + (e >> sh);  // token * Hk + key head
+        const int c = 8 * (int)(e & ((1u << sh) - 1));
+        const float4* src = reinterpret_cast<const float4*>(part + row * rep * d + c);
+        float sum[8] = {};
+#pragma unroll 2
+        for (int r = 0; r < rep; ++r, src += d / 4) {
+            const float4 x = __ldcs(src), y = __ldcs(src + 1);
+            sum[0] += x.x; sum[1] += x.y; sum[2] += x.z; sum[3] += x.w;
+            sum[4] += y.x; sum[5] += y.y; sum[6] += y.z; sum[7] += y.w;
+        }
+        store8(out + row * d + c, sum);
     }
 }
 
@@ -563,10 +582,7 @@ void run_bwd(const Problem& p, const void* q, const void* k, const void* v, cons
     GDN_LAUNCH("decay_gate", st, (decay_gate_kernel<<<dim3((unsigned)((long long)p.seq.nseq * p.H), chunks), 128, 0, st>>>(
         p.seq, p.H, row_blocks(p.dk), g, (const float*)(base + l.dotq), (const float*)(base + l.dotk),
         (const float*)(base + l.cross), dg)));
-    if (rep > 1) {
-        launch_group_sum(p, p.dk, (const float*)(base + l.dq), dq, st);
-        launch_group_sum(p, p.dk, (const float*)(base + l.dk), dk, st);
-    }
+    if (rep > 1) launch_group_sum(p, (const float*)(base + l.dq), (const float*)(base + l.dk), dq, dk, st);
 }
 
 template <typename T>
@@ -656,12 +672,13 @@ void run_step(int N, int H, int Hk, int dk, int dv, float scale, const void* q, 
 
 }  // namespace
 
-void launch_group_sum(const Problem& p, int d, const float* part, void* out, cudaStream_t st) {
-    const dim3 grid((unsigned)p.seq.nseq, spread(p, ((long long)(p.seq.cu ? p.seq.rows : p.seq.len) * p.Hk * d) / 1024 + 1));
+void launch_group_sum(const Problem& p, const float* part_q, const float* part_k, void* dq, void* dk, cudaStream_t st) {
+    const dim3 grid((unsigned)p.seq.nseq, spread(p, ((long long)(p.seq.cu ? p.seq.rows : p.seq.len) * p.Hk * p.dk) / 2048 + 1), 2);
+    const int rep = p.H / p.Hk;
     if (p.dtype == GDN_BF16)
-        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<<<grid, 256, 0, st>>>(p.seq, p.Hk, p.H / p.Hk, d, part, (__nv_bfloat16*)out)));
+        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<<<grid, 256, 0, st>>>(p.seq, p.Hk, rep, p.dk, part_q, part_k, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk)));
     else
-        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<<<grid, 256, 0, st>>>(p.seq, p.Hk, p.H / p.Hk, d, part, (float*)out)));
+        GDN_LAUNCH("decay_group_sum", st, (decay_group_sum_kernel<<<grid, 256, 0, st>>>(p.seq, p.Hk, rep, p.dk, part_q, part_k, (float*)dq, (float*)dk)));
 }
 
 size_t simt_fwd_workspace(const Problem& p) { return kStatusBytes + runs_bytes(p, cut(p, p.dv)); }

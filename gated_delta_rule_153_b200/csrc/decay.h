@@ -58,7 +58,7 @@ void launch_simt_bwd(const Problem& p, const void* q, const void* k, const void*
                      float* dg, float* dh0, void* ws, cudaStream_t st);
 
 // dq or dk of shared key heads: [token][H][d] fp32 summed over each group into [token][Hk][d].
-void launch_group_sum(const Problem& p, int d, const float* part, void* out, cudaStream_t st);
+void launch_group_sum(const Problem& p, const float* part_q, const float* part_k, void* dq, void* dk, cudaStream_t st);
 
 // Tensor cores: bf16 with dk, dv in {64, 128} (decay_walk.cu).  The launchers return
 // false if a tensor map could not be encoded (nothing launched).

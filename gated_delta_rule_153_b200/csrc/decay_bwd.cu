@@ -50,7 +50,7 @@ struct alignas(1024) Smem {
     Gates gate[2];
     float r[2][4][CT], c[2][4][CT], a[2][4][CT], b[2][4][CT];  // [chunk parity][column quarter][token]
     float col[kEpi][2][16];
-    uint64_t t_full, kv_full, s_full[2], gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, e3r, e3, o_done, e4, gfree[2],
+    uint64_t t_full, kv_full, s_full[2], gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, e3r, e3[2], o_done, e4, gfree[2],
         drain;
     uint32_t tmem;
 };
@@ -127,7 +127,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
     if (tid == 0) {
         for (uint64_t* b : {&s.t_full, &s.kv_full, &s.s_full[0], &s.s_full[1], &s.a_done, &s.x_done, &s.q_done, &s.a2_done, &s.x2_done, &s.o_done, &s.drain})
             mbar_init(b, 1);
-        for (uint64_t* b : {&s.zeroed, &s.e1, &s.e2, &s.e3r, &s.e3, &s.e4}) mbar_init(b, kEpi);
+        for (uint64_t* b : {&s.zeroed, &s.e1, &s.e2, &s.e3r, &s.e3[0], &s.e3[1], &s.e4}) mbar_init(b, kEpi);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.gfull[i], 32);
             mbar_init(&s.gfree[i], 1);
@@ -396,7 +396,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             tc5::wait_st();
             tc5::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.e3);
+            if (lane == 0) mbar_arrive(&s.e3[ph]);
             if (!(ok = warp_wait(&s.o_done, ph))) break;
             tc5::fence_after();
             put(tiles ? s.out_k() : nullptr, p.dk, TX, QK, DK);
@@ -578,7 +578,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                 ++ns[0];
                 ++ns[1];
             }
-            if (!(ok = warp_wait(&s.e3, ph))) break;  // K's rows are read by then too
+            if (!(ok = warp_wait(&s.e3[ph], (x >> 1) & 1))) break;  // K's rows are read by then too
             tc5::fence_after();
             if (un < units) {
                 load_kv(un, nx);
@@ -645,7 +645,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             const long long un = next_unit(u + gridDim.x, nx);
             // the other gates are free once the chunk before is done with them (its e3)
             if (un < units) form(un, nx, x + 1);
-            if (!(ok = warp_wait(&s.e3, ph))) break;
+            if (!(ok = warp_wait(&s.e3[ph], (x >> 1) & 1))) break;
             // dg: lane holds tokens 4 lane .. 4 lane + 3
             const int h = (int)(u % p.H);
             float y[4], b[4], sy = 0.f, sb = 0.f;
@@ -754,10 +754,7 @@ bool launch_tc_bwd(const Problem& p, const void* q, const void* k, const void* v
     else if (p.dk == 64) launch<64, 128>(a, p, st);
     else if (p.dv == 64) launch<128, 64>(a, p, st);
     else launch<128, 128>(a, p, st);
-    if (parts) {
-        launch_group_sum(p, p.dk, (const float*)(base + l.dq), dq, st);
-        launch_group_sum(p, p.dk, (const float*)(base + l.dk), dk, st);
-    }
+    if (parts) launch_group_sum(p, (const float*)(base + l.dq), (const float*)(base + l.dk), dq, dk, st);
     return true;
 }
 

@@ -64,8 +64,9 @@ struct alignas(1024) Smem {
     unsigned char S[DK * 128];   // the entering state in bf16, [key channel][64 value channels]
     Gates gate[NST];
     float col[kEpi][CT];         // per warp of P: the column factors of its decays
-    uint64_t full[NST], gfull[NST], gfree[NST];
-    uint64_t img_ready, img_free, q_full, a_done, p_ready, vt_ready, n_done, s_ready, x_done, o_done, o_free, drain;
+    // of each stage, so that nobody who waits for one can fall two phases behind
+    uint64_t full[NST], gfull[NST], gfree[NST], n_done[NST], o_done[NST];
+    uint64_t img_ready, img_free, q_full, a_done, p_ready, vt_ready, s_ready, x_done, o_free, drain;
     uint32_t tmem;
 };
 
@@ -118,6 +119,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&s.full[i], 1);
+            mbar_init(&s.n_done[i], 1);
+            mbar_init(&s.o_done[i], 1);
             mbar_init(&s.gfull[i], 32);
             mbar_init(&s.gfree[i], (MODE == 0 ? kEpi : 0) + kState + kSplit<MODE>);
         }
@@ -127,10 +130,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
         mbar_init(&s.vt_ready, kSplit<MODE>);
-        mbar_init(&s.n_done, 1);
         mbar_init(&s.s_ready, kState);
         mbar_init(&s.x_done, 1);
-        mbar_init(&s.o_done, 1);
         mbar_init(&s.o_free, kEpi);
         mbar_init(&s.drain, 1);
         fence_mbar_init();
@@ -156,7 +157,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.gfree[st]);
             if (!warp_wait(&s.full[st], (c / NST) & 1)) break;
-            if (c > 0 && !warp_wait(&s.n_done, (c - 1) & 1)) break;  // N(c-1) is done with the terms before
+            if (c > 0 && !warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1)) break;  // N(c-1) is done with the terms before
 #pragma unroll 1
             for (int q = 0; q < PIECES; ++q) {
                 const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q));
@@ -237,19 +238,19 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                             a[q] = 16 * J + q <= i ? a[q] * d : 0.f;
                         }
                     } else {
-                    const float4* cf = reinterpret_cast<const float4*>(col + 16 * J);
+                        const float4* cf = reinterpret_cast<const float4*>(col + 16 * J);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float4 w = cf[q];
-                        mul2(w.x, w.y, w.x, w.y, f, f);
-                        mul2(w.z, w.w, w.z, w.w, f, f);
-                        mul2(a[4 * q], a[4 * q + 1], a[4 * q], a[4 * q + 1], w.x, w.y);
-                        mul2(a[4 * q + 2], a[4 * q + 3], a[4 * q + 2], a[4 * q + 3], w.z, w.w);
-                    }
-                    if (diag) {
+                        for (int q = 0; q < 4; ++q) {
+                            float4 w = cf[q];
+                            mul2(w.x, w.y, w.x, w.y, f, f);
+                            mul2(w.z, w.w, w.z, w.w, f, f);
+                            mul2(a[4 * q], a[4 * q + 1], a[4 * q], a[4 * q + 1], w.x, w.y);
+                            mul2(a[4 * q + 2], a[4 * q + 3], a[4 * q + 2], a[4 * q + 3], w.z, w.w);
+                        }
+                        if (diag) {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) a[q] = 16 * J + q <= i ? a[q] : 0.f;
-                    }
+                            for (int q = 0; q < 16; ++q) a[q] = 16 * J + q <= i ? a[q] : 0.f;
+                        }
                     }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) pk[q] = pack_bf16(a[2 * q], a[2 * q + 1]);
@@ -267,7 +268,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     mbar_arrive(&s.p_ready);
                     mbar_arrive(&s.gfree[st]);
                 }
-                if (!warp_wait(&s.o_done, c & 1)) break;
+                if (!warp_wait(&s.o_done[st], (c / NST) & 1)) break;
                 tc5::fence_after();
                 // lanes 2m, 2m+1 trade 16-byte pieces, so that each store instruction
                 // writes whole 32-byte sectors: first row 2m, then row 2m + 1
@@ -342,7 +343,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
             if (c > 0) {  // S entering chunk c; X(c-1), which read the last one, came before N(c-1)
-                if (!(ok = warp_wait(&s.n_done, (c - 1) & 1))) break;
+                if (!(ok = warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1))) break;
                 tc5::fence_after();
                 add_n();
             }
@@ -404,7 +405,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             ++done;
         }
         if (ok && nc > 0) {
-            if (warp_wait(&s.n_done, (nc - 1) & 1)) {
+            if (warp_wait(&s.n_done[(nc - 1) % NST], ((nc - 1) / NST) & 1)) {
                 tc5::fence_after();
                 add_n();
             }
@@ -425,14 +426,14 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             int c = 0, nq = 0;
             for (; c < nc; ++c) {
                 // each operand goes in as soon as the products are done with the last in its place
-                const int st = c % NST, ph = (c - NST) & 1;
+                const int st = c % NST, ph = (c / NST - 1) & 1;
                 auto& q = s.st[st];
                 const int tok = (int)(tok0 + (long long)chunk_of(c) * CT), kh = h / p.rep;
-                if (c >= NST && !wait_for(&s.n_done, ph)) break;
+                if (c >= NST && !wait_for(&s.n_done[st], ph)) break;
                 mbar_arrive_expect(&s.full[st], (DK / 64 + 1) * PANEL);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x) tma_load_3d(q.K[x], &p.kmap, 64 * x, kh, tok, &s.full[st]);
-                if (MODE == 0 && c >= NST && !wait_for(&s.o_done, ph)) {
+                if (MODE == 0 && c >= NST && !wait_for(&s.o_done[st], ph)) {
                     ++c;  // K's copies are in flight, V's will not come
                     break;
                 }
@@ -500,7 +501,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             if (elect_one()) {
 #pragma unroll 2
                 for (int k = 0; k < CT / 16; ++k) tc5::mma(tm + TN, dKt + k * KROWS, dVt + k * KROWS, ID_N, k > 0);
-                tc5::commit(&s.n_done);
+                tc5::commit(&s.n_done[st]);
             }
             __syncwarp();
             if constexpr (MODE == 0) {
@@ -509,7 +510,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 if (elect_one()) {
 #pragma unroll 2
                     for (int k = 0; k < CT / 16; ++k) tc5::mma_ts(tm + TY, tm + TP + 8 * k, dV + k * KROWS, ID_X, k > 0);
-                    tc5::commit(&s.o_done);
+                    tc5::commit(&s.o_done[st]);
                 }
                 __syncwarp();
             }
