@@ -45,7 +45,6 @@ namespace decay {
 namespace {
 
 constexpr int TT = 32;          // tokens per tile
-constexpr int WT = 128;         // threads per CTA
 constexpr int RB = 64;          // rows of R per CTA
 constexpr int AC = 64;          // tokens per chunk of the gate gradient
 
@@ -77,6 +76,7 @@ struct Walk {
     // Few chains are cut into runs of `len` tiles: first what each run adds to a zero R
     // and its decay (MAP), then all runs at once, each from what the ones before leave.
     int runs, len;
+    bool wide;              // at most one CTA per SM: 256 threads
     float *runR, *runA;     // [chain][run][RD][CD] and [chain][run]
     unsigned int* status;
 };
@@ -107,22 +107,24 @@ struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in dif
     float x[TT][CD + 4], w[TT][CD + 4], y[TT][RB + 4], z[TT][RB + 4], p[TT][TT + 4];
     float r[CD][RB + 4];
     float2 g[TT];
-    float f[TT], h[TT], own[TT], red[WT / 32];
+    float f[TT], h[TT], own[TT], red[8];
 };
 
-template <int CD, typename T, bool REV, bool MAP>
+// WT threads.  With 256 the next tile's loads are on their way while this one is worked on.
+template <int CD, typename T, bool REV, bool MAP, int WT>
 __global__ void __launch_bounds__(WT)
 decay_walk_kernel(const Walk p) {
     extern __shared__ __align__(16) unsigned char raw[];
     WalkSmem<CD>& s = *reinterpret_cast<WalkSmem<CD>*>(raw);
     using F = Four<T>;
     constexpr int NX = TT * CD / 4 / WT > 0 ? TT * CD / 4 / WT : 1;  // groups of four per thread and tile
-    constexpr int NC = CD / 8;                                       // columns of R per thread
-    constexpr int NY = TT * RB / 4 / WT;
-    const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
+    constexpr int NC = CD * 16 / WT;                                 // columns of R per thread
+    constexpr int NY = TT * RB / 4 / WT, NT = TT * 16 / WT;
+    const int h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long tok0;
-    int n;
+    int n, seq, run;
+    if (!item_of(p.seq, p.runs, p.len * TT, MAP ? 1 : 0, blockIdx.x / p.H, seq, run)) return;
     if (!span_of(p.seq, seq, tok0, n)) {
         if (tid == 0) atomicOr(p.status, 2u);
         return;
@@ -130,9 +132,9 @@ decay_walk_kernel(const Walk p) {
     const size_t sh = (size_t)seq * p.H + h;
     const long long slot0 = tok0 / AC + seq;
     const int tiles = (n + TT - 1) / TT;
-    const int i0 = blockIdx.z * p.len, i1 = min(tiles, i0 + p.len);  // this run, in the order of the walk
+    const int i0 = run * p.len, i1 = min(tiles, i0 + p.len);  // this run, in the order of the walk
     // the run that ends the chain (the first of an empty one) writes the last state
-    const bool ends = i1 == tiles && (blockIdx.z == 0 || i0 < tiles);
+    const bool ends = i1 == tiles && (run == 0 || i0 < tiles);
     if (MAP ? i1 >= tiles : i0 >= tiles && !ends) return;
     // R, column-major; from run 1 on with what the runs before this one leave
 #pragma unroll 8
@@ -140,33 +142,41 @@ decay_walk_kernel(const Walk p) {
         const int c = p.init_t ? e / RB : e % CD, r = p.init_t ? e % RB : e / CD, row = r0 + r;
         s.r[c][r] = MAP || !p.init || row >= p.RD ? 0.f : __ldg(p.init + (p.init_t ? (sh * CD + c) * p.RD + row : (sh * p.RD + row) * CD + c));
     }
-    if (!MAP && blockIdx.z > 0) {
+    if (!MAP && run > 0) {
         __syncthreads();
-        for (int q = 0; q < blockIdx.z; ++q) {
-            const float f = __ldg(p.runA + sh * p.runs + q), *from = p.runR + ((sh * p.runs + q) * p.RD + r0) * CD;
-#pragma unroll 8
-            for (int e = tid; e < CD * RB; e += WT) {
-                const int c = e % CD, r = e / CD;
-                if (r0 + r < p.RD) s.r[c][r] = f * s.r[c][r] + __ldg(from + (size_t)r * CD + c);
+        // R <- prod a_q R + sum_q (prod_{p > q} a_p) N_q
+        float f = 1.f, mine[CD * RB / WT];
+        const float *a = p.runA + sh * p.runs, *from = p.runR + (sh * p.runs * p.RD + r0) * CD;
+#pragma unroll
+        for (int i = 0; i < CD * RB / WT; ++i) mine[i] = 0.f;
+#pragma unroll 1
+        for (int q = run - 1; q >= 0; --q, f *= __ldg(a + q + 1)) {
+#pragma unroll
+            for (int i = 0; i < CD * RB / WT; ++i) {
+                const int e = tid + WT * i;
+                if (r0 + e / CD < p.RD) mine[i] = fmaf(f, __ldg(from + (size_t)q * p.RD * CD + e), mine[i]);
             }
+        }
+#pragma unroll
+        for (int i = 0; i < CD * RB / WT; ++i) {
+            const int e = tid + WT * i;
+            s.r[e % CD][e / CD] = fmaf(f, s.r[e % CD][e / CD], mine[i]);
         }
     }
     float all = 1.f;  // the decay of the run so far
     const bool has_z = !MAP && p.dots != nullptr;
-    for (int it = i0; it < i1; ++it) {
-        const int tile = REV ? tiles - 1 - it : it;
-        const int m = min(TT, n - tile * TT);
+    constexpr bool AHEAD = WT == 256;
+    const int r = 4 * (tid % 16);  // this thread's rows of R
+    typename F::Raw vx[NX], vw[NX], vy[NY], vz[NY];  // all on their way before any is put down
+    float pg = 0.f;
+    auto fetch = [&](int it) {
+        const int tile = REV ? tiles - 1 - it : it, m = min(TT, n - tile * TT);
         const long long t0 = tok0 + (long long)tile * TT;
-        const int end = tile * TT + m;
-        const bool border = end % AC == 0 || end == n;  // the tile ends a chunk
-        const long long slot = slot0 + (end - 1) / AC;
-        const int r = 4 * (tid % 16);  // this thread's rows of R
         const typename F::Raw zero{};
         auto get = [&](const Operand& o, int t, int c, bool in) {
             return in ? __ldg(reinterpret_cast<const typename F::Raw*>((const T*)o.p + row_of(o, t0 + t, h) + c)) : zero;
         };
-        const float pg = warp == 0 && lane < m ? __ldg(p.g + (size_t)(t0 + lane) * p.H + h) : 0.f;
-        typename F::Raw vx[NX], vw[NX], vy[NY], vz[NY];  // all on their way before any is put down
+        pg = warp == 0 && lane < m ? __ldg(p.g + (size_t)(t0 + lane) * p.H + h) : 0.f;
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
@@ -175,20 +185,31 @@ decay_walk_kernel(const Walk p) {
         }
 #pragma unroll
         for (int i = 0; i < NY; ++i) {
-            const int t = tid / 16 + 8 * i;
+            const int t = tid / 16 + WT / 16 * i;
             vy[i] = get(p.y, t, r0 + r, t < m && r0 + r < p.RD);
             if (has_z) vz[i] = get(p.z, t, r0 + r, t < m && r0 + r < p.RD);
         }
+    };
+    if (AHEAD && i0 < i1) fetch(i0);
+    for (int it = i0; it < i1; ++it) {
+        const int tile = REV ? tiles - 1 - it : it;
+        const int m = min(TT, n - tile * TT);
+        const long long t0 = tok0 + (long long)tile * TT;
+        const int end = tile * TT + m;
+        const bool border = end % AC == 0 || end == n;  // the tile ends a chunk
+        const long long slot = slot0 + (end - 1) / AC;
+        if (!AHEAD) fetch(it);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             const int e = 4 * (tid + WT * i), t = e / CD, c = e % CD;
+            if (TT * CD / 4 < WT && t >= TT) break;
             if (!MAP) *reinterpret_cast<float4*>(&s.x[t][c]) = F::of(vx[i]);
             *reinterpret_cast<float4*>(&s.w[t][c]) = F::of(vw[i]);
         }
 #pragma unroll
         for (int i = 0; i < NY; ++i) {
-            const int t = tid / 16 + 8 * i;
+            const int t = tid / 16 + WT / 16 * i;
             const float4 v = F::of(vy[i]);
             *reinterpret_cast<float4*>(&s.y[t][r]) = make_float4(p.c_y * v.x, p.c_y * v.y, p.c_y * v.z, p.c_y * v.w);
             if (has_z) *reinterpret_cast<float4*>(&s.z[t][r]) = F::of(vz[i]);
@@ -208,42 +229,43 @@ decay_walk_kernel(const Walk p) {
             s.h[lane] = REV ? a : b;
         }
         __syncthreads();
+        if (AHEAD && it + 1 < i1) fetch(it + 1);
         if constexpr (!MAP) {
-            {   // p[t][u] = D_tu (w_u . x_t) for t = tid / 8 + 16 i, u = tid % 8 + 8 j (neighbouring
-                // lanes read neighbouring rows, which are in different banks), its diagonal apart
-                const int ta = tid / 8, ua = tid % 8;
-                float a[2][4] = {};
+            {   // p[t][u] = D_tu (w_u . x_t) for t = tid / 16 + WT / 16 i, u = tid % 16 + 16 j (neighbouring
+                // lanes read neighbouring rows, which are in different banks), its diagonal apart;
+                // even and odd channels are added up apart
+                const int ta = tid / 16, ua = tid % 16;
+                float2 a[NT][2] = {};
 #pragma unroll 2
                 for (int c = 0; c < CD; c += 4) {
-                    float4 xv[2], wv[4];
+                    float4 xv[NT], wv[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[ta + 16 * i][c]);
+                    for (int i = 0; i < NT; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[ta + WT / 16 * i][c]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) wv[j] = *reinterpret_cast<const float4*>(&s.w[ua + 8 * j][c]);
+                    for (int j = 0; j < 2; ++j) wv[j] = *reinterpret_cast<const float4*>(&s.w[ua + 16 * j][c]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            a[i][j] = fmaf(xv[i].x, wv[j].x, a[i][j]);
-                            a[i][j] = fmaf(xv[i].y, wv[j].y, a[i][j]);
-                            a[i][j] = fmaf(xv[i].z, wv[j].z, a[i][j]);
-                            a[i][j] = fmaf(xv[i].w, wv[j].w, a[i][j]);
+                        for (int j = 0; j < 2; ++j) {
+                            fma2(a[i][j].x, a[i][j].y, xv[i].x, xv[i].y, wv[j].x, wv[j].y, a[i][j].x, a[i][j].y);
+                            fma2(a[i][j].x, a[i][j].y, xv[i].z, xv[i].w, wv[j].z, wv[j].w, a[i][j].x, a[i][j].y);
                         }
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int t = ta + 16 * i, u = ua + 8 * j;
-                        if (t == u) s.own[t] = a[i][j];
+                    for (int j = 0; j < 2; ++j) {
+                        const int t = ta + WT / 16 * i, u = ua + 16 * j;
+                        const float d = a[i][j].x + a[i][j].y;
+                        if (t == u) s.own[t] = d;
                         const bool in = REV ? u > t : u < t;
-                        s.p[t][u] = in ? a[i][j] * (REV ? pair_decay(s.g[u], s.g[t]) : pair_decay(s.g[t], s.g[u])) : 0.f;
+                        s.p[t][u] = in ? d * (REV ? pair_decay(s.g[u], s.g[t]) : pair_decay(s.g[t], s.g[u])) : 0.f;
                     }
             }
             __syncthreads();
-            // out: 4 tokens x 4 rows
-            const int tb = 4 * (tid / 16);
-            float a[4][4] = {};
+            // out: NT tokens x 4 rows
+            const int tb = NT * (tid / 16);
+            float a[NT][4] = {};
             auto add = [&](float (&o)[4], float q, const float4& v) {
                 o[0] = fmaf(q, v.x, o[0]);
                 o[1] = fmaf(q, v.y, o[1]);
@@ -252,14 +274,13 @@ decay_walk_kernel(const Walk p) {
             };
 #pragma unroll 2
             for (int c = 0; c < CD; c += 4) {
-                float4 xv[4], rv[4];
+                float4 xv[NT], rv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    xv[i] = *reinterpret_cast<const float4*>(&s.x[tb + i][c]);
-                    rv[i] = *reinterpret_cast<const float4*>(&s.r[c + i][r]);
-                }
+                for (int i = 0; i < NT; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[tb + i][c]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) rv[i] = *reinterpret_cast<const float4*>(&s.r[c + i][r]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
                     add(a[i], xv[i].x, rv[0]);
                     add(a[i], xv[i].y, rv[1]);
                     add(a[i], xv[i].z, rv[2]);
@@ -267,21 +288,20 @@ decay_walk_kernel(const Walk p) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NT; ++i) {
                 const float f = s.f[tb + i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[i][j] *= f;
             }
 #pragma unroll 2
             for (int u = 0; u < TT; u += 4) {
-                float4 pv[4], yv[4];
+                float4 pv[NT], yv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    pv[i] = *reinterpret_cast<const float4*>(&s.p[tb + i][u]);
-                    yv[i] = *reinterpret_cast<const float4*>(&s.y[u + i][r]);
-                }
+                for (int i = 0; i < NT; ++i) pv[i] = *reinterpret_cast<const float4*>(&s.p[tb + i][u]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) yv[i] = *reinterpret_cast<const float4*>(&s.y[u + i][r]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
                     add(a[i], pv[i].x, yv[0]);
                     add(a[i], pv[i].y, yv[1]);
                     add(a[i], pv[i].z, yv[2]);
@@ -289,7 +309,7 @@ decay_walk_kernel(const Walk p) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NT; ++i) {
                 const int t = tb + i;
                 const size_t row = (size_t)(t0 + t) * p.H + h;
                 if (has_z) {
@@ -367,7 +387,7 @@ decay_walk_kernel(const Walk p) {
             }
         }
     }
-    float* const to = MAP ? p.runR + ((sh * p.runs + blockIdx.z) * p.RD) * CD : p.last && ends ? p.last + sh * p.RD * CD : nullptr;
+    float* const to = MAP ? p.runR + ((sh * p.runs + run) * p.RD) * CD : p.last && ends ? p.last + sh * p.RD * CD : nullptr;
     if (to) {
         __syncthreads();
         for (int e = tid; e < CD * RB; e += WT) {
@@ -375,7 +395,7 @@ decay_walk_kernel(const Walk p) {
             if (r0 + r < p.RD) to[(size_t)(r0 + r) * CD + c] = s.r[c][r];
         }
     }
-    if (MAP && tid == 0 && blockIdx.y == 0) p.runA[sh * p.runs + blockIdx.z] = all;
+    if (MAP && tid == 0 && blockIdx.y == 0) p.runA[sh * p.runs + run] = all;
 }
 
 // dg of one chunk per warp: the suffix sums of q.dq' - k.dk' and the chunk end's <S, dS>.
@@ -453,52 +473,56 @@ decay_group_sum_kernel(Seqs q, int Hk, int rep, int d, const float* __restrict__
     }
 }
 
+template <int CD, typename T, bool REV, int WT>
+void launch_walk_of(const Walk& w, cudaStream_t st) {
+    const auto grid = [&](int runs) { return dim3((unsigned)(items(w.seq, runs, w.len * TT) * w.H), (w.RD + RB - 1) / RB); };
+    const int smem = sizeof(WalkSmem<CD>);
+    if (w.runs > 1) {
+        cudaFuncSetAttribute(decay_walk_kernel<CD, T, REV, true, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        GDN_LAUNCH("decay_map", st, (decay_walk_kernel<CD, T, REV, true, WT><<<w.seq.cu ? grid(w.runs) : grid(w.runs - 1), WT, smem, st>>>(w)));
+    }
+    cudaFuncSetAttribute(decay_walk_kernel<CD, T, REV, false, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    GDN_LAUNCH(REV ? "decay_walk_rev" : "decay_walk", st, (decay_walk_kernel<CD, T, REV, false, WT><<<grid(w.runs), WT, smem, st>>>(w)));
+}
+
 template <typename T, bool REV>
 void launch_walk(const Walk& w, int CD, cudaStream_t st) {
-    auto go = [&](auto cd, const char* name) {
-        constexpr int C = decltype(cd)::value;
-        dim3 grid((unsigned)((long long)w.seq.nseq * w.H), (w.RD + RB - 1) / RB, w.runs);
-        const int smem = sizeof(WalkSmem<C>);
-        if (w.runs > 1) {
-            const dim3 maps(grid.x, grid.y, w.runs - 1);
-            cudaFuncSetAttribute(decay_walk_kernel<C, T, REV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            GDN_LAUNCH("decay_map", st, (decay_walk_kernel<C, T, REV, true><<<maps, WT, smem, st>>>(w)));
-        }
-        cudaFuncSetAttribute(decay_walk_kernel<C, T, REV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        GDN_LAUNCH(name, st, (decay_walk_kernel<C, T, REV, false><<<grid, WT, smem, st>>>(w)));
-    };
-    const char* name = REV ? "decay_walk_rev" : "decay_walk";
     switch (CD) {
-        case 16: go(std::integral_constant<int, 16>{}, name); break;
-        case 32: go(std::integral_constant<int, 32>{}, name); break;
-        case 64: go(std::integral_constant<int, 64>{}, name); break;
-        default: go(std::integral_constant<int, 128>{}, name); break;
+        case 16: launch_walk_of<16, T, REV, 256>(w, st); break;
+        case 32: launch_walk_of<32, T, REV, 256>(w, st); break;
+        case 64: launch_walk_of<64, T, REV, 256>(w, st); break;
+        default:
+            if (w.wide) launch_walk_of<128, T, REV, 256>(w, st);
+            else launch_walk_of<128, T, REV, 128>(w, st);
     }
 }
 
 int row_blocks(int RD) { return (RD + RB - 1) / RB; }
 
-// Runs per chain, of whole chunks: 1 when the chains fill the device.  Two launches
-// and the first one's pass over the states cost about four tiles, a tile of it a third
-// of one of the walk.
+// Runs per chain, of whole chunks: 1 when the chains fill the device.  Estimated in
+// tiles on the critical path: a tile of the map costs a third of one of the walk, the
+// second launch about four, and adding up what the runs before leave 0.1 each.  Packed
+// sequences have rows / length + nseq runs together, however long the longest is.
 struct Cut {
     int runs, len;
+    long long ctas;  // with something to do
 };
 Cut cut(const Problem& p, int RD) {
     const int tiles = ((p.seq.cu ? p.seq.rows : p.seq.len) + TT - 1) / TT;
-    const long long ctas = (long long)p.seq.nseq * p.H * row_blocks(RD);
+    const long long heads = (long long)p.H * row_blocks(RD);
     auto waves = [](long long n) { return (double)((n + 295) / 296); };  // two CTAs per SM
-    Cut best{1, std::max(tiles, 1)};
-    double cost = tiles * waves(ctas);
-    for (int r = 2; r <= 16; ++r) {
+    Cut best{1, std::max(tiles, 1), heads * p.seq.nseq};
+    double cost = tiles * waves(heads * p.seq.nseq);
+    for (int r = 2; r <= 64; ++r) {
         int len = (tiles + r - 1) / r;
         len += len % 2;  // whole chunks of the gate gradient
         const int runs = (tiles + len - 1) / len;
         if (runs < 2) break;
-        const double c = len * (waves(ctas * runs) + waves(ctas * (runs - 1)) / 3) + 4;
+        const long long all = heads * items(p.seq, runs, len * TT);
+        const double c = len * waves(all) * 4 / 3 + 4 + 0.1 * runs;
         if (c < 0.9 * cost) {
             cost = c;
-            best = Cut{runs, len};
+            best = Cut{runs, len, all};
         }
     }
     return best;
@@ -511,6 +535,7 @@ size_t runs_bytes(const Problem& p, const Cut& c) {
 void set_runs(Walk& w, const Problem& p, const Cut& c, void* at) {
     w.runs = c.runs;
     w.len = c.len;
+    w.wide = c.ctas <= 148;
     w.runR = (float*)at;
     w.runA = w.runR + (size_t)p.seq.nseq * p.H * c.runs * p.dk * p.dv;
 }

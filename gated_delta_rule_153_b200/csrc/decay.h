@@ -30,6 +30,11 @@ struct Problem {
 // never meet, whatever their lengths, so no prefix sum over them is needed.
 __host__ __device__ inline long long chunk_slots(const Seqs& q, int C) { return q.rows / C + (long long)q.nseq; }
 
+// Items of a grid (item_of): each with one CTA per head and block of value channels.
+inline long long items(const Seqs& q, int runs, int run_len) {
+    return q.cu && runs > 1 ? q.rows / run_len + (long long)q.nseq : (long long)q.nseq * runs;
+}
+
 #ifdef __CUDACC__
 // The token range of sequence s.  False if its offsets are not one: out of the
 // row, decreasing, or below the offset before them (it would then share tokens
@@ -42,6 +47,40 @@ __device__ __forceinline__ bool span_of(const Seqs& q, int s, long long& tok0, i
     tok0 = a;
     n = b - a;
     return !(a < 0 || b < a || b > q.rows || (s > 0 && q.cu[s - 1] > a));
+}
+
+// Chains cut into runs of `run_len` tokens: the sequence and run of a CTA's item.  A batch
+// has the items of run 0 first, then those of run 1; packed sequences have theirs one
+// sequence after the other, so that the CTAs with something to do are neighbours and
+// the device spreads them evenly: at most rows / run_len + nseq of them, all of a grid.
+// `skip` leaves out the last runs.  Called by whole warps; false past the end.
+__device__ __forceinline__ bool item_of(const Seqs& q, int runs, int run_len, int skip, int item, int& seq, int& run) {
+    if (!q.cu || runs == 1) {
+        seq = item % q.nseq;
+        run = item / q.nseq;
+        return true;
+    }
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < q.nseq; s0 += 32) {
+        long long tok0;
+        int n, mine = 0;
+        if (s0 + lane < q.nseq)  // a sequence whose offsets are none has one, to say so
+            mine = span_of(q, s0 + lane, tok0, n) && n > run_len ? (n + run_len - 1) / run_len - skip : 1 - skip;
+        int upto = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, upto > item);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            seq = s0 + at;
+            run = item - __shfl_sync(0xffffffffu, upto - mine, at);
+            return true;
+        }
+        item -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
 }
 #endif
 

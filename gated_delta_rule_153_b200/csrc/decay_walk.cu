@@ -96,10 +96,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem<DK>& s = *reinterpret_cast<Smem<DK>*>(align1k(raw));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int vb = blockIdx.y, run = blockIdx.z;
-    const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int vb = blockIdx.y, h = blockIdx.x % p.H;
     long long tok0;
-    int n;
+    int n, seq, run;
+    if (!item_of(p.seq, p.runs, p.len * CT, MODE == 1 ? 1 : 0, blockIdx.x / p.H, seq, run)) return;
     if (!span_of(p.seq, seq, tok0, n)) {
         if (tid == 0) atomicOr(p.status, 2u);
         return;
@@ -319,6 +319,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) S[e] = h0 ? h0[(size_t)e * DK] : 0.f;
         if (MODE != 1 && own) {
+#pragma unroll 1
             for (int q = 0; q < run; ++q) {  // what the runs before this one leave
                 const float a = p.runG[chain * p.runs + q];
                 const float* N = p.runS + ((chain * gridDim.y + vb) * p.runs + q) * slab + (size_t)(32 * half) * DK + r;
@@ -569,28 +570,28 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
 
 // Runs per chain: 1 when the chains fill the device; otherwise the number that
 // gives the shortest estimated time, in chunk steps on the critical path.  A
-// step of the walk costs about 1, one of the map (MODE 1) about 0.7, and the
-// second launch about 4.
+// step of the walk costs about 1, one of the map (MODE 1) about 0.7, the second launch
+// about 2, and adding up what the runs before leave 0.2 each.  Packed sequences have
+// rows / length + nseq runs together, however long the longest is.
 struct Cut {
     int runs, len;
 };
-Cut cut(long long ctas, int chunks) {
+Cut cut_of(const Problem& p) {
+    const int chunks = ((p.seq.cu ? p.seq.rows : p.seq.len) + CT - 1) / CT, nseq = p.seq.nseq;
+    const long long heads = (long long)p.H * (p.dv / NB);
     Cut best{1, std::max(chunks, 1)};
     auto waves = [](long long n) { return (double)((n + 147) / 148); };
-    double cost = chunks * waves(ctas);
-    for (int r = 2; r <= 16 && r <= chunks; ++r) {
+    double cost = chunks * waves(heads * nseq);
+    for (int r = 2; r <= 64 && r <= chunks; ++r) {
         const int len = (chunks + r - 1) / r, runs = (chunks + len - 1) / len;
-        const double c = len * (waves(ctas * runs) + 0.7 * waves(ctas * (runs - 1))) + 4;
+        const long long all = heads * items(p.seq, runs, len * CT), maps = p.seq.cu ? all : all - heads * nseq;
+        const double c = len * (waves(all) + 0.7 * waves(maps)) + 2 + 0.2 * runs;
         if (c < 0.9 * cost) {
             cost = c;
             best = Cut{runs, len};
         }
     }
     return best;
-}
-
-Cut cut_of(const Problem& p) {
-    return cut((long long)p.seq.nseq * p.H * (p.dv / NB), ((p.seq.cu ? p.seq.rows : p.seq.len) + CT - 1) / CT);
 }
 
 template <int MODE, bool REV>
@@ -627,9 +628,9 @@ Params params_of(const Problem& p, const Cut& c, const float* g, void* runs, voi
 // All runs of a call: with more than one, first what each leaves.
 template <int MODE, bool REV>
 void launch_runs(const Params& a, const Problem& p, cudaStream_t st) {
-    const dim3 grid((unsigned)((size_t)p.seq.nseq * p.H), p.dv / NB, a.runs);
-    if (a.runs > 1) launch<1, REV>(a, p.dk, dim3(grid.x, grid.y, a.runs - 1), st);
-    launch<MODE, REV>(a, p.dk, grid, st);
+    const auto grid = [&](int runs) { return dim3((unsigned)(items(p.seq, runs, a.len * CT) * p.H), p.dv / NB); };
+    if (a.runs > 1) launch<1, REV>(a, p.dk, p.seq.cu ? grid(a.runs) : grid(a.runs - 1), st);
+    launch<MODE, REV>(a, p.dk, grid(a.runs), st);
 }
 
 }  // namespace
