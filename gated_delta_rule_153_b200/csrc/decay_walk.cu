@@ -54,19 +54,21 @@ template <int MODE>
 constexpr int kThreads = 32 * (kEpi + kState + 3 + (MODE == 0 ? 4 : MODE == 2 ? 1 : 0));
 constexpr int NST = 2;
 
-template <int DK>
+template <int DK, int MODE>
 struct alignas(1024) Smem {
-    unsigned char Q[DK / 64][PANEL];
+    unsigned char Q[DK / 64][PANEL];  // MODE 2: the state's image on its way out
     struct Stage {
         unsigned char K[DK / 64][PANEL], V[PANEL];
     } st[NST];
     unsigned char Vt[3][PANEL];  // decayed V, three bf16 terms
-    unsigned char S[DK * 128];   // the entering state in bf16, [key channel][64 value channels]
+    // MODE 0: the entering state in bf16, [key channel][64 value channels]; MODE 2 backwards:
+    // the two terms of the forward state at the chunk's start
+    unsigned char S[MODE == 2 ? 2 : 1][DK * 128];
     Gates gate[NST];
     float col[kEpi][CT];         // per warp of P: the column factors of its decays
     // of each stage, so that nobody who waits for one can fall two phases behind
     uint64_t full[NST], gfull[NST], gfree[NST], n_done[NST], o_done[NST];
-    uint64_t img_ready, img_free, q_full, a_done, p_ready, vt_ready, s_ready, x_done, o_free, drain;
+    uint64_t img_ready, img_free, fwd_full, fwd_free, q_full, a_done, p_ready, vt_ready, s_ready, x_done, o_free, drain;
     uint32_t tmem;
 };
 
@@ -94,7 +96,7 @@ template <int DK, int MODE, bool REV>
 __global__ void __launch_bounds__(kThreads<MODE>, 1)
 decay_tc_walk_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) unsigned char raw[];
-    Smem<DK>& s = *reinterpret_cast<Smem<DK>*>(align1k(raw));
+    Smem<DK, MODE>& s = *reinterpret_cast<Smem<DK, MODE>*>(align1k(raw));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vb = blockIdx.y, h = blockIdx.x % p.H;
     long long tok0;
@@ -127,6 +129,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         mbar_init(&s.q_full, 1);
         mbar_init(&s.img_ready, kState);
         mbar_init(&s.img_free, 1);
+        mbar_init(&s.fwd_full, 1);
+        mbar_init(&s.fwd_free, kState);
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
         mbar_init(&s.vt_ready, kSplit<MODE>);
@@ -147,6 +151,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     // ---- V of each chunk, decayed, in three bf16 terms: thread = token, a share of the channels ----
     auto split = [&](int w) {
         constexpr int PIECES = 32 / kSplit<MODE>;  // 16-byte pieces of this thread's row of V
+        bool held = true;
         const int r = 32 * (w & 3) + lane, part = w >> 2;
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
@@ -157,27 +162,38 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.gfree[st]);
             if (!warp_wait(&s.full[st], (c / NST) & 1)) break;
-            if (c > 0 && !warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1)) break;  // N(c-1) is done with the terms before
+            // four pieces at a time, the first while the products still read the terms before
 #pragma unroll 1
-            for (int q = 0; q < PIECES; ++q) {
-                const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q));
-                uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
-                if (r >= L) {  // rows past the chunk's tokens become zero, in V and K too
-                    v = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
-                }
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t t[4][3];
+            for (int q0 = 0; q0 < PIECES; q0 += 4) {
+                uint32_t t[4][3][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 f = unpack_bf16(in[e]);
-                    mul2(f.x, f.y, f.x, f.y, wt, wt);
-                    split_bf16<3>(t[e], f.x, f.y);
-                }
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q0 + q));
+                    uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
+                    if (r >= L) {  // rows past the chunk's tokens become zero, in V and K too
+                        v = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
+                    }
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = unpack_bf16(in[e]);
+                        mul2(f.x, f.y, f.x, f.y, wt, wt);
+                        uint32_t x[3];
+                        split_bf16<3>(x, f.x, f.y);
+                        t[q][0][e] = x[0], t[q][1][e] = x[1], t[q][2][e] = x[2];
+                    }
+                }
+                if (q0 == 0 && c > 0 && !(held = warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1))) break;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q0 + q));
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[q][k][0], t[q][k][1], t[q][k][2], t[q][k][3]);
+                }
             }
+            if (!held) break;
             if (r >= L) {
 #pragma unroll 1
                 for (int q = part; q < DK / 8; q += kSplit<MODE> / 4)
@@ -352,7 +368,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 if (own) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4*>(s.S + 2 * swz<64>(r, 32 * half + 8 * q)) =
+                        *reinterpret_cast<uint4*>(s.S[0] + 2 * swz<64>(r, 32 * half + 8 * q)) =
                             make_uint4(pack_bf16(S[8 * q], S[8 * q + 1]), pack_bf16(S[8 * q + 2], S[8 * q + 3]),
                                        pack_bf16(S[8 * q + 4], S[8 * q + 5]), pack_bf16(S[8 * q + 6], S[8 * q + 7]));
                 }
@@ -369,21 +385,26 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             if constexpr (MODE == 2) {
                 if (REV) {
                     // <S, dS> of the chunk: this thread's part of both
-                    const size_t img = (((slot0 + chunk_of(c)) * p.H + h) * 2 * gridDim.y + vb) * slab;
-                    float d = 0.f;
+                    float2 d2 = make_float2(0.f, 0.f);
+                    if (!(ok = warp_wait(&s.fwd_full, c & 1))) break;
                     if (own) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.other + img + swz<64>(r, 32 * half + 8 * q)));
-                            const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.other + img + gridDim.y * slab + swz<64>(r, 32 * half + 8 * q)));
+                            const uint32_t at = 2 * swz<64>(r, 32 * half + 8 * q);
+                            const uint4 a = *reinterpret_cast<const uint4*>(s.S[0] + at), b = *reinterpret_cast<const uint4*>(s.S[MODE == 2] + at);
                             const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float2 hi = unpack_bf16(x[e]), lo = unpack_bf16(y[e]);
-                                d += S[8 * q + 2 * e] * (hi.x + lo.x) + S[8 * q + 2 * e + 1] * (hi.y + lo.y);
+                                float2 hi = unpack_bf16(x[e]);
+                                const float2 lo = unpack_bf16(y[e]);
+                                add2f(hi.x, hi.y, hi.x, hi.y, lo.x, lo.y);
+                                fma2(d2.x, d2.y, S[8 * q + 2 * e], S[8 * q + 2 * e + 1], hi.x, hi.y, d2.x, d2.y);
                             }
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.fwd_free);
+                    float d = d2.x + d2.y;
                     d = warp_sum(d);
                     if (lane == 0) s.col[warp - kEpi][c & 1] = total * d;
                 }
@@ -439,6 +460,19 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     break;
                 }
                 tma_load_3d(q.V, &p.vmap, vb * NB, h, tok, &s.full[st]);
+                if constexpr (MODE == 2 && REV) {
+                    if (c > 0 && !wait_for(&s.fwd_free, (c - 1) & 1)) {
+                        ++c;
+                        break;
+                    }
+                    const size_t term = gridDim.y * (size_t)(DK * 128);
+                    const unsigned char* from = reinterpret_cast<const unsigned char*>(p.other) +
+                                                ((slot0 + chunk_of(c)) * p.H + h) * (2 * term) + vb * (size_t)(DK * 128);
+                    mbar_arrive_expect(&s.fwd_full, 2 * DK * 128);
+                    bulk_g2s(s.S[0], from, DK * 128, &s.fwd_full);
+                    bulk_g2s(s.S[1], from + term, DK * 128, &s.fwd_full);
+                    nq = c + 1;
+                }
                 if constexpr (MODE == 0) {
                     if (c > 0 && !wait_for(&s.x_done, (c - 1) & 1)) {
                         ++c;
@@ -454,7 +488,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             // no copy may be in flight when the CTA ends (after a wait that gave up, a
             // stage that is not whole makes this one give up too: by then its copies are in)
             for (int d = max(0, c - NST); d < c; ++d) wait_for(&s.full[d % NST], (d / NST) & 1);
-            if (nq) wait_for(&s.q_full, (nq - 1) & 1);
+            if (nq) wait_for(MODE == 0 ? &s.q_full : &s.fwd_full, (nq - 1) & 1);
         }
     } else if (warp == kEpi + kState + 1) {
         // ---- products: the warp stays together, one lane issues ----------------
@@ -598,7 +632,7 @@ template <int MODE, bool REV>
 void launch(const Params& a, int dk, dim3 grid, cudaStream_t st) {
     auto go = [&](auto d) {
         constexpr int DK = decltype(d)::value;
-        const int smem = sizeof(Smem<DK>) + 1024;
+        const int smem = sizeof(Smem<DK, MODE>) + 1024;
         cudaFuncSetAttribute(decay_tc_walk_kernel<DK, MODE, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         GDN_LAUNCH(MODE == 0 ? "decay_tc_walk" : MODE == 1 ? "decay_tc_map" : "decay_tc_states", st,
                    (decay_tc_walk_kernel<DK, MODE, REV><<<grid, kThreads<MODE>, smem, st>>>(a)));
