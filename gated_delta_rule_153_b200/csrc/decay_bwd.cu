@@ -129,7 +129,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             mbar_init(b, 1);
         for (uint64_t* b : {&s.zeroed, &s.e1, &s.e2, &s.e3r, &s.e3[0], &s.e3[1], &s.e4}) mbar_init(b, kEpi);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.gfull[i], 32);
+            mbar_init(&s.gfull[i], 1);
             mbar_init(&s.gfree[i], 1);
         }
         fence_mbar_init();
@@ -635,7 +635,8 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
         auto form = [&](long long u, const Chunk& c, int n) {
             load_gates(g, p.g + (size_t)c.tok * p.H + (int)(u % p.H), p.H, c.L);
             form_gates(s.gate[n & 1], g);
-            mbar_arrive(&s.gfull[n & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.gfull[n & 1]);
         };
         long long u = next_unit(blockIdx.x, ch);
         if (u < units) form(u, ch, 0);

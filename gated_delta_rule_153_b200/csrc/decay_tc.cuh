@@ -79,7 +79,7 @@ GDN_DEV void form_gates(Gates& s, const float (&x)[4]) {
         if (j > 0) c[j] = add2(c[j], c[j - 1]);
     }
     float2 run = c[3];  // over this lane and those before it
-#pragma unroll 1
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float2 y = make_float2(__shfl_up_sync(0xffffffffu, run.x, o), __shfl_up_sync(0xffffffffu, run.y, o));
         if (lane >= o) run = add2(run, y);

@@ -67,7 +67,7 @@ struct alignas(1024) Smem {
     Gates gate[NST];
     float col[kEpi][CT];         // per warp of P: the column factors of its decays
     // of each stage, so that nobody who waits for one can fall two phases behind
-    uint64_t full[NST], gfull[NST], gfree[NST], n_done[NST], o_done[NST];
+    uint64_t full[NST], v_full[NST], v_free[NST], gfull[NST], gfree[NST], n_done[NST], o_done[NST];
     uint64_t img_ready, img_free, fwd_full, fwd_free, q_full, a_done, p_ready, vt_ready, s_ready, x_done, o_free, drain;
     uint32_t tmem;
 };
@@ -121,9 +121,11 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&s.full[i], 1);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_free[i], kSplit<MODE>);
             mbar_init(&s.n_done[i], 1);
             mbar_init(&s.o_done[i], 1);
-            mbar_init(&s.gfull[i], 32);
+            mbar_init(&s.gfull[i], 1);
             mbar_init(&s.gfree[i], (MODE == 0 ? kEpi : 0) + kState + kSplit<MODE>);
         }
         mbar_init(&s.q_full, 1);
@@ -161,7 +163,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             const float wt = r < L ? (REV ? p.scale * start_decay(gr) : pair_decay(ge, gr)) : 0.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.gfree[st]);
-            if (!warp_wait(&s.full[st], (c / NST) & 1)) break;
+            if (!warp_wait(&s.v_full[st], (c / NST) & 1)) break;
             // four pieces at a time, the first while the products still read the terms before
 #pragma unroll 1
             for (int q0 = 0; q0 < PIECES; q0 += 4) {
@@ -170,9 +172,9 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q0 + q));
                     uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
-                    if (r >= L) {  // rows past the chunk's tokens become zero, in V and K too
+                    if (r >= L) {  // rows past the chunk's tokens become zero, in V (for Y) and K too
                         v = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
+                        if (MODE == 0) *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
                     }
                     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -184,6 +186,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                         t[q][0][e] = x[0], t[q][1][e] = x[1], t[q][2][e] = x[2];
                     }
                 }
+                if (MODE != 0) {  // the only batch: V's place is free
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.v_free[st]);
+                }
                 if (q0 == 0 && c > 0 && !(held = warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1))) break;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -194,6 +200,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 }
             }
             if (!held) break;
+            if (L < CT && !warp_wait(&s.full[st], (c / NST) & 1)) break;
             if (r >= L) {
 #pragma unroll 1
                 for (int q = part; q < DK / 8; q += kSplit<MODE> / 4)
@@ -445,26 +452,31 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     } else if (warp == kEpi + kState) {
         // ---- loads -----------------------------------------------------------
         if (lane == 0) {
-            int c = 0, nq = 0;
-            for (; c < nc; ++c) {
+            int nk = 0, nv = 0, nq = 0;  // copies begun
+            for (int c = 0; c < nc; ++c) {
                 // each operand goes in as soon as the products are done with the last in its place
                 const int st = c % NST, ph = (c / NST - 1) & 1;
                 auto& q = s.st[st];
                 const int tok = (int)(tok0 + (long long)chunk_of(c) * CT), kh = h / p.rep;
+                if (MODE != 0) {
+                    if (c >= NST && !wait_for(&s.v_free[st], ph)) break;
+                    mbar_arrive_expect(&s.v_full[st], PANEL);
+                    tma_load_3d(q.V, &p.vmap, vb * NB, h, tok, &s.v_full[st]);
+                    nv = c + 1;
+                }
                 if (c >= NST && !wait_for(&s.n_done[st], ph)) break;
-                mbar_arrive_expect(&s.full[st], (DK / 64 + 1) * PANEL);
+                mbar_arrive_expect(&s.full[st], DK / 64 * PANEL);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x) tma_load_3d(q.K[x], &p.kmap, 64 * x, kh, tok, &s.full[st]);
-                if (MODE == 0 && c >= NST && !wait_for(&s.o_done[st], ph)) {
-                    ++c;  // K's copies are in flight, V's will not come
-                    break;
+                nk = c + 1;
+                if (MODE == 0) {
+                    if (c >= NST && !wait_for(&s.o_done[st], ph)) break;
+                    mbar_arrive_expect(&s.v_full[st], PANEL);
+                    tma_load_3d(q.V, &p.vmap, vb * NB, h, tok, &s.v_full[st]);
+                    nv = c + 1;
                 }
-                tma_load_3d(q.V, &p.vmap, vb * NB, h, tok, &s.full[st]);
                 if constexpr (MODE == 2 && REV) {
-                    if (c > 0 && !wait_for(&s.fwd_free, (c - 1) & 1)) {
-                        ++c;
-                        break;
-                    }
+                    if (c > 0 && !wait_for(&s.fwd_free, (c - 1) & 1)) break;
                     const size_t term = gridDim.y * (size_t)(DK * 128);
                     const unsigned char* from = reinterpret_cast<const unsigned char*>(p.other) +
                                                 ((slot0 + chunk_of(c)) * p.H + h) * (2 * term) + vb * (size_t)(DK * 128);
@@ -474,10 +486,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     nq = c + 1;
                 }
                 if constexpr (MODE == 0) {
-                    if (c > 0 && !wait_for(&s.x_done, (c - 1) & 1)) {
-                        ++c;
-                        break;
-                    }
+                    if (c > 0 && !wait_for(&s.x_done, (c - 1) & 1)) break;
                     mbar_arrive_expect(&s.q_full, DK / 64 * PANEL);
 #pragma unroll
                     for (int x = 0; x < DK / 64; ++x) tma_load_3d(s.Q[x], &p.qmap, 64 * x, kh, tok, &s.q_full);
@@ -485,9 +494,9 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 }
                 ++done;
             }
-            // no copy may be in flight when the CTA ends (after a wait that gave up, a
-            // stage that is not whole makes this one give up too: by then its copies are in)
-            for (int d = max(0, c - NST); d < c; ++d) wait_for(&s.full[d % NST], (d / NST) & 1);
+            // no copy may be in flight when the CTA ends
+            for (int d = max(0, nk - NST); d < nk; ++d) wait_for(&s.full[d % NST], (d / NST) & 1);
+            for (int d = max(0, nv - NST); d < nv; ++d) wait_for(&s.v_full[d % NST], (d / NST) & 1);
             if (nq) wait_for(MODE == 0 ? &s.q_full : &s.fwd_full, (nq - 1) & 1);
         }
     } else if (warp == kEpi + kState + 1) {
@@ -530,7 +539,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
             }
             // N(c); with 64 key channels lanes 64-127 read the V tile behind K and are ignored
-            if (MODE != 0 && !warp_wait(&s.s_ready, c & 1)) break;
+            if (MODE != 0 && (!warp_wait(&s.full[st], (c / NST) & 1) || !warp_wait(&s.s_ready, c & 1))) break;
             if (!warp_wait(&s.vt_ready, c & 1)) break;
             tc5::fence_after();
             if (elect_one()) {
@@ -578,20 +587,24 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         }
         if (lane == 0) bulk_wait<0>();
     } else {
-        // ---- gates: the next chunk's values are on their way while this one's wait ----
-        float x[4];
-        auto load = [&](int c) {
-            load_gates(x, p.g + (size_t)(tok0 + (long long)chunk_of(c) * CT) * p.H + h, p.H, min(CT, n - chunk_of(c) * CT));
+        // ---- gates: the next two chunks' values are on their way while this one's wait ----
+        float xa[4], xb[4];
+        auto load = [&](float (&x)[4], int c) {
+            if (c < nc) load_gates(x, p.g + (size_t)(tok0 + (long long)chunk_of(c) * CT) * p.H + h, p.H, min(CT, n - chunk_of(c) * CT));
         };
-        if (nc > 0) load(0);
-        for (int c = 0; c < nc; ++c) {
+        auto form = [&](float (&x)[4], int c) {
             const int st = c % NST;
-            if (c >= NST && !warp_wait(&s.gfree[st], ((c / NST) - 1) & 1)) break;
+            if (c >= NST && !warp_wait(&s.gfree[st], ((c / NST) - 1) & 1)) return false;
             form_gates(s.gate[st], x);
-            mbar_arrive(&s.gfull[st]);
-            if (c + 1 < nc) load(c + 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.gfull[st]);
+            load(x, c + 2);
             ++done;
-        }
+            return true;
+        };
+        load(xa, 0);
+        load(xb, 1);
+        for (int c = 0; c < nc && form(xa, c) && (c + 1 == nc || form(xb, c + 1)); c += 2) {}
     }
     if (lane == 0 && done < nc) atomicOr(p.status, 1u);
     tc5::fence_before();
