@@ -53,6 +53,10 @@ constexpr int kSplit = MODE == 0 ? 4 : kEpi;
 template <int MODE>
 constexpr int kThreads = 32 * (kEpi + kState + 3 + (MODE == 0 ? 4 : MODE == 2 ? 1 : 0));
 constexpr int NST = 2;
+// bf16 terms of the decayed V: three are exact to fp32; the states that go out in two
+// terms themselves (2^-16) and nowhere else are made of two.
+template <int MODE, bool REV>
+constexpr int kTerms = MODE == 2 && !REV ? 2 : 3;
 
 template <int DK, int MODE>
 struct alignas(1024) Smem {
@@ -95,6 +99,7 @@ constexpr uint32_t TA = 0, TP = 128, TX = 192, TY = 256, TN = 320, kCols = 512;
 template <int DK, int MODE, bool REV>
 __global__ void __launch_bounds__(kThreads<MODE>, 1)
 decay_tc_walk_kernel(const __grid_constant__ Params p) {
+    constexpr int TERMS = kTerms<MODE, REV>;
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem<DK, MODE>& s = *reinterpret_cast<Smem<DK, MODE>*>(align1k(raw));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -167,7 +172,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             // four pieces at a time, the first while the products still read the terms before
 #pragma unroll 1
             for (int q0 = 0; q0 < PIECES; q0 += 4) {
-                uint32_t t[4][3][4];
+                uint32_t t[4][TERMS][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q0 + q));
@@ -181,9 +186,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     for (int e = 0; e < 4; ++e) {
                         float2 f = unpack_bf16(in[e]);
                         mul2(f.x, f.y, f.x, f.y, wt, wt);
-                        uint32_t x[3];
-                        split_bf16<3>(x, f.x, f.y);
-                        t[q][0][e] = x[0], t[q][1][e] = x[1], t[q][2][e] = x[2];
+                        uint32_t x[TERMS];
+                        split_bf16<TERMS>(x, f.x, f.y);
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k) t[q][k][e] = x[k];
                     }
                 }
                 if (MODE != 0) {  // the only batch: V's place is free
@@ -195,7 +201,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q0 + q));
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
+                    for (int k = 0; k < TERMS; ++k)
                         *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[q][k][0], t[q][k][1], t[q][k][2], t[q][k][3]);
                 }
             }
@@ -354,7 +360,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         float total = 1.f, decay = 1.f;
         auto add_n = [&]() {  // S <- e^{G_last} S + N, N in one accumulator per term of V
 #pragma unroll 1
-            for (int x = 0; x < 3; ++x) {
+            for (int x = 0; x < TERMS; ++x) {
                 float N[32];
                 tc5::ld32(N, trow + TN + NB * x + 32 * half);
                 tc5::wait_ld();
@@ -503,7 +509,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         // ---- products: the warp stays together, one lane issues ----------------
         constexpr uint32_t ID_A = tc5::idesc_bf16(128, 128, false, false);
         constexpr uint32_t ID_X = tc5::idesc_bf16(128, NB, false, true);
-        constexpr uint32_t ID_N = tc5::idesc_bf16(128, 3 * NB, true, true);
+        constexpr uint32_t ID_N = tc5::idesc_bf16(128, TERMS * NB, true, true);
         // descriptors of step 0; a K step is 32 bytes along 64-channel rows (then the
         // next panel), or 16 rows down a tile
         constexpr uint64_t KROWS = (16 * 128) >> 4, KCOLS = 32 >> 4, KPANEL = PANEL >> 4;
