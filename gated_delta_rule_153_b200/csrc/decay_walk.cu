@@ -140,10 +140,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         mbar_init(&s.fwd_free, kState);
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
-        mbar_init(&s.vt_ready, kSplit<MODE>);
+        mbar_init(&s.vt_ready, kSplit<MODE> + (MODE == 0 ? kState : 0));
         mbar_init(&s.s_ready, kState);
         mbar_init(&s.x_done, 1);
-        mbar_init(&s.o_free, kEpi);
+        mbar_init(&s.o_free, kEpi + kState);
         mbar_init(&s.drain, 1);
         fence_mbar_init();
     }
@@ -155,57 +155,67 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     int done = 0;  // chunks this warp went through: fewer than nc after a wait that gave up
     const uint32_t trow = tm + ((uint32_t)(32 * (warp & 3)) << 16);
 
-    // ---- V of each chunk, decayed, in three bf16 terms: thread = token, a share of the channels ----
+    // ---- V of a chunk, decayed, in bf16 terms: thread = token r, NP 16-byte pieces of its row ----
+    // what token r adds decays, forwards to the chunk's end, backwards from its start
+    auto weight = [&](int st, int r, int L) {
+        const float2 ge = s.gate[st].G[CT - 1], gr = s.gate[st].G[r];
+        return r < L ? (REV ? p.scale * start_decay(gr) : pair_decay(ge, gr)) : 0.f;
+    };
+    auto make = [&](auto& t, int st, int r, int q0, float wt, bool in) {
+        constexpr int NP = sizeof(t) / sizeof(t[0]);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const uint32_t at = 2 * swz<64>(r, 8 * (q0 + q));
+            uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
+            if (!in) {  // rows past the chunk's tokens become zero, in V (for Y) and K too
+                v = make_uint4(0, 0, 0, 0);
+                if (MODE == 0) *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
+            }
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 f = unpack_bf16(u[e]);
+                mul2(f.x, f.y, f.x, f.y, wt, wt);
+                uint32_t x[TERMS];
+                split_bf16<TERMS>(x, f.x, f.y);
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k) t[q][k][e] = x[k];
+            }
+        }
+    };
+    auto put = [&](auto& t, int r, int q0) {
+        constexpr int NP = sizeof(t) / sizeof(t[0]);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const uint32_t at = 2 * swz<64>(r, 8 * (q0 + q));
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k)
+                *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[q][k][0], t[q][k][1], t[q][k][2], t[q][k][3]);
+        }
+    };
+    // The warps of its own (MODE 0: pieces 0 .. 5 of 8, the others are the state warps'), w = 0 ..
     auto split = [&](int w) {
-        constexpr int PIECES = 32 / kSplit<MODE>;  // 16-byte pieces of this thread's row of V
-        bool held = true;
+        constexpr int NP = MODE == 0 ? 3 : 4;  // the first NP are made while the products still read the terms before
         const int r = 32 * (w & 3) + lane, part = w >> 2;
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
             if (!warp_wait(&s.gfull[st], (c / NST) & 1)) break;
-            // forwards what token r adds decays to the chunk's end, backwards from its start
-            const float2 ge = s.gate[st].G[CT - 1], gr = s.gate[st].G[r];
-            const float wt = r < L ? (REV ? p.scale * start_decay(gr) : pair_decay(ge, gr)) : 0.f;
+            const float wt = weight(st, r, L);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.gfree[st]);
             if (!warp_wait(&s.v_full[st], (c / NST) & 1)) break;
-            // four pieces at a time, the first while the products still read the terms before
-#pragma unroll 1
-            for (int q0 = 0; q0 < PIECES; q0 += 4) {
-                uint32_t t[4][TERMS][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q0 + q));
-                    uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
-                    if (r >= L) {  // rows past the chunk's tokens become zero, in V (for Y) and K too
-                        v = make_uint4(0, 0, 0, 0);
-                        if (MODE == 0) *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
-                    }
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 f = unpack_bf16(in[e]);
-                        mul2(f.x, f.y, f.x, f.y, wt, wt);
-                        uint32_t x[TERMS];
-                        split_bf16<TERMS>(x, f.x, f.y);
-#pragma unroll
-                        for (int k = 0; k < TERMS; ++k) t[q][k][e] = x[k];
-                    }
-                }
-                if (MODE != 0) {  // the only batch: V's place is free
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.v_free[st]);
-                }
-                if (q0 == 0 && c > 0 && !(held = warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1))) break;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t at = 2 * swz<64>(r, 8 * (PIECES * part + q0 + q));
-#pragma unroll
-                    for (int k = 0; k < TERMS; ++k)
-                        *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[q][k][0], t[q][k][1], t[q][k][2], t[q][k][3]);
-                }
+            uint32_t t[NP][TERMS][4];
+            make(t, st, r, NP * part, wt, r < L);
+            if (MODE != 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.v_free[st]);
             }
-            if (!held) break;
+            if (c > 0 && !warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1)) break;
+            put(t, r, NP * part);
+            if (MODE == 0) {
+                make(t, st, r, NP, wt, r < L);
+                put(t, r, NP);
+            }
             if (L < CT && !warp_wait(&s.full[st], (c / NST) & 1)) break;
             if (r >= L) {
 #pragma unroll 1
@@ -219,25 +229,63 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         }
     };
 
+    // 16 channels (from vc on) of O of chunk c: thread = query token r, as X and Y lie;
+    // ein = scale e^{G_r}.  False after a wait that gave up.
+    auto out = [&](int c, int r, int vc, float ein) {
+        const int L = min(CT, n - chunk_of(c) * CT);
+        if (!warp_wait(&s.o_done[c % NST], (c / NST) & 1)) return false;
+        tc5::fence_after();
+        float x[16], y[16];
+        tc5::ld16(x, trow + TX + vc);
+        tc5::ld16(y, trow + TY + vc);
+        tc5::wait_ld();
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o_free);
+        uint32_t w[8], mine[4], got[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            fma2(x[2 * e], x[2 * e + 1], ein, ein, x[2 * e], x[2 * e + 1], y[2 * e], y[2 * e + 1]);
+            w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+        }
+        // lanes 2m, 2m+1 trade 16-byte pieces, so that each store instruction
+        // writes whole 32-byte sectors: first row 2m, then row 2m + 1
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            mine[e] = odd ? w[4 + e] : w[e];
+            got[e] = __shfl_xor_sync(0xffffffffu, odd ? w[e] : w[4 + e], 1);
+        }
+        // even lanes now hold the first piece of both rows, odd lanes the second
+        const uint4 a = make_uint4(mine[0], mine[1], mine[2], mine[3]);
+        const uint4 b = make_uint4(got[0], got[1], got[2], got[3]);
+        __nv_bfloat16* row = p.o + ((size_t)(tok0 + (long long)chunk_of(c) * CT + (r & ~1)) * p.H + h) * p.dv + vb * NB + vc + (odd ? 8 : 0);
+        if ((r & ~1) < L) *reinterpret_cast<uint4*>(row) = odd ? b : a;
+        if ((r | 1) < L) *reinterpret_cast<uint4*>(row + (size_t)p.H * p.dv) = odd ? a : b;
+        return true;
+    };
+
     if (warp < kEpi) {
         if constexpr (MODE == 0) {
-            // ---- P, then O: thread = query token --------------------------------
-            // (two warps per 32 tokens: odd and even 16-column pieces of A, halves of O)
+            // ---- P: thread = query token, two warps per 32 tokens for the odd and even
+            // 16-column pieces of A ------------------------------------------------
             const int blk = warp & 3, half = warp >> 2, i = 32 * blk + lane;
-            for (int c = 0; c < nc; ++c) {
-                const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
-                const Gates& G = s.gate[st];
-                if (!warp_wait(&s.gfull[st], (c / NST) & 1)) break;
-                // Decays factor about a base token b, e^{G_i - G_b} e^{G_b - G_j}: for the blocks
-                // before this row's the end of the block before, so that both factors are at
-                // most 1; for its own block the middle, where they stay within fp32 unless
-                // half the block decays by more than 2^100.  The column factors are shared by
-                // the warp's rows.
-                const float2 gi = G.G[i], gm = G.G[32 * blk + 15];
+            float* const col = s.col[warp];
+            float rf = 0.f, rd = 0.f, ein = 0.f;
+            bool wide = false;
+            float2 gi;
+            // Decays factor about a base token b, e^{G_i - G_b} e^{G_b - G_j}: for the blocks
+            // before this row's the end of the block before, so that both factors are at
+            // most 1; for its own block the middle, where they stay within fp32 unless
+            // half the block decays by more than 2^100.  The column factors are shared by
+            // the warp's rows.
+            auto factors = [&](int c) {
+                const Gates& G = s.gate[c % NST];
+                if (!warp_wait(&s.gfull[c % NST], (c / NST) & 1)) return false;
+                gi = G.G[i];
+                const float2 gm = G.G[32 * blk + 15];
                 const float first = diff2(G.G[32 * blk], gm), last_ = diff2(gm, G.G[32 * blk + 31]);
-                const bool wide = !(first < 100.f && last_ < 100.f);  // the same for the whole warp
-                float* const col = s.col[warp];
-                float rf = 0.f;
+                wide = !(first < 100.f && last_ < 100.f);  // the same for the whole warp
                 __syncwarp();
                 if (blk) {
                     const float2 gb = G.G[32 * blk - 1];
@@ -245,11 +293,17 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
 #pragma unroll 1
                     for (int j = lane; j < 32 * blk; j += 32) col[j] = pair_decay(gb, G.G[j]);
                 }
-                const float rd = p.scale * ex2(diff2(gi, gm));
+                rd = p.scale * ex2(diff2(gi, gm));
                 col[32 * blk + lane] = ex2(diff2(gm, gi));
                 __syncwarp();
-                const float ein = p.scale * start_decay(gi);
-                const uint32_t tp = trow + TP;
+                ein = p.scale * start_decay(gi);
+                return true;
+            };
+            const uint32_t tp = trow + TP;
+            if (nc > 0 && !factors(0)) done = -1;
+            for (int c = 0; done == c && c < nc; ++c) {
+                const int st = c % NST;
+                const Gates& G = s.gate[st];
                 if (!warp_wait(&s.a_done, c & 1)) break;
                 tc5::fence_after();
 #pragma unroll 1
@@ -297,43 +351,9 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     mbar_arrive(&s.p_ready);
                     mbar_arrive(&s.gfree[st]);
                 }
-                if (!warp_wait(&s.o_done[st], (c / NST) & 1)) break;
-                tc5::fence_after();
-                // lanes 2m, 2m+1 trade 16-byte pieces, so that each store instruction
-                // writes whole 32-byte sectors: first row 2m, then row 2m + 1
-                const bool odd = lane & 1;
-                __nv_bfloat16* row = p.o + ((size_t)(tok0 + (long long)chunk_of(c) * CT + (i & ~1)) * p.H + h) * p.dv +
-                                     vb * NB + 32 * half + (odd ? 8 : 0);
-                const size_t next = (size_t)p.H * p.dv;
-                const bool up = (i & ~1) < L, dn = (i | 1) < L;
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    float x[16], y[16];
-                    tc5::ld16(x, trow + TX + 32 * half + 16 * q);
-                    tc5::ld16(y, trow + TY + 32 * half + 16 * q);
-                    tc5::wait_ld();
-                    if (q == 1) {
-                        tc5::fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.o_free);
-                    }
-                    uint32_t w[8], mine[4], got[4];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        fma2(x[2 * e], x[2 * e + 1], ein, ein, x[2 * e], x[2 * e + 1], y[2 * e], y[2 * e + 1]);
-                        w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        mine[e] = odd ? w[4 + e] : w[e];
-                        got[e] = __shfl_xor_sync(0xffffffffu, odd ? w[e] : w[4 + e], 1);
-                    }
-                    // even lanes now hold the first piece of both rows, odd lanes the second
-                    const uint4 a = make_uint4(mine[0], mine[1], mine[2], mine[3]);
-                    const uint4 b = make_uint4(got[0], got[1], got[2], got[3]);
-                    if (up) *reinterpret_cast<uint4*>(row + 16 * q) = odd ? b : a;
-                    if (dn) *reinterpret_cast<uint4*>(row + next + 16 * q) = odd ? a : b;
-                }
+                const float e = ein;
+                if (c + 1 < nc && !factors(c + 1)) break;  // while the products make Y
+                if (!out(c, i, 32 * half + 16, e)) break;
                 ++done;
             }
         }
@@ -357,7 +377,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             }
         }
         bool ok = true;
-        float total = 1.f, decay = 1.f;
+        float total = 1.f, decay = 1.f, ein = 0.f;
         auto add_n = [&]() {  // S <- e^{G_last} S + N, N in one accumulator per term of V
 #pragma unroll 1
             for (int x = 0; x < TERMS; ++x) {
@@ -372,11 +392,29 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         };
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
+            float next_ein = 0.f, next_total = 0.f;
+            uint32_t t[1][TERMS][4];
+            if constexpr (MODE == 0) {
+                if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
+                next_ein = p.scale * start_decay(s.gate[st].G[r]);
+                next_total = start_decay(s.gate[st].G[CT - 1]);
+                const float wt = weight(st, r, L);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.gfree[st]);
+                if (!(ok = warp_wait(&s.v_full[st], (c / NST) & 1))) break;
+                make(t, st, r, 6 + half, wt, r < L);
+            }
             if (c > 0) {  // S entering chunk c; X(c-1), which read the last one, came before N(c-1)
                 if (!(ok = warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1))) break;
                 tc5::fence_after();
-                add_n();
             }
+            if constexpr (MODE == 0) {
+                put(t, r, 6 + half);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.vt_ready);
+            }
+            if (c > 0) add_n();
             if constexpr (MODE == 0) {
                 if (own) {
 #pragma unroll
@@ -390,11 +428,17 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             // N(c-1) is in the registers (and, MODE 0, S where X finds it)
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.s_ready);
-            if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
-            total = start_decay(s.gate[st].G[CT - 1]);
-            decay *= total;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.gfree[st]);
+            if (MODE == 0 && c > 0 && !(ok = out(c - 1, r, 32 * half, ein))) break;
+            if constexpr (MODE == 0) {
+                ein = next_ein;
+                total = next_total;
+            } else {
+                if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
+                total = start_decay(s.gate[st].G[CT - 1]);
+                decay *= total;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.gfree[st]);
+            }
             if constexpr (MODE == 2) {
                 if (REV) {
                     // <S, dS> of the chunk: this thread's part of both
@@ -440,6 +484,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             ++done;
         }
         if (ok && nc > 0) {
+            if (MODE == 0 && !out(nc - 1, r, 32 * half, ein)) --done;
             if (warp_wait(&s.n_done[(nc - 1) % NST], ((nc - 1) / NST) & 1)) {
                 tc5::fence_after();
                 add_n();
