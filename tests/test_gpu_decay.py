@@ -288,3 +288,34 @@ def test_prompt_then_steps_is_one_prompt(dev):
     o1, S = gdn.gdn_decay_fwd(*[d[n][:, :133].contiguous() for n in names], d["h0"], scale=0.5)
     steps = [gdn.gdn_decay_step(*[d[n][:, t].contiguous() for n in names], S, scale=0.5) for t in range(133, 140)]
     check(dict(o=torch.cat([o1, torch.stack(steps, 1)], 1), hT=S), x, scale=0.5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_packed_sequences_in_runs(dev, dtype):
+    """More sequences than a warp has lanes, of one head, so that the longer ones are cut
+    into runs; empty ones among them."""
+    gen = torch.Generator().manual_seed(61)
+    lens = torch.randint(0, 60, (45,), generator=gen).tolist()
+    lens[3], lens[20], lens[21], lens[33], lens[44] = 700, 0, 0, 513, 385
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    x = make(1, cu[-1], 1, 1, 64, 64, dtype, seed=14, nstates=len(lens), shift=-3.0)
+    check(run(x, dev, cu=cu, scale=0.7), x, cu=cu, scale=0.7, T=700)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bad_offsets_in_runs(dev, dtype):
+    """Offsets that decrease, in a call whose sequences are cut into runs: reported, the
+    sequences before them right, and nothing outside the tensors touched."""
+    x = make(1, 1400, 1, 1, 64, 64, dtype, seed=15, nstates=6)
+    d = {n: t.to(dev) for n, t in x.items()}
+    cu = torch.tensor([0, 600, 650, 20, 1400, 1399, 1400], dtype=torch.int32, device=dev)
+    ws = torch.empty(1 << 27, dtype=torch.uint8, device=dev)
+    a = [d[n] for n in ("q", "k", "v", "g")]
+    o, _ = gdn.gdn_decay_fwd(*a, d["h0"], cu_seqlens=cu, workspace=ws)
+    assert gdn.gdn_query_device_status(ws) == gdn.GDN_ERR_INVALID_ARG
+    gdn.gdn_decay_bwd(*a, d["dO"], d["h0"], d["dhT"], cu_seqlens=cu, workspace=ws)
+    assert gdn.gdn_query_device_status(ws) == gdn.GDN_ERR_INVALID_ARG
+    first = {n: t[:, :600] if t.shape[1] == 1400 else t[:1] for n, t in x.items()}
+    check(dict(o=o[:, :600]), first)
