@@ -28,9 +28,11 @@
 //     out_t = c (f_t R x_t + sum_s D_ts (w_s.x_t) y_s),   R <- e^{G_last} R + sum_s h_s y_s w_s^T
 // over s <= t, with f = e^G and h = e^{G_last - G} forwards, and over s >= t, with the two
 // exchanged, backwards.  All of it is small matrix products in fp32 on CUDA cores, from
-// shared memory in register tiles of up to 16 x 4; a CTA holds 64 rows of R.  What bounds it is the issue of
-// fp32 FMAs and, twice as long, the shared-memory loads that feed them (a 16-byte load
-// takes four cycles of the SM's 128 bytes per cycle, whatever its lanes share).
+// shared memory in register tiles (2 x 2, 2 x 4 and 4 x 4 with 256 threads); a CTA holds
+// 64 rows of R.  What bounds it is the issue of fp32 FMAs and, 1.5 to 2 times as long, the
+// shared-memory loads that feed them (a 16-byte load takes four cycles of the SM's 128
+// bytes per cycle, whatever its lanes share): 8,100 of them per tile of 64 x 64 dims.
+// Forward, 32 x 1024 tokens of 8 heads: 312 us at 64 x 64 dims, 1,010 us at 128 x 128.
 #include <math.h>
 
 #include <algorithm>
@@ -110,7 +112,11 @@ struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in dif
     float f[TT], h[TT], own[TT], red[8];
 };
 
-// WT threads.  With 256 the next tile's loads are on their way while this one is worked on.
+// WT threads.  128 have the larger register tiles, and so fewer loads from shared memory per
+// product; 256 hide its latency better, with the next tile's rows on their way while this
+// one is worked on.  128 x 128 dims: 256 where a CTA has an SM to itself (777 tokens of
+// 4 heads: 63 us against 95), else 128 (32 x 1024 tokens of 8 heads: 1,010 us against
+// 1,304).  Smaller dims: 256 throughout (within 2 % at that size, faster with few CTAs).
 template <int CD, typename T, bool REV, bool MAP, int WT>
 __global__ void __launch_bounds__(WT)
 decay_walk_kernel(const Walk p) {
@@ -502,7 +508,9 @@ int row_blocks(int RD) { return (RD + RB - 1) / RB; }
 // Runs per chain, of whole chunks: 1 when the chains fill the device.  Estimated in
 // tiles on the critical path: a tile of the map costs a third of one of the walk, the
 // second launch about four, and adding up what the runs before leave 0.1 each.  Packed
-// sequences have rows / length + nseq runs together, however long the longest is.
+// sequences have rows / length + nseq runs together, however long the longest is.  (7
+// packed sequences of up to 1002 tokens, 6 heads, 64 x 64: runs of 4 tiles 53 us, whole
+// chains 197 us.)
 struct Cut {
     int runs, len;
     long long ctas;  // with something to do
@@ -512,7 +520,7 @@ Cut cut(const Problem& p, int RD) {
     const long long heads = (long long)p.H * row_blocks(RD);
     auto waves = [](long long n) { return (double)((n + 295) / 296); };  // two CTAs per SM
     Cut best{1, std::max(tiles, 1), heads * p.seq.nseq};
-    double cost = tiles * waves(heads * p.seq.nseq);
+    double cost = ceil(longest(p.seq) / TT) * waves(heads * p.seq.nseq);
     for (int r = 2; r <= 64; ++r) {
         int len = (tiles + r - 1) / r;
         len += len % 2;  // whole chunks of the gate gradient
@@ -624,10 +632,11 @@ void run_fwd(const Problem& p, const void* q, const void* k, const void* v, cons
 
 // ---- the single-token step ---------------------------------------------------
 // S <- a S + v k^T, o = S (scale q), in place: one 128-bit read and write per
-// four state elements.  A row of DK floats is covered by DK/16 lanes holding
-// 16 columns each (columns 4 (lane + L j) + e, whole 128-byte lines per warp
-// instruction), two rows per thread; CTAs split the rows of a state as well, so
-// that few streams still spread over the SMs.
+// four state elements, which is what bounds it: 256 sequences of 16 heads, 128 x 128,
+// in 93 us, 5.8 TB/s.  A row of DK floats is covered by DK/16 lanes holding 16 columns
+// each (columns 4 (lane + L j) + e, whole 128-byte lines per warp instruction), two
+// rows per thread; CTAs split the rows of a state as well, so that few streams still
+// spread over the SMs.
 constexpr int ST = 128;
 
 template <int DK, typename T>

@@ -35,6 +35,15 @@ inline long long items(const Seqs& q, int runs, int run_len) {
     return q.cu && runs > 1 ? q.rows / run_len + (long long)q.nseq : (long long)q.nseq * runs;
 }
 
+// The longest sequence as far as the host can tell: a row cut at random into n sequences
+// has a longest of rows (1 + 1/2 + .. + 1/n) / n on average.
+inline double longest(const Seqs& q) {
+    if (!q.cu) return q.len;
+    double h = 0;
+    for (int i = 1; i <= q.nseq; ++i) h += 1.0 / i;
+    return q.rows * h / q.nseq;
+}
+
 #ifdef __CUDACC__
 // The token range of sequence s.  False if its offsets are not one: out of the
 // row, decreasing, or below the offset before them (it would then share tokens

@@ -22,19 +22,32 @@
 // the state is split into three bf16 terms (exact to fp32), because errors there
 // would stay in the state, which is kept and returned in fp32.
 //
-// Roles: warps 0-7 turn A into P and combine O (thread = query token); warps 8-15
-// own the state (thread = key channel, half of the value channels); warp 16 issues
-// the loads, warp 17 the products, warp 18 forms the gates' cumsum, the last four split V.
-// K and V tiles go through a two-stage ring; Q, which A and X are done with early
-// in a chunk, has one place.
+// Roles: warps 0-7 make P of A (thread = query token), then the column factors of the
+// next chunk's decays, then half of O; warps 8-15 own the state (thread = key channel,
+// half of the value channels) and combine the other half of O; warp 16 issues the loads,
+// warp 17 the products, warp 18 forms the gates' cumsum, two chunks ahead.  The decayed V
+// is split by the last four warps and, a quarter of it, by the state's.  K and V tiles
+// go through a two-stage ring; Q, which A and X are done with early in a chunk, has
+// one place.
 //
 // MODE 2 walks K and V (backwards: Q and dO, with the gradient of the state) and
 // writes the state entering each chunk, as two bf16 terms, for the backward's
-// local products (decay_bwd.cu).
+// local products (decay_bwd.cu); warps 0-7 split V.
 // MODE 1 walks K and V alone and writes the state a run of chunks adds to a zero
 // state, with the run's decay.  With few chains, each is cut into runs: MODE 1 over
 // all runs but the last, then MODE 0 or 2 over all runs at once, each starting from the
 // sum of the runs before it.
+//
+// What bounds it, at 8 x 2048 tokens of 8 heads, dk = dv = 128 (128 chains of 16
+// chunks): MODE 0 takes 52 us, 2.6 TB/s of the bytes it cannot do without.  A chunk takes
+// 4,500 cycles: A, P (2,000 cycles: two warps per scheduler, latency), Y, O, each waiting
+// for the one before, with X and N in between; the tensor pipe is busy for a third of them.
+// With O left to the warps of P alone it took 55 us (5,200 cycles), with O left to the
+// state's 53 us.  MODE 2 takes 32 us forwards and 45 us backwards: 2,900 and 3,700
+// cycles, of which the copies of 80 KB (forwards 48 KB and the 32 KB image out, backwards
+// the forward image as well) at the 26 bytes per cycle that an SM gets from HBM are most.
+#include <math.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -669,8 +682,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
 // Runs per chain: 1 when the chains fill the device; otherwise the number that
 // gives the shortest estimated time, in chunk steps on the critical path.  A
 // step of the walk costs about 1, one of the map (MODE 1) about 0.7, the second launch
-// about 2, and adding up what the runs before leave 0.2 each.  Packed sequences have
-// rows / length + nseq runs together, however long the longest is.
+// about 4, and adding up what the runs before leave 0.2 each.  Packed sequences have
+// rows / length + nseq runs together, however long the longest is.  (16 heads of 8192
+// tokens: 4 runs 85 us, 1 run 169 us.  9 packed sequences of up to 968 tokens, 8 heads:
+// runs of 3 chunks 33 us, whole chains 31 us.)
 struct Cut {
     int runs, len;
 };
@@ -679,11 +694,11 @@ Cut cut_of(const Problem& p) {
     const long long heads = (long long)p.H * (p.dv / NB);
     Cut best{1, std::max(chunks, 1)};
     auto waves = [](long long n) { return (double)((n + 147) / 148); };
-    double cost = chunks * waves(heads * nseq);
+    double cost = ceil(longest(p.seq) / CT) * waves(heads * nseq);
     for (int r = 2; r <= 64 && r <= chunks; ++r) {
         const int len = (chunks + r - 1) / r, runs = (chunks + len - 1) / len;
         const long long all = heads * items(p.seq, runs, len * CT), maps = p.seq.cu ? all : all - heads * nseq;
-        const double c = len * (waves(all) + 0.7 * waves(maps)) + 2 + 0.2 * runs;
+        const double c = len * (waves(all) + 0.7 * waves(maps)) + 4 + 0.2 * runs;
         if (c < 0.9 * cost) {
             cost = c;
             best = Cut{runs, len};
@@ -733,6 +748,9 @@ void launch_runs(const Params& a, const Problem& p, cudaStream_t st) {
 
 }  // namespace
 
+// The dims that fill whole 64-channel panels; the products of smaller ones would be
+// padding for the most part.  (16 heads of 8192 tokens, 128 x 128: 85 us here and 767 us
+// on CUDA cores; the 350M-scale training step 238 us and 2.9 ms.)
 bool tc_supported(const Problem& p) {
     return p.dtype == GDN_BF16 && (p.dk == 64 || p.dk == 128) && (p.dv == 64 || p.dv == 128);
 }

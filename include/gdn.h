@@ -341,9 +341,14 @@ gdn_status gdn_recurrent_step(int N, int H, int dk, int dv, gdn_dtype dtype,
  * nothing outside the tensors is touched); sequences must not overlap.  nseq = 0 with a null
  * cu_seqlens is the plain batch.
  * Values: g <= 0 (documented, not checked); g = -inf is a reset.  The decay of a
- * pair of tokens is formed from an fp64 cumsum or token by token, the state and
- * dg from products exact to fp32: hT, dh0 and dg carry fp32 accuracy with bf16
- * inputs too; o, dq, dk, dv are rounded to `dtype` once more at the end.
+ * pair of tokens is the exponential of a difference in a cumsum of two floats per
+ * token (error below 2^-40 of it).  The state that hT and dh0 come from is summed
+ * in fp32 from products exact to fp32, with bf16 inputs too.  dg is summed in fp32;
+ * with bf16 inputs and dk, dv in {64, 128} (tensor cores) the states enter it in two
+ * bf16 terms each, 2^-16 of their entries, and without h0 and dhT it keeps
+ * nearly all of fp32.  There o, dq, dk, dv take the states and the decayed
+ * pair products in bf16, one rounding each (2^-8); all are rounded to `dtype` at
+ * the end.
  * The backward is that of <dO, o> + <dhT, hT> (dhT NULL = 0) and recomputes the
  * states; dh0 is required exactly when h0 is given.
  * dk, dv in {16, 32, 64, 128} (else GDN_ERR_UNSUPPORTED); all pointers 16-byte
@@ -389,7 +394,11 @@ gdn_status gdn_decay_step(int N, int H, int Hk, int dk, int dv, gdn_dtype dtype,
  * head h / (Hq / Hkv):
  *     o_i = sum_p softmax_p(scale q_i . k_p) v_p,
  * the softmax statistics and sums in fp32, the weights rounded to bf16 for their
- * product with v.
+ * product with v.  What nobody sees (cache rows past cache_len, other branches'
+ * nodes) has no effect, whatever its keys and scores are; but the weights' zeros
+ * do multiply v, so the v of a node or cached position that some node of the
+ * sequence sees must be finite for the sequence's other nodes to be.  A score of NaN, or
+ * of +inf, makes the rows that see it NaN.
  * gdn_tree_append copies the k and v rows of the root path of accepted[n] (-1:
  * nothing) to the cache positions cache_len[n] .. and writes the new length to
  * new_len[n] (new_len may be cache_len).

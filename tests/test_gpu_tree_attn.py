@@ -210,3 +210,28 @@ def test_verify_append_verify(dev):
     kc, vc, new = oracle.append(x["parent"], acc.cpu(), x["k"], x["v"], x["kc"], x["vc"], x["table"], x["lens"])
     assert torch.equal(n.cpu(), new)
     check(dict(x, kc=kc, vc=vc, lens=new), dev, 0.125, o=o2)
+
+
+def test_nan_reaches_who_sees_it(dev):
+    """A NaN in a node's key: NaN for the node and its descendants, nothing for the others;
+    one in a cached key within the length: NaN for all nodes of the sequence."""
+    x = make([140, 200], 12, 4, 2, 64, 32, kind="random", seed=31)
+    clean = run(x, dev, 0.125)
+    y = {n: t.clone() for n, t in x.items()}
+    y["k"][0, 3, 1, 5] = float("nan")
+    o = run(y, dev, 0.125)
+    sees = torch.zeros(12, dtype=torch.bool)
+    for i in range(12):
+        j = i
+        while j >= 0:
+            sees[i] |= j == 3
+            j = int(x["parent"][0, j])
+    for i in range(12):
+        assert torch.equal(o[0, i, :2], clean[0, i, :2])
+        assert bool(o[0, i, 2:].isnan().all()) if sees[i] else torch.equal(o[0, i, 2:], clean[0, i, 2:]), i
+    assert torch.equal(o[1], clean[1])
+    p = 100
+    y = {n: t.clone() for n, t in x.items()}
+    y["kc"][x["table"][1, p // 32], p % 32, 0, 0] = float("nan")
+    o = run(y, dev, 0.125)
+    assert bool(o[1, :, :2].isnan().all()) and torch.equal(o[1, :, 2:], clean[1, :, 2:]) and torch.equal(o[0], clean[0])
