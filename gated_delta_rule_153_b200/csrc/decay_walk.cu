@@ -750,7 +750,7 @@ void launch_runs(const Params& a, const Problem& p, cudaStream_t st) {
 
 // The dims that fill whole 64-channel panels; the products of smaller ones would be
 // padding for the most part.  (16 heads of 8192 tokens, 128 x 128: 85 us here and 767 us
-// on CUDA cores; the 350M-scale training step 238 us and 2.9 ms.)
+// on CUDA cores; the 350M-scale training step 237 us and 2.9 ms.)
 bool tc_supported(const Problem& p) {
     return p.dtype == GDN_BF16 && (p.dk == 64 || p.dk == 128) && (p.dv == 64 || p.dv == 128);
 }
