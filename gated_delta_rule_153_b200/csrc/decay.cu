@@ -79,7 +79,7 @@ struct Walk {
     // and its decay (MAP), then all runs at once, each from what the ones before leave.
     int runs, len;
     bool wide;              // at most one CTA per SM: 256 threads
-    float *runR, *runA;     // [chain][run][RD][CD] and [chain][run]
+    float *runR, *runA;     // [item][H][RD][CD] and [item][H]
     unsigned int* status;
 };
 
@@ -129,8 +129,8 @@ decay_walk_kernel(const Walk p) {
     const int h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long tok0;
-    int n, seq, run;
-    if (!item_of(p.seq, p.runs, p.len * TT, MAP ? 1 : 0, blockIdx.x / p.H, seq, run)) return;
+    int n, seq, run, first;
+    if (!item_of(p.seq, p.runs, p.len * TT, MAP ? 1 : 0, blockIdx.x / p.H, seq, run, first)) return;
     if (!span_of(p.seq, seq, tok0, n)) {
         if (tid == 0) atomicOr(p.status, 2u);
         return;
@@ -152,15 +152,16 @@ decay_walk_kernel(const Walk p) {
         __syncthreads();
         // R <- prod a_q R + sum_q (prod_{p > q} a_p) N_q
         float f = 1.f, mine[CD * RB / WT];
-        const float *a = p.runA + sh * p.runs, *from = p.runR + (sh * p.runs * p.RD + r0) * CD;
+        const size_t next = (size_t)p.H * p.RD * CD;  // from a run to the next
+        const float *a = p.runA + (size_t)first * p.H + h, *from = p.runR + ((size_t)first * p.H + h) * p.RD * CD + r0 * CD;
 #pragma unroll
         for (int i = 0; i < CD * RB / WT; ++i) mine[i] = 0.f;
 #pragma unroll 1
-        for (int q = run - 1; q >= 0; --q, f *= __ldg(a + q + 1)) {
+        for (int q = run - 1; q >= 0; --q, f *= __ldg(a + (size_t)(q + 1) * p.H)) {
 #pragma unroll
             for (int i = 0; i < CD * RB / WT; ++i) {
                 const int e = tid + WT * i;
-                if (r0 + e / CD < p.RD) mine[i] = fmaf(f, __ldg(from + (size_t)q * p.RD * CD + e), mine[i]);
+                if (r0 + e / CD < p.RD) mine[i] = fmaf(f, __ldg(from + q * next + e), mine[i]);
             }
         }
 #pragma unroll
@@ -393,7 +394,7 @@ decay_walk_kernel(const Walk p) {
             }
         }
     }
-    float* const to = MAP ? p.runR + ((sh * p.runs + run) * p.RD) * CD : p.last && ends ? p.last + sh * p.RD * CD : nullptr;
+    float* const to = MAP ? p.runR + ((size_t)(first + run) * p.H + h) * p.RD * CD : p.last && ends ? p.last + sh * p.RD * CD : nullptr;
     if (to) {
         __syncthreads();
         for (int e = tid; e < CD * RB; e += WT) {
@@ -401,7 +402,7 @@ decay_walk_kernel(const Walk p) {
             if (r0 + r < p.RD) to[(size_t)(r0 + r) * CD + c] = s.r[c][r];
         }
     }
-    if (MAP && tid == 0 && blockIdx.y == 0) p.runA[sh * p.runs + run] = all;
+    if (MAP && tid == 0 && blockIdx.y == 0) p.runA[(size_t)(first + run) * p.H + h] = all;
 }
 
 // dg of one chunk per warp: the suffix sums of q.dq' - k.dk' and the chunk end's <S, dS>.
@@ -537,15 +538,15 @@ Cut cut(const Problem& p, int RD) {
 }
 size_t runs_bytes(const Problem& p, const Cut& c) {
     if (c.runs == 1) return 0;
-    const size_t chains = (size_t)p.seq.nseq * p.H;
-    return chains * c.runs * (size_t)p.dk * p.dv * 4 + ((chains * c.runs * 4 + 255) & ~(size_t)255);
+    const size_t n = (size_t)items(p.seq, c.runs, c.len * TT) * p.H;
+    return n * p.dk * p.dv * 4 + ((n * 4 + 255) & ~(size_t)255);
 }
 void set_runs(Walk& w, const Problem& p, const Cut& c, void* at) {
     w.runs = c.runs;
     w.len = c.len;
     w.wide = c.ctas <= 148;
     w.runR = (float*)at;
-    w.runA = w.runR + (size_t)p.seq.nseq * p.H * c.runs * p.dk * p.dv;
+    w.runA = w.runR + (size_t)items(p.seq, c.runs, c.len * TT) * p.H * p.dk * p.dv;
 }
 
 struct BwdLayout {

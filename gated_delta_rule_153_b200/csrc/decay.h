@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stddef.h>
 
 #include "../../include/gdn.h"
@@ -30,18 +31,17 @@ struct Problem {
 // never meet, whatever their lengths, so no prefix sum over them is needed.
 __host__ __device__ inline long long chunk_slots(const Seqs& q, int C) { return q.rows / C + (long long)q.nseq; }
 
-// Items of a grid (item_of): each with one CTA per head and block of value channels.
+// Items of a grid (item_of), each with one CTA per head and block of value channels; what
+// the runs leave is kept per item and head.
 inline long long items(const Seqs& q, int runs, int run_len) {
     return q.cu && runs > 1 ? q.rows / run_len + (long long)q.nseq : (long long)q.nseq * runs;
 }
 
 // The longest sequence as far as the host can tell: a row cut at random into n sequences
-// has a longest of rows (1 + 1/2 + .. + 1/n) / n on average.
+// has a longest of rows (1 + 1/2 + .. + 1/n) / n on average, the sum being ln n + 0.577 + 1/2n.
 inline double longest(const Seqs& q) {
-    if (!q.cu) return q.len;
-    double h = 0;
-    for (int i = 1; i <= q.nseq; ++i) h += 1.0 / i;
-    return q.rows * h / q.nseq;
+    const double n = q.nseq;
+    return q.cu && q.nseq > 1 ? q.rows * (log(n) + 0.577 + 0.5 / n) / n : q.len;
 }
 
 #ifdef __CUDACC__
@@ -62,14 +62,18 @@ __device__ __forceinline__ bool span_of(const Seqs& q, int s, long long& tok0, i
 // has the items of run 0 first, then those of run 1; packed sequences have theirs one
 // sequence after the other, so that the CTAs with something to do are neighbours and
 // the device spreads them evenly: at most rows / run_len + nseq of them, all of a grid.
-// `skip` leaves out the last runs.  Called by whole warps; false past the end.
-__device__ __forceinline__ bool item_of(const Seqs& q, int runs, int run_len, int skip, int item, int& seq, int& run) {
+// `skip` (0 or 1) leaves out the last runs.  `first` is the place of the sequence's run 0
+// in what the runs leave: its item among those without last runs.  Called by whole
+// warps; false past the end.
+__device__ __forceinline__ bool item_of(const Seqs& q, int runs, int run_len, int skip, int item, int& seq, int& run,
+                                        int& first) {
     if (!q.cu || runs == 1) {
         seq = item % q.nseq;
         run = item / q.nseq;
+        first = seq * runs;
         return true;
     }
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, all = item;
     for (int s0 = 0; s0 < q.nseq; s0 += 32) {
         long long tok0;
         int n, mine = 0;
@@ -85,6 +89,7 @@ __device__ __forceinline__ bool item_of(const Seqs& q, int runs, int run_len, in
             const int at = __ffs(past) - 1;
             seq = s0 + at;
             run = item - __shfl_sync(0xffffffffu, upto - mine, at);
+            first = all - run - (skip ? 0 : seq);  // every sequence before has one last run
             return true;
         }
         item -= __shfl_sync(0xffffffffu, upto, 31);

@@ -98,7 +98,7 @@ struct Params {
     __nv_bfloat16* o;
     float* hT;
     int runs, len;        // runs per chain, chunks per run
-    float *runS, *runG;   // [chain][value block][run][DK][64] and [chain][run] of MODE 1
+    float *runS, *runG;   // [item][head][value block][DK][64] and [item][head] of MODE 1
     // MODE 2: [slot][head][2 terms][value block][DK][64] bf16, the state entering each chunk
     __nv_bfloat16* image;
     const __nv_bfloat16* other;  // backwards: the forward states, dotted into cross
@@ -118,8 +118,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vb = blockIdx.y, h = blockIdx.x % p.H;
     long long tok0;
-    int n, seq, run;
-    if (!item_of(p.seq, p.runs, p.len * CT, MODE == 1 ? 1 : 0, blockIdx.x / p.H, seq, run)) return;
+    int n, seq, run, first;
+    if (!item_of(p.seq, p.runs, p.len * CT, MODE == 1 ? 1 : 0, blockIdx.x / p.H, seq, run, first)) return;
     if (!span_of(p.seq, seq, tok0, n)) {
         if (tid == 0) atomicOr(p.status, 2u);
         return;
@@ -383,8 +383,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         if (MODE != 1 && own) {
 #pragma unroll 1
             for (int q = 0; q < run; ++q) {  // what the runs before this one leave
-                const float a = p.runG[chain * p.runs + q];
-                const float* N = p.runS + ((chain * gridDim.y + vb) * p.runs + q) * slab + (size_t)(32 * half) * DK + r;
+                const float a = p.runG[(size_t)(first + q) * p.H + h];
+                const float* N = p.runS + (((size_t)(first + q) * p.H + h) * gridDim.y + vb) * slab + (size_t)(32 * half) * DK + r;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) S[e] = a * S[e] + N[(size_t)e * DK];
             }
@@ -505,14 +505,14 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         }
         if (own) {
             float* to = nullptr;
-            if (MODE == 1) to = p.runS + ((chain * gridDim.y + vb) * p.runs + run) * slab + (size_t)(32 * half) * DK + r;
+            if (MODE == 1) to = p.runS + (((size_t)(first + run) * p.H + h) * gridDim.y + vb) * slab + (size_t)(32 * half) * DK + r;
             else if (last && p.hT) to = p.hT + (chain * p.dv + vb * NB + 32 * half) * DK + r;
             if (to) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) to[(size_t)e * DK] = S[e];
             }
         }
-        if (MODE == 1 && vb == 0 && warp == kEpi && lane == 0) p.runG[chain * p.runs + run] = decay;
+        if (MODE == 1 && vb == 0 && warp == kEpi && lane == 0) p.runG[(size_t)(first + run) * p.H + h] = decay;
     } else if (warp == kEpi + kState) {
         // ---- loads -----------------------------------------------------------
         if (lane == 0) {
@@ -723,8 +723,8 @@ void launch(const Params& a, int dk, dim3 grid, cudaStream_t st) {
 // Workspace of the runs, after `base` bytes: their states and decays.
 size_t runs_bytes(const Problem& p, const Cut& c) {
     if (c.runs == 1) return 0;
-    const size_t chains = (size_t)p.seq.nseq * p.H;
-    return chains * c.runs * ((size_t)p.dk * p.dv * 4) + ((chains * c.runs * 4 + 255) & ~(size_t)255);
+    const size_t n = (size_t)items(p.seq, c.runs, c.len * CT) * p.H;
+    return n * p.dk * p.dv * 4 + ((n * 4 + 255) & ~(size_t)255);
 }
 
 Params params_of(const Problem& p, const Cut& c, const float* g, void* runs, void* ws) {
@@ -734,7 +734,7 @@ Params params_of(const Problem& p, const Cut& c, const float* g, void* runs, voi
     a.runs = c.runs; a.len = c.len;
     a.status = (unsigned int*)ws;
     a.runS = (float*)runs;
-    a.runG = a.runS + (size_t)p.seq.nseq * p.H * c.runs * p.dk * p.dv;
+    a.runG = a.runS + (size_t)items(p.seq, c.runs, c.len * CT) * p.H * p.dk * p.dv;
     return a;
 }
 
