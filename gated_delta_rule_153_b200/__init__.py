@@ -710,7 +710,7 @@ class _On:
                 raise ValueError(f"stream of {stream.device} for tensors on {device}")
             self.ctx, self.handle = torch.cuda.stream(stream), stream.cuda_stream  # sets its device too
         else:
-            if device.index != torch.cuda.current_device():
+            if device.index != torch._C._cuda_getDevice():
                 self.ctx = torch.cuda.device(device)
             self.handle = torch._C._cuda_getCurrentRawStream(device.index)
 
