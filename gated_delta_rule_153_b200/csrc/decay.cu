@@ -47,7 +47,7 @@ namespace decay {
 namespace {
 
 constexpr int TT = 32;          // tokens per tile
-constexpr int RB = 64;          // rows of R per CTA
+constexpr int kRows = 64;       // rows of R per CTA at most
 constexpr int AC = 64;          // tokens per chunk of the gate gradient
 
 // A gate of -inf (or one so low that e^g is zero in fp32) is a reset.
@@ -104,7 +104,7 @@ GDN_DEV void put4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-template <int CD>
+template <int CD, int RB>
 struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in different banks
     float x[TT][CD + 4], w[TT][CD + 4], y[TT][RB + 4], z[TT][RB + 4], p[TT][TT + 4];
     float r[CD][RB + 4];
@@ -112,20 +112,26 @@ struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in dif
     float f[TT], h[TT], own[TT], red[8];
 };
 
-// WT threads.  128 have the larger register tiles, and so fewer loads from shared memory per
+// RB rows of R per CTA, WT threads.  16 and 32 rows in all have kernels of their own with
+// 128 threads: lanes for 64 would idle (32 x 1024 tokens of 8 heads, 16 x 16 dims: 114 us
+// against 175, 128 columns and 16 rows: 329 us against 507).  With 64 rows, 128
+// threads have the larger register tiles, and so fewer loads from shared memory per
 // product; 256 hide its latency better, with the next tile's rows on their way while this
-// one is worked on.  128 x 128 dims: 256 where a CTA has an SM to itself (777 tokens of
+// one is worked on.  128 columns: 256 where a CTA has an SM to itself (777 tokens of
 // 4 heads: 63 us against 95), else 128 (32 x 1024 tokens of 8 heads: 1,010 us against
-// 1,304).  Smaller dims: 256 throughout (within 2 % at that size, faster with few CTAs).
-template <int CD, typename T, bool REV, bool MAP, int WT>
+// 1,304).  Fewer columns: 256 throughout (within 2 % at that size, faster with few CTAs).
+template <int CD, int RB, typename T, bool REV, bool MAP, int WT>
 __global__ void __launch_bounds__(WT)
 decay_walk_kernel(const Walk p) {
     extern __shared__ __align__(16) unsigned char raw[];
-    WalkSmem<CD>& s = *reinterpret_cast<WalkSmem<CD>*>(raw);
+    WalkSmem<CD, RB>& s = *reinterpret_cast<WalkSmem<CD, RB>*>(raw);
     using F = Four<T>;
     constexpr int NX = TT * CD / 4 / WT > 0 ? TT * CD / 4 / WT : 1;  // groups of four per thread and tile
-    constexpr int NC = CD * 16 / WT;                                 // columns of R per thread
-    constexpr int NY = TT * RB / 4 / WT, NT = TT * 16 / WT;
+    constexpr int LR = RB / 4;                                       // lanes of a row of out
+    constexpr int NC = CD * LR / WT > 0 ? CD * LR / WT : 1;          // columns of R per thread
+    constexpr int NY = TT * LR / WT, NT = TT * LR / WT;              // rows of y, tokens of out per thread
+    constexpr int NP = TT * 16 / WT;                                 // rows of p per thread
+    static_assert(NT >= 1, "a thread has a token");
     const int h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long tok0;
@@ -172,8 +178,8 @@ decay_walk_kernel(const Walk p) {
     }
     float all = 1.f;  // the decay of the run so far
     const bool has_z = !MAP && p.dots != nullptr;
-    constexpr bool AHEAD = WT == 256;
-    const int r = 4 * (tid % 16);  // this thread's rows of R
+    constexpr bool AHEAD = WT == 256 || (RB < kRows && CD < 128);
+    const int r = 4 * (tid % LR);  // this thread's rows of R
     typename F::Raw vx[NX], vw[NX], vy[NY], vz[NY];  // all on their way before any is put down
     float pg = 0.f;
     auto fetch = [&](int it) {
@@ -192,7 +198,7 @@ decay_walk_kernel(const Walk p) {
         }
 #pragma unroll
         for (int i = 0; i < NY; ++i) {
-            const int t = tid / 16 + WT / 16 * i;
+            const int t = tid / LR + WT / LR * i;
             vy[i] = get(p.y, t, r0 + r, t < m && r0 + r < p.RD);
             if (has_z) vz[i] = get(p.z, t, r0 + r, t < m && r0 + r < p.RD);
         }
@@ -216,7 +222,7 @@ decay_walk_kernel(const Walk p) {
         }
 #pragma unroll
         for (int i = 0; i < NY; ++i) {
-            const int t = tid / 16 + WT / 16 * i;
+            const int t = tid / LR + WT / LR * i;
             const float4 v = F::of(vy[i]);
             *reinterpret_cast<float4*>(&s.y[t][r]) = make_float4(p.c_y * v.x, p.c_y * v.y, p.c_y * v.z, p.c_y * v.w);
             if (has_z) *reinterpret_cast<float4*>(&s.z[t][r]) = F::of(vz[i]);
@@ -242,16 +248,16 @@ decay_walk_kernel(const Walk p) {
                 // lanes read neighbouring rows, which are in different banks), its diagonal apart;
                 // even and odd channels are added up apart
                 const int ta = tid / 16, ua = tid % 16;
-                float2 a[NT][2] = {};
+                float2 a[NP][2] = {};
 #pragma unroll 2
                 for (int c = 0; c < CD; c += 4) {
-                    float4 xv[NT], wv[2];
+                    float4 xv[NP], wv[2];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[ta + WT / 16 * i][c]);
+                    for (int i = 0; i < NP; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[ta + WT / 16 * i][c]);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) wv[j] = *reinterpret_cast<const float4*>(&s.w[ua + 16 * j][c]);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+                    for (int i = 0; i < NP; ++i)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             fma2(a[i][j].x, a[i][j].y, xv[i].x, xv[i].y, wv[j].x, wv[j].y, a[i][j].x, a[i][j].y);
@@ -259,7 +265,7 @@ decay_walk_kernel(const Walk p) {
                         }
                 }
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+                for (int i = 0; i < NP; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int t = ta + WT / 16 * i, u = ua + 16 * j;
@@ -271,7 +277,7 @@ decay_walk_kernel(const Walk p) {
             }
             __syncthreads();
             // out: NT tokens x 4 rows
-            const int tb = NT * (tid / 16);
+            const int tb = NT * (tid / LR);
             float a[NT][4] = {};
             auto add = [&](float (&o)[4], float q, const float4& v) {
                 o[0] = fmaf(q, v.x, o[0]);
@@ -323,8 +329,8 @@ decay_walk_kernel(const Walk p) {
                     const float4 zv = *reinterpret_cast<const float4*>(&s.z[t][r]);
                     float d = zv.x * a[i][0] + zv.y * a[i][1] + zv.z * a[i][2] + zv.w * a[i][3];
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                    if (tid % 16 == 0 && t < m) p.dots[(size_t)blockIdx.y * p.seq.rows * p.H + row] = p.c_out * d;
+                    for (int o = LR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if (tid % LR == 0 && t < m) p.dots[(size_t)blockIdx.y * p.seq.rows * p.H + row] = p.c_out * d;
                 }
                 if (t < m && r0 + r < p.RD) {
                     add(a[i], s.own[t], *reinterpret_cast<const float4*>(&s.y[t][r]));
@@ -334,11 +340,12 @@ decay_walk_kernel(const Walk p) {
                 }
             }
         }
-        const int c0 = tid / 16 * NC;  // this thread's columns of R
+        const int c0 = tid / LR * NC;  // this thread's columns of R
+        const bool has_r = CD * LR >= WT || c0 < CD;
         if (!MAP && REV && p.cross && border) {
             // R is dS^T at the end of this chunk: dot it with the state there
             float d = 0.f;
-            if (r0 + r < p.RD) {
+            if (has_r && r0 + r < p.RD) {
                 const float* A = p.anchor + (((size_t)slot * p.H + h) * p.RD + r0 + r) * CD + c0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -356,7 +363,7 @@ decay_walk_kernel(const Walk p) {
         }
         const float total = start_decay(s.g[TT - 1]);
         all *= total;
-        {   // R; a thread: NC columns x 4 rows
+        if (has_r) {  // R; a thread: NC columns x 4 rows
             float a[NC][4];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -480,31 +487,40 @@ decay_group_sum_kernel(Seqs q, int Hk, int rep, int d, const float* __restrict__
     }
 }
 
-template <int CD, typename T, bool REV, int WT>
+template <int CD, int RB, typename T, bool REV, int WT>
 void launch_walk_of(const Walk& w, cudaStream_t st) {
     const auto grid = [&](int runs) { return dim3((unsigned)(items(w.seq, runs, w.len * TT) * w.H), (w.RD + RB - 1) / RB); };
-    const int smem = sizeof(WalkSmem<CD>);
+    const int smem = sizeof(WalkSmem<CD, RB>);
     if (w.runs > 1) {
-        cudaFuncSetAttribute(decay_walk_kernel<CD, T, REV, true, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        GDN_LAUNCH("decay_map", st, (decay_walk_kernel<CD, T, REV, true, WT><<<w.seq.cu ? grid(w.runs) : grid(w.runs - 1), WT, smem, st>>>(w)));
+        auto* map = decay_walk_kernel<CD, RB, T, REV, true, WT>;
+        cudaFuncSetAttribute(map, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        GDN_LAUNCH("decay_map", st, (map<<<w.seq.cu ? grid(w.runs) : grid(w.runs - 1), WT, smem, st>>>(w)));
     }
-    cudaFuncSetAttribute(decay_walk_kernel<CD, T, REV, false, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    GDN_LAUNCH(REV ? "decay_walk_rev" : "decay_walk", st, (decay_walk_kernel<CD, T, REV, false, WT><<<grid(w.runs), WT, smem, st>>>(w)));
+    auto* walk = decay_walk_kernel<CD, RB, T, REV, false, WT>;
+    cudaFuncSetAttribute(walk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    GDN_LAUNCH(REV ? "decay_walk_rev" : "decay_walk", st, (walk<<<grid(w.runs), WT, smem, st>>>(w)));
+}
+
+template <int CD, typename T, bool REV>
+void launch_walk_rows(const Walk& w, cudaStream_t st) {
+    if (w.RD == 16) launch_walk_of<CD, 16, T, REV, 128>(w, st);
+    else if (w.RD == 32) launch_walk_of<CD, 32, T, REV, 128>(w, st);
+    else if constexpr (CD < 128) launch_walk_of<CD, kRows, T, REV, 256>(w, st);
+    else if (w.wide) launch_walk_of<CD, kRows, T, REV, 256>(w, st);
+    else launch_walk_of<CD, kRows, T, REV, 128>(w, st);
 }
 
 template <typename T, bool REV>
 void launch_walk(const Walk& w, int CD, cudaStream_t st) {
     switch (CD) {
-        case 16: launch_walk_of<16, T, REV, 256>(w, st); break;
-        case 32: launch_walk_of<32, T, REV, 256>(w, st); break;
-        case 64: launch_walk_of<64, T, REV, 256>(w, st); break;
-        default:
-            if (w.wide) launch_walk_of<128, T, REV, 256>(w, st);
-            else launch_walk_of<128, T, REV, 128>(w, st);
+        case 16: launch_walk_rows<16, T, REV>(w, st); break;
+        case 32: launch_walk_rows<32, T, REV>(w, st); break;
+        case 64: launch_walk_rows<64, T, REV>(w, st); break;
+        default: launch_walk_rows<128, T, REV>(w, st);
     }
 }
 
-int row_blocks(int RD) { return (RD + RB - 1) / RB; }
+int row_blocks(int RD) { return (RD + kRows - 1) / kRows; }
 
 // Runs per chain, of whole chunks: 1 when the chains fill the device.  Estimated in
 // tiles on the critical path: a tile of the map costs a third of one of the walk, the

@@ -290,8 +290,9 @@ def test_prompt_then_steps_is_one_prompt(dev):
     check(dict(o=torch.cat([o1, torch.stack(steps, 1)], 1), hT=S), x, scale=0.5)
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (16, 128), (128, 32)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_many_packed_sequences_in_runs(dev, dtype):
+def test_many_packed_sequences_in_runs(dev, dtype, dk, dv):
     """More sequences than a warp has lanes, of one head, so that the longer ones are cut
     into runs; empty ones among them."""
     gen = torch.Generator().manual_seed(61)
@@ -300,7 +301,7 @@ def test_many_packed_sequences_in_runs(dev, dtype):
     cu = [0]
     for n in lens:
         cu.append(cu[-1] + n)
-    x = make(1, cu[-1], 1, 1, 64, 64, dtype, seed=14, nstates=len(lens), shift=-3.0)
+    x = make(1, cu[-1], 1, 1, dk, dv, dtype, seed=14, nstates=len(lens), shift=-3.0)
     check(run(x, dev, cu=cu, scale=0.7), x, cu=cu, scale=0.7, T=700)
 
 
