@@ -28,11 +28,11 @@
 //     out_t = c (f_t R x_t + sum_s D_ts (w_s.x_t) y_s),   R <- e^{G_last} R + sum_s h_s y_s w_s^T
 // over s <= t, with f = e^G and h = e^{G_last - G} forwards, and over s >= t, with the two
 // exchanged, backwards.  All of it is small matrix products in fp32 on CUDA cores, from
-// shared memory in register tiles (2 x 2, 2 x 4 and 4 x 4 with 256 threads); a CTA holds
+// shared memory in register tiles (2 x 2 and 4 x 4 with 256 threads); a CTA holds
 // 64 rows of R.  What bounds it is the issue of fp32 FMAs and, 1.5 to 2 times as long, the
 // shared-memory loads that feed them (a 16-byte load takes four cycles of the SM's 128
-// bytes per cycle, whatever its lanes share): 8,100 of them per tile of 64 x 64 dims.
-// Forward, 32 x 1024 tokens of 8 heads: 312 us at 64 x 64 dims, 1,010 us at 128 x 128.
+// bytes per cycle, whatever its lanes share): about 6,700 of them per tile of 64 x 64 dims.
+// Forward, 32 x 1024 tokens of 8 heads: 281 us at 64 x 64 dims, 1,010 us at 128 x 128.
 #include <math.h>
 
 #include <algorithm>
@@ -104,10 +104,11 @@ GDN_DEV void put4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-template <int CD, int RB>
+template <int CD, int RB, int WT>
 struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in different banks
     float x[TT][CD + 4], w[TT][CD + 4], y[TT][RB + 4], z[TT][RB + 4], p[TT][TT + 4];
     float r[CD][RB + 4];
+    float4 half[2][TT * RB / 4 / WT][WT == 256 && CD < 128 ? WT / 2 : 1];
     float2 g[TT];
     float f[TT], h[TT], own[TT], red[8];
 };
@@ -118,13 +119,13 @@ struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in dif
 // threads have the larger register tiles, and so fewer loads from shared memory per
 // product; 256 hide its latency better, with the next tile's rows on their way while this
 // one is worked on.  128 columns: 256 where a CTA has an SM to itself (777 tokens of
-// 4 heads: 63 us against 95), else 128 (32 x 1024 tokens of 8 heads: 1,010 us against
+// 4 heads: 71 us against 95), else 128 (32 x 1024 tokens of 8 heads: 1,010 us against
 // 1,304).  Fewer columns: 256 throughout (within 2 % at that size, faster with few CTAs).
 template <int CD, int RB, typename T, bool REV, bool MAP, int WT>
 __global__ void __launch_bounds__(WT)
 decay_walk_kernel(const Walk p) {
     extern __shared__ __align__(16) unsigned char raw[];
-    WalkSmem<CD, RB>& s = *reinterpret_cast<WalkSmem<CD, RB>*>(raw);
+    WalkSmem<CD, RB, WT>& s = *reinterpret_cast<WalkSmem<CD, RB, WT>*>(raw);
     using F = Four<T>;
     constexpr int NX = TT * CD / 4 / WT > 0 ? TT * CD / 4 / WT : 1;  // groups of four per thread and tile
     constexpr int LR = RB / 4;                                       // lanes of a row of out
@@ -132,6 +133,11 @@ decay_walk_kernel(const Walk p) {
     constexpr int NY = TT * LR / WT, NT = TT * LR / WT;              // rows of y, tokens of out per thread
     constexpr int NP = TT * 16 / WT;                                 // rows of p per thread
     static_assert(NT >= 1, "a thread has a token");
+    // 256 threads: two halves of them take half of each sum over channels and tokens, in
+    // 4 x 4 tiles, and each finishes half of the tokens (64 x 64 dims, 32 x 1024 tokens of
+    // 8 heads: 281 us against 310 in 2 x 4 tiles; with 128 columns, 80 against 77 for 777
+    // tokens of 4 heads, so not there)
+    constexpr int KS = WT == 256 && CD < 128 ? 2 : 1;
     const int h = blockIdx.x % p.H, r0 = blockIdx.y * RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long tok0;
@@ -179,7 +185,7 @@ decay_walk_kernel(const Walk p) {
     float all = 1.f;  // the decay of the run so far
     const bool has_z = !MAP && p.dots != nullptr;
     constexpr bool AHEAD = WT == 256 || (RB < kRows && CD < 128);
-    const int r = 4 * (tid % LR);  // this thread's rows of R
+    const int r = 4 * (tid % LR), part = KS == 2 ? tid / (WT / KS) : 0;  // this thread's rows of R, and half
     typename F::Raw vx[NX], vw[NX], vy[NY], vz[NY];  // all on their way before any is put down
     float pg = 0.f;
     auto fetch = [&](int it) {
@@ -243,6 +249,13 @@ decay_walk_kernel(const Walk p) {
         }
         __syncthreads();
         if (AHEAD && it + 1 < i1) fetch(it + 1);
+        float sum[NT][4];
+        auto add = [&](float (&o)[4], float q, const float4& v) {
+            o[0] = fmaf(q, v.x, o[0]);
+            o[1] = fmaf(q, v.y, o[1]);
+            o[2] = fmaf(q, v.z, o[2]);
+            o[3] = fmaf(q, v.w, o[3]);
+        };
         if constexpr (!MAP) {
             {   // p[t][u] = D_tu (w_u . x_t) for t = tid / 16 + WT / 16 i, u = tid % 16 + 16 j (neighbouring
                 // lanes read neighbouring rows, which are in different banks), its diagonal apart;
@@ -276,24 +289,18 @@ decay_walk_kernel(const Walk p) {
                     }
             }
             __syncthreads();
-            // out: NT tokens x 4 rows
-            const int tb = NT * (tid / LR);
-            float a[NT][4] = {};
-            auto add = [&](float (&o)[4], float q, const float4& v) {
-                o[0] = fmaf(q, v.x, o[0]);
-                o[1] = fmaf(q, v.y, o[1]);
-                o[2] = fmaf(q, v.z, o[2]);
-                o[3] = fmaf(q, v.w, o[3]);
-            };
+            // out: KS NT tokens x 4 rows, over this half of the channels and of the tile's tokens
+            const int tb = KS * NT * (tid % (WT / KS) / LR);
+            float a[KS * NT][4] = {};
 #pragma unroll 2
-            for (int c = 0; c < CD; c += 4) {
-                float4 xv[NT], rv[4];
+            for (int c = part * (CD / KS); c < (part + 1) * (CD / KS); c += 4) {
+                float4 xv[KS * NT], rv[4];
 #pragma unroll
-                for (int i = 0; i < NT; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[tb + i][c]);
+                for (int i = 0; i < KS * NT; ++i) xv[i] = *reinterpret_cast<const float4*>(&s.x[tb + i][c]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rv[i] = *reinterpret_cast<const float4*>(&s.r[c + i][r]);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
+                for (int i = 0; i < KS * NT; ++i) {
                     add(a[i], xv[i].x, rv[0]);
                     add(a[i], xv[i].y, rv[1]);
                     add(a[i], xv[i].z, rv[2]);
@@ -301,42 +308,35 @@ decay_walk_kernel(const Walk p) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
+            for (int i = 0; i < KS * NT; ++i) {
                 const float f = s.f[tb + i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[i][j] *= f;
             }
 #pragma unroll 2
-            for (int u = 0; u < TT; u += 4) {
-                float4 pv[NT], yv[4];
+            for (int u = part * (TT / KS); u < (part + 1) * (TT / KS); u += 4) {
+                float4 pv[KS * NT], yv[4];
 #pragma unroll
-                for (int i = 0; i < NT; ++i) pv[i] = *reinterpret_cast<const float4*>(&s.p[tb + i][u]);
+                for (int i = 0; i < KS * NT; ++i) pv[i] = *reinterpret_cast<const float4*>(&s.p[tb + i][u]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) yv[i] = *reinterpret_cast<const float4*>(&s.y[u + i][r]);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
+                for (int i = 0; i < KS * NT; ++i) {
                     add(a[i], pv[i].x, yv[0]);
                     add(a[i], pv[i].y, yv[1]);
                     add(a[i], pv[i].z, yv[2]);
                     add(a[i], pv[i].w, yv[3]);
                 }
             }
+            // half of the tokens' sums go to the other half's threads, the other half come from them
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const int t = tb + i;
-                const size_t row = (size_t)(t0 + t) * p.H + h;
-                if (has_z) {
-                    const float4 zv = *reinterpret_cast<const float4*>(&s.z[t][r]);
-                    float d = zv.x * a[i][0] + zv.y * a[i][1] + zv.z * a[i][2] + zv.w * a[i][3];
 #pragma unroll
-                    for (int o = LR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                    if (tid % LR == 0 && t < m) p.dots[(size_t)blockIdx.y * p.seq.rows * p.H + row] = p.c_out * d;
-                }
-                if (t < m && r0 + r < p.RD) {
-                    add(a[i], s.own[t], *reinterpret_cast<const float4*>(&s.y[t][r]));
-                    const float4 v = make_float4(p.c_out * a[i][0], p.c_out * a[i][1], p.c_out * a[i][2], p.c_out * a[i][3]);
-                    if (p.out_f32) put4((float*)p.out + row * p.RD + r0 + r, v);
-                    else put4((T*)p.out + row * p.RD + r0 + r, v);
+                for (int j = 0; j < 4; ++j) sum[i][j] = KS == 2 && part ? a[(KS - 1) * NT + i][j] : a[i][j];
+                if constexpr (KS == 2) {
+                    const int g = (KS - 1) * NT + i;
+                    s.half[part][i][tid % (WT / KS)] = part ? make_float4(a[i][0], a[i][1], a[i][2], a[i][3])
+                                                            : make_float4(a[g][0], a[g][1], a[g][2], a[g][3]);
                 }
             }
         }
@@ -360,6 +360,31 @@ decay_walk_kernel(const Walk p) {
             float d = 0.f;
             for (int w = 0; w < WT / 32; ++w) d += s.red[w];
             p.cross[((size_t)blockIdx.y * chunk_slots(p.seq, AC) + slot) * p.H + h] = d;
+        }
+        if constexpr (!MAP) {
+            const int t_out = KS * NT * (tid % (WT / KS) / LR) + part * NT;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int t = t_out + i;
+                if constexpr (KS == 2) {
+                    const float4 v = s.half[1 - part][i][tid % (WT / KS)];
+                    sum[i][0] += v.x; sum[i][1] += v.y; sum[i][2] += v.z; sum[i][3] += v.w;
+                }
+                const size_t row = (size_t)(t0 + t) * p.H + h;
+                if (has_z) {
+                    const float4 zv = *reinterpret_cast<const float4*>(&s.z[t][r]);
+                    float d = zv.x * sum[i][0] + zv.y * sum[i][1] + zv.z * sum[i][2] + zv.w * sum[i][3];
+#pragma unroll
+                    for (int o = LR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if (tid % LR == 0 && t < m) p.dots[(size_t)blockIdx.y * p.seq.rows * p.H + row] = p.c_out * d;
+                }
+                if (t < m && r0 + r < p.RD) {
+                    add(sum[i], s.own[t], *reinterpret_cast<const float4*>(&s.y[t][r]));
+                    const float4 v = make_float4(p.c_out * sum[i][0], p.c_out * sum[i][1], p.c_out * sum[i][2], p.c_out * sum[i][3]);
+                    if (p.out_f32) put4((float*)p.out + row * p.RD + r0 + r, v);
+                    else put4((T*)p.out + row * p.RD + r0 + r, v);
+                }
+            }
         }
         const float total = start_decay(s.g[TT - 1]);
         all *= total;
@@ -490,7 +515,7 @@ decay_group_sum_kernel(Seqs q, int Hk, int rep, int d, const float* __restrict__
 template <int CD, int RB, typename T, bool REV, int WT>
 void launch_walk_of(const Walk& w, cudaStream_t st) {
     const auto grid = [&](int runs) { return dim3((unsigned)(items(w.seq, runs, w.len * TT) * w.H), (w.RD + RB - 1) / RB); };
-    const int smem = sizeof(WalkSmem<CD, RB>);
+    const int smem = sizeof(WalkSmem<CD, RB, WT>);
     if (w.runs > 1) {
         auto* map = decay_walk_kernel<CD, RB, T, REV, true, WT>;
         cudaFuncSetAttribute(map, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
