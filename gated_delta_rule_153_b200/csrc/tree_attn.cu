@@ -795,7 +795,8 @@ gdn_status check(int N, int M, int Hq, int Hkv, int d, gdn_dtype dtype, int page
     if (N < 1 || M < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || pages < 1 || width < 1) return GDN_ERR_INVALID_ARG;
     if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
     if ((long long)N * M * Hq > 0x7fffffffLL || (long long)pages * page > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
-    if ((long long)width * page > 0x7fffffffLL - kMaxNodes) return GDN_ERR_INVALID_ARG;
+    // positions, rounded up to whole key tiles and with the nodes behind them, are 32-bit
+    if ((long long)width * page > 0x7fffffffLL - 2 * KT) return GDN_ERR_INVALID_ARG;
     if (M > kMaxNodes || dtype != GDN_BF16 || (d != 64 && d != 128)) return GDN_ERR_UNSUPPORTED;
     if (page != 16 && page != 32 && page != 64 && page != 128) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;

@@ -101,6 +101,7 @@ def append(N=2, M=4, Hkv=2, d=64, dtype=BF, pages=9, page=16, width=4, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(N=0), INV), (dict(M=0), INV), (dict(Hkv=0), INV), (dict(pages=0), INV), (dict(width=0), INV),
     (dict(dtype=4), INV), (dict(pages=1 << 30, page=128), INV), (dict(width=1 << 30, page=128), INV),
+    (dict(width=(1 << 24) - 1, page=128), INV),
     (dict(M=65), UNS), (dict(d=96), UNS), (dict(d=256), UNS), (dict(dtype=F32), UNS), (dict(page=48), UNS),
     (dict(page=256), UNS)])
 def test_tree_dims(kw, code):
