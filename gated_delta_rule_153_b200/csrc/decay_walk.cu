@@ -63,6 +63,9 @@ constexpr int kEpi = 8, kState = 8;  // warps that make P and O, and that own th
 // Warps that split V: four of their own in MODE 0, else the eight that P and O leave idle.
 template <int MODE>
 constexpr int kSplit = MODE == 0 ? 4 : kEpi;
+// Whether the state's warps split a quarter of V: where they do not write images too.
+template <int MODE>
+constexpr bool kShare = MODE != 2;
 template <int MODE>
 constexpr int kThreads = 32 * (kEpi + kState + 3 + (MODE == 0 ? 4 : MODE == 2 ? 1 : 0));
 constexpr int NST = 2;
@@ -140,7 +143,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.v_free[i], kSplit<MODE>);
+            mbar_init(&s.v_free[i], kSplit<MODE> + (kShare<MODE> ? kState : 0));
             mbar_init(&s.n_done[i], 1);
             mbar_init(&s.o_done[i], 1);
             mbar_init(&s.gfull[i], 1);
@@ -153,7 +156,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         mbar_init(&s.fwd_free, kState);
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
-        mbar_init(&s.vt_ready, kSplit<MODE> + (MODE == 0 ? kState : 0));
+        mbar_init(&s.vt_ready, kSplit<MODE> + (kShare<MODE> ? kState : 0));
         mbar_init(&s.s_ready, kState);
         mbar_init(&s.x_done, 1);
         mbar_init(&s.o_free, kEpi + kState);
@@ -206,9 +209,9 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 *reinterpret_cast<uint4*>(s.Vt[k] + at) = make_uint4(t[q][k][0], t[q][k][1], t[q][k][2], t[q][k][3]);
         }
     };
-    // The warps of its own (MODE 0: pieces 0 .. 5 of 8, the others are the state warps'), w = 0 ..
+    // The warps of its own (with kShare pieces 0 .. 5 of 8, the others are the state warps'), w = 0 ..
     auto split = [&](int w) {
-        constexpr int NP = MODE == 0 ? 3 : 4;  // the first NP are made while the products still read the terms before
+        constexpr int NP = kShare<MODE> ? 3 : 4;  // the first NP are made while the products still read the terms before
         const int r = 32 * (w & 3) + lane, part = w >> 2;
         for (int c = 0; c < nc; ++c) {
             const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
@@ -407,21 +410,25 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             const int st = c % NST, L = min(CT, n - chunk_of(c) * CT);
             float next_ein = 0.f, next_total = 0.f;
             uint32_t t[1][TERMS][4];
-            if constexpr (MODE == 0) {
+            if constexpr (kShare<MODE>) {
                 if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
-                next_ein = p.scale * start_decay(s.gate[st].G[r]);
+                if (MODE == 0) next_ein = p.scale * start_decay(s.gate[st].G[r]);
                 next_total = start_decay(s.gate[st].G[CT - 1]);
                 const float wt = weight(st, r, L);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.gfree[st]);
                 if (!(ok = warp_wait(&s.v_full[st], (c / NST) & 1))) break;
                 make(t, st, r, 6 + half, wt, r < L);
+                if (MODE != 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.v_free[st]);
+                }
             }
             if (c > 0) {  // S entering chunk c; X(c-1), which read the last one, came before N(c-1)
                 if (!(ok = warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1))) break;
                 tc5::fence_after();
             }
-            if constexpr (MODE == 0) {
+            if constexpr (kShare<MODE>) {
                 put(t, r, 6 + half);
                 fence_async_smem();
                 __syncwarp();
@@ -442,13 +449,13 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.s_ready);
             if (MODE == 0 && c > 0 && !(ok = out(c - 1, r, 32 * half, ein))) break;
-            if constexpr (MODE == 0) {
+            if constexpr (kShare<MODE>) {
                 ein = next_ein;
                 total = next_total;
+                decay *= total;
             } else {
                 if (!(ok = warp_wait(&s.gfull[st], (c / NST) & 1))) break;
                 total = start_decay(s.gate[st].G[CT - 1]);
-                decay *= total;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.gfree[st]);
             }
