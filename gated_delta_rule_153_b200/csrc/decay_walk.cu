@@ -88,7 +88,7 @@ struct alignas(1024) Smem {
     float col[kEpi][CT];         // per warp of P: the column factors of its decays
     // of each stage, so that nobody who waits for one can fall two phases behind
     uint64_t full[NST], v_full[NST], v_free[NST], gfull[NST], gfree[NST], n_done[NST], o_done[NST];
-    uint64_t img_ready, img_free, fwd_full, fwd_free, q_full, a_done, p_ready, vt_ready, s_ready, x_done, o_free, drain;
+    uint64_t img_ready, img_free, fwd_full, fwd_free, q_full, a_done, p_ready, vt_ready, s_ready[2], x_done, o_free, drain;
     uint32_t tmem;
 };
 
@@ -111,6 +111,9 @@ struct Params {
 
 // tensor-memory columns: A, P (bf16 pairs), X, Y, N (the terms of V apart)
 constexpr uint32_t TA = 0, TP = 128, TX = 192, TY = 256, TN = 320, kCols = 512;
+// N of chunk c: without the others it has two places
+template <int MODE>
+GDN_DEV uint32_t tn(int c) { return MODE == 0 ? TN : 3 * NB * (c & 1); }
 
 template <int DK, int MODE, bool REV>
 __global__ void __launch_bounds__(kThreads<MODE>, 1)
@@ -157,7 +160,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         mbar_init(&s.a_done, 1);
         mbar_init(&s.p_ready, kEpi);
         mbar_init(&s.vt_ready, kSplit<MODE> + (kShare<MODE> ? kState : 0));
-        mbar_init(&s.s_ready, kState);
+        mbar_init(&s.s_ready[0], kState);
+        mbar_init(&s.s_ready[1], kState);
         mbar_init(&s.x_done, 1);
         mbar_init(&s.o_free, kEpi + kState);
         mbar_init(&s.drain, 1);
@@ -394,11 +398,11 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         }
         bool ok = true;
         float total = 1.f, decay = 1.f, ein = 0.f;
-        auto add_n = [&]() {  // S <- e^{G_last} S + N, N in one accumulator per term of V
+        auto add_n = [&](int c) {  // S <- e^{G_last} S + N(c), N in one accumulator per term of V
 #pragma unroll 1
             for (int x = 0; x < TERMS; ++x) {
                 float N[32];
-                tc5::ld32(N, trow + TN + NB * x + 32 * half);
+                tc5::ld32(N, trow + tn<MODE>(c) + NB * x + 32 * half);
                 tc5::wait_ld();
                 const float a = x ? 1.f : total;
 #pragma unroll
@@ -434,7 +438,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.vt_ready);
             }
-            if (c > 0) add_n();
+            if (c > 0) add_n(c - 1);
             if constexpr (MODE == 0) {
                 if (own) {
 #pragma unroll
@@ -447,7 +451,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             }
             // N(c-1) is in the registers (and, MODE 0, S where X finds it)
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.s_ready);
+            if (lane == 0) mbar_arrive(&s.s_ready[c & 1]);
             if (MODE == 0 && c > 0 && !(ok = out(c - 1, r, 32 * half, ein))) break;
             if constexpr (kShare<MODE>) {
                 ein = next_ein;
@@ -507,7 +511,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             if (MODE == 0 && !out(nc - 1, r, 32 * half, ein)) --done;
             if (warp_wait(&s.n_done[(nc - 1) % NST], ((nc - 1) / NST) & 1)) {
                 tc5::fence_after();
-                add_n();
+                add_n(nc - 1);
             }
         }
         if (own) {
@@ -598,7 +602,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                     tc5::commit(&s.a_done);
                 }
                 __syncwarp();
-                if (!warp_wait(&s.s_ready, c & 1)) break;
+                if (!warp_wait(&s.s_ready[c & 1], (c >> 1) & 1)) break;
                 if (c > 0 && !warp_wait(&s.o_free, (c - 1) & 1)) break;
                 tc5::fence_after();
                 if (elect_one()) {
@@ -610,12 +614,14 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
             }
             // N(c); with 64 key channels lanes 64-127 read the V tile behind K and are ignored
-            if (MODE != 0 && (!warp_wait(&s.full[st], (c / NST) & 1) || !warp_wait(&s.s_ready, c & 1))) break;
+            // (MODE 1, 2: where N(c-2) was, which is in the registers once S entering c - 1 is)
+            if (MODE != 0 && !warp_wait(&s.full[st], (c / NST) & 1)) break;
+            if (MODE != 0 && c > 0 && !warp_wait(&s.s_ready[(c - 1) & 1], ((c - 1) >> 1) & 1)) break;
             if (!warp_wait(&s.vt_ready, c & 1)) break;
             tc5::fence_after();
             if (elect_one()) {
 #pragma unroll 2
-                for (int k = 0; k < CT / 16; ++k) tc5::mma(tm + TN, dKt + k * KROWS, dVt + k * KROWS, ID_N, k > 0);
+                for (int k = 0; k < CT / 16; ++k) tc5::mma(tm + tn<MODE>(c), dKt + k * KROWS, dVt + k * KROWS, ID_N, k > 0);
                 tc5::commit(&s.n_done[st]);
             }
             __syncwarp();
