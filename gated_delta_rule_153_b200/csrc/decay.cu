@@ -551,7 +551,7 @@ int row_blocks(int RD) { return (RD + kRows - 1) / kRows; }
 // tiles on the critical path: a tile of the map costs a third of one of the walk, the
 // second launch about four, and adding up what the runs before leave 0.1 each.  Packed
 // sequences have rows / length + nseq runs together, however long the longest is.  (7
-// packed sequences of up to 1002 tokens, 6 heads, 64 x 64: runs of 4 tiles 53 us, whole
+// packed sequences of up to 1002 tokens, 6 heads, 64 x 64: runs of 4 tiles 49 us, whole
 // chains 197 us.)
 struct Cut {
     int runs, len;

@@ -26,7 +26,7 @@
 // next chunk start as each operand is done with.
 //
 // What bounds it, at 8 x 2048 tokens of 8 heads, dk = dv = 128 (1,024 chunk-heads, seven
-// per SM): 104 us, 15 us a chunk, 3.3 TB/s of DRAM traffic (356 MB, S and dS are 134 of
+// per SM): 105 us, 15 us a chunk, 3.3 TB/s of DRAM traffic (356 MB, S and dS are 134 of
 // them) with the tensor pipe busy for a quarter.  The four rounds of products and elementwise
 // work of a chunk wait for one another, and shared memory (230 KB) and tensor memory
 // (all 512 columns) hold one chunk.  Results leave by TMA from shared memory.

@@ -39,11 +39,11 @@
 // sum of the runs before it.
 //
 // What bounds it, at 8 x 2048 tokens of 8 heads, dk = dv = 128 (128 chains of 16
-// chunks): MODE 0 takes 52 us, 2.6 TB/s of the bytes it cannot do without.  A chunk takes
+// chunks): MODE 0 takes 51 us, 2.6 TB/s of the bytes it cannot do without.  A chunk takes
 // 4,500 cycles: A, P (2,000 cycles: two warps per scheduler, latency), Y, O, each waiting
 // for the one before, with X and N in between; the tensor pipe is busy for a third of them.
 // With O left to the warps of P alone it took 55 us (5,200 cycles), with O left to the
-// state's 53 us.  MODE 2 takes 32 us forwards and 45 us backwards: 2,900 and 3,700
+// state's 53 us.  MODE 2 takes 33 us forwards and 44 us backwards: 2,500 and 3,700
 // cycles, of which the copies of 80 KB (forwards 48 KB and the 32 KB image out, backwards
 // the forward image as well) at the 26 bytes per cycle that an SM gets from HBM are most.
 #include <math.h>
@@ -697,8 +697,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
 // step of the walk costs about 1, one of the map (MODE 1) about 0.7, the second launch
 // about 4, and adding up what the runs before leave 0.2 each.  Packed sequences have
 // rows / length + nseq runs together, however long the longest is.  (16 heads of 8192
-// tokens: 4 runs 85 us, 1 run 169 us.  9 packed sequences of up to 968 tokens, 8 heads:
-// runs of 3 chunks 33 us, whole chains 31 us.)
+// tokens: 4 runs 81 us, 1 run 169 us.  9 packed sequences of up to 968 tokens, 8 heads:
+// runs of 3 chunks 33 us, whole chains 29 us.)
 struct Cut {
     int runs, len;
 };
@@ -762,8 +762,8 @@ void launch_runs(const Params& a, const Problem& p, cudaStream_t st) {
 }  // namespace
 
 // The dims that fill whole 64-channel panels; the products of smaller ones would be
-// padding for the most part.  (16 heads of 8192 tokens, 128 x 128: 85 us here and 767 us
-// on CUDA cores; the 350M-scale training step 237 us and 2.9 ms.)
+// padding for the most part.  (16 heads of 8192 tokens, 128 x 128: 81 us here and 767 us
+// on CUDA cores; the 350M-scale training step 232 us and 2.9 ms.)
 bool tc_supported(const Problem& p) {
     return p.dtype == GDN_BF16 && (p.dk == 64 || p.dk == 128) && (p.dv == 64 || p.dv == 128);
 }
