@@ -44,10 +44,10 @@ template <int DK, int DV>
 struct alignas(1024) Smem {
     unsigned char Q[DK / 64][PANEL], K[DK / 64][PANEL], V[DV / 64][PANEL], Y[DV / 64][PANEL];  // Y = dO
     unsigned char S[2][DV / 64][DK * 128];  // the two terms of S, then of dS
-    // Results on their way out: dq, then dk and dv.  At the largest dims they go by way of S: dq
-    // through its second term, between its last use and the arrival of dS's, dk and dv
-    // through both, between dS and the next chunk's S, which only the second
-    // products of that chunk need.
+    // Results on their way out: dq, then dk and dv, each once the store before it has read
+    // its source.  At the largest dims they go by way of S: dq through its second term,
+    // between its last use and the arrival of dS's, dk and dv through both, between dS and
+    // the next chunk's S, which only the second products of that chunk need.
     static constexpr bool kOwnOut = DK + DV < 256;
     unsigned char O[kOwnOut ? (DK + DV) / 64 : 1][kOwnOut ? PANEL : 16];
     GDN_DEV unsigned char* out_q() { return kOwnOut ? O[0] : S[1][0]; }
@@ -586,6 +586,9 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             }
             if (!(ok = warp_wait(&s.e3[ph], (x >> 1) & 1))) break;  // K's rows are read by then too
             tc5::fence_after();
+            // dk, written after the products below, goes where the store of dq reads
+            if (s.kOwnOut && lane == 0) bulk_wait_read<0>();
+            __syncwarp();
             if (un < units) {
                 load_kv(un, nx);
                 ++nkv;
