@@ -261,8 +261,8 @@ tree_attn_kernel(const __grid_constant__ Params p) {
         w.span = span_of(p, w.n);
         pieces = max(1, min(p.split, w.span.steps / 2));
         if (q < pieces) {
-            w.at = (long long)(unit % units) * w.span.steps + w.span.steps * q / pieces;
-            w.end = (long long)(unit % units) * w.span.steps + w.span.steps * (q + 1) / pieces;
+            w.at = (long long)(unit % units) * w.span.steps + share_start(w.span.steps, pieces, q);
+            w.end = (long long)(unit % units) * w.span.steps + share_start(w.span.steps, pieces, q + 1);
         }
     } else if (b < parts) {
         w = Walk{share_start(s.total, parts, b), share_start(s.total, parts, b + 1), s.before, s.n0, {}};
