@@ -608,7 +608,8 @@ tree_attn_kernel(const __grid_constant__ Params p) {
                 }
                 const int pos = (g.span.first + t) * KT + lane * p.c.page;
                 int pg = -1;
-                if (lane < pages && pos < g.span.len) {
+                // (a page wholly before the window may have been given back: its entry is not read)
+                if (lane < pages && pos < g.span.len && (p.window == 0 || pos + p.c.page > g.span.len - p.window + 1)) {
                     pg = p.c.table[(size_t)g.n * p.c.width + pos / p.c.page];
                     if (pg < 0 || pg >= p.c.pages) {
                         atomicOr(p.status, 2u);

@@ -406,7 +406,8 @@ gdn_status gdn_decay_step(int N, int H, int Hk, int dk, int dv, gdn_dtype dtype,
  * block_table [N, width] int32; q, o [N, M, Hq, d]; k, v [N, M, Hkv, d];
  * k_cache, v_cache [pages, page, Hkv, d].  Position p of sequence n is row
  * p % page of page block_table[n, p / page]; entries past the last used page
- * are not read.  Pages may be shared by sequences, but not one that is appended
+ * are not read, and with a window neither are those of pages that end before
+ * cache_len - window + 1 (a rolling cache may have given them back).  Pages may be shared by sequences, but not one that is appended
  * to.
  * GDN_BF16, d in {64, 128}, page in {16, 32, 64, 128}, M <= 64 (else
  * GDN_ERR_UNSUPPORTED).  Device data is checked on the device: a parent out of
