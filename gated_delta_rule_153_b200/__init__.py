@@ -736,19 +736,28 @@ def _want(t, name, dtype, shape, device):
 
 
 _CODES = {}  # torch dtypes of q, k, v and the like, filled on first use
+_INT = 2 ** 31 - 1  # the library's sizes are C ints, and ctypes would drop the higher bits
+
+
+def _int(n, name):
+    """A size that fits a C int."""
+    if n > _INT:
+        raise ValueError(f"{name} = {n} is more than {_INT}")
+    return n
 
 
 def _lead(t, name, dims):
     """The first tensor of a call: (dtype code, device, shape)."""
     try:
         code, shape = _CODES[t.dtype], t.shape
-        if len(shape) == dims and t.is_cuda and t.is_contiguous():
+        if len(shape) == dims and t.is_cuda and t.is_contiguous() and max(shape) <= _INT:
             return code, t.device, shape
     except (KeyError, AttributeError):
         pass
     _need(t, name)
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
+    _int(max(t.shape), f"a size of {name}")
     _CODES[t.dtype] = _dtype_code(t)
     return _CODES[t.dtype], t.device, t.shape
 
@@ -806,7 +815,7 @@ def _decay_inputs(q, k, v, g, h0, cu_seqlens, scale):
             raise ValueError(f"cu_seqlens must be [nseq + 1] int32 on {dev}")
         if B != 1:
             raise ValueError("packed sequences take q [1, total_tokens, Hk, dk]")
-        nseq = cu_seqlens.shape[0] - 1
+        nseq = _int(cu_seqlens.shape[0] - 1, "nseq")
     states = (nseq or B, H, dv, dk)
     if h0 is not None:
         _want(h0, "h0", torch.float32, states, dev)
@@ -896,6 +905,7 @@ def _tree_cache(parent, k, v, k_cache, v_cache, block_table, cache_len):
     _want(v_cache, "v_cache", k.dtype, k_cache.shape, dev)
     width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
     _want(block_table, "block_table", torch.int32, (N, width), dev)
+    _int(width, "block_table's width")
     _want(cache_len, "cache_len", torch.int32, (N,), dev)
     return code, dev, N, M, Hkv, d, pages, page, width
 
@@ -907,9 +917,10 @@ def gdn_tree_attn(parent, q, k, v, k_cache, v_cache, block_table, cache_len, *, 
     [N,M,Hkv,d]; k_cache, v_cache [pages,page,Hkv,d]; block_table [N,width] and
     cache_len [N] int32.  window > 0: only positions less than ``window`` back.
     Returns o [N,M,Hq,d]."""
+    window = max(-1, min(window, _INT))  # no position is further back
     dt, dev, N, M, Hkv, d, pages, page, width = _tree_cache(parent, k, v, k_cache, v_cache, block_table,
                                                             cache_len)
-    Hq = q.shape[2] if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
+    Hq = _int(q.shape[2], "Hq") if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
     _want(q, "q", k.dtype, (N, M, Hq, d), dev)
     with _On(dev, stream) as s:
         o = _like(o, "o", q)
@@ -949,7 +960,7 @@ def _norm_inputs(x, z, w):
     _need(x, "x")
     if x.dim() < 2:
         raise ValueError("x must be [..., H, d]")
-    H, d = x.shape[-2], x.shape[-1]
+    H, d = _int(x.shape[-2], "H"), _int(x.shape[-1], "d")
     _want(z, "z", x.dtype, x.shape, x.device)
     shared = isinstance(w, torch.Tensor) and w.dim() == 1
     _want(w, "w", torch.float32, (d,) if shared else (H, d), x.device)
