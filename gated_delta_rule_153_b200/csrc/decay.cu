@@ -111,6 +111,7 @@ struct WalkSmem {  // rows padded by 16 bytes: eight rows of a column are in dif
     float4 half[2][TT * RB / 4 / WT][WT == 256 && CD < 128 ? WT / 2 : 1];
     float2 g[TT];
     float f[TT], h[TT], own[TT], red[8];
+    FirstBad<RB> bad;  // values of y that are not finite
 };
 
 // RB rows of R per CTA, WT threads.  16 and 32 rows in all have kernels of their own with
@@ -182,6 +183,7 @@ decay_walk_kernel(const Walk p) {
             s.r[e % CD][e / CD] = fmaf(f, s.r[e % CD][e / CD], mine[i]);
         }
     }
+    if (!MAP) s.bad.none(tid);
     float all = 1.f;  // the decay of the run so far
     const bool has_z = !MAP && p.dots != nullptr;
     constexpr bool AHEAD = WT == 256 || (RB < kRows && CD < 128);
@@ -209,6 +211,7 @@ decay_walk_kernel(const Walk p) {
             if (has_z) vz[i] = get(p.z, t, r0 + r, t < m && r0 + r < p.RD);
         }
     };
+    auto place = [&](int it, int t) { return (it - i0) * TT + (REV ? TT - 1 - t : t); };  // as the run is walked
     if (AHEAD && i0 < i1) fetch(i0);
     for (int it = i0; it < i1; ++it) {
         const int tile = REV ? tiles - 1 - it : it;
@@ -230,7 +233,17 @@ decay_walk_kernel(const Walk p) {
         for (int i = 0; i < NY; ++i) {
             const int t = tid / LR + WT / LR * i;
             const float4 v = F::of(vy[i]);
-            *reinterpret_cast<float4*>(&s.y[t][r]) = make_float4(p.c_y * v.x, p.c_y * v.y, p.c_y * v.z, p.c_y * v.w);
+            float4 y = make_float4(p.c_y * v.x, p.c_y * v.y, p.c_y * v.z, p.c_y * v.w);
+            if (!(0.f * y.x + 0.f * y.y + 0.f * y.z + 0.f * y.w == 0.f)) {
+                float* const e[4] = {&y.x, &y.y, &y.z, &y.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (!(fabsf(*e[j]) < INFINITY)) {
+                        *e[j] = MAP ? __uint_as_float(kNaN) : 0.f;
+                        if (!MAP) s.bad.mark(r + j, place(it, t));
+                    }
+            }
+            *reinterpret_cast<float4*>(&s.y[t][r]) = y;
             if (has_z) *reinterpret_cast<float4*>(&s.z[t][r]) = F::of(vz[i]);
         }
         if (warp == 0) {  // the gates' cumsum, in two floats
@@ -249,6 +262,7 @@ decay_walk_kernel(const Walk p) {
         }
         __syncthreads();
         if (AHEAD && it + 1 < i1) fetch(it + 1);
+        const int bad = MAP ? kNever : s.bad.any;
         float sum[NT][4];
         auto add = [&](float (&o)[4], float q, const float4& v) {
             o[0] = fmaf(q, v.x, o[0]);
@@ -370,6 +384,11 @@ decay_walk_kernel(const Walk p) {
                     const float4 v = s.half[1 - part][i][tid % (WT / KS)];
                     sum[i][0] += v.x; sum[i][1] += v.y; sum[i][2] += v.z; sum[i][3] += v.w;
                 }
+                if (bad <= place(it, t)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (s.bad.at[r + j] <= place(it, t)) sum[i][j] = __uint_as_float(kNaN);
+                }
                 const size_t row = (size_t)(t0 + t) * p.H + h;
                 if (has_z) {
                     const float4 zv = *reinterpret_cast<const float4*>(&s.z[t][r]);
@@ -414,6 +433,14 @@ decay_walk_kernel(const Walk p) {
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[c][j] = fmaf(w[c], q[j], a[c][j]);
+            }
+            if (bad < (it - i0 + 1) * TT) {  // y went in without
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (s.bad.at[r + j] != kNever) {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) a[c][j] = __uint_as_float(kNaN);
+                    }
             }
 #pragma unroll
             for (int c = 0; c < NC; ++c) {

@@ -104,6 +104,33 @@ GDN_DEV void split_bf16(uint32_t (&t)[TERMS], float x, float y) {
     }
 }
 
+// Zeros of any sign while every bf16 of the x so far was finite, else NaN in one half or both.
+GDN_DEV uint32_t seen_bf16(uint32_t x, uint32_t so_far) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(so_far) : "r"(x), "r"(0u));
+    return so_far;
+}
+GDN_DEV bool all_finite(uint32_t seen) { return (seen & 0x7fff7fffu) == 0; }
+
+// Where a chain's values first were not finite, per channel and for the earliest of them, in
+// tokens from the chain's start as it is walked.  Such a value belongs to its own token's
+// result and to later ones; in a product over all of a tile's tokens its zero weight
+// would make the earlier ones NaN too, so it goes into the product as zero, and the
+// results from its token on are made NaN (also where +-inf would be exact).
+constexpr int kNever = 0x7fffffff;
+constexpr uint32_t kNaN = 0x7fc00000u;
+template <int N>
+struct FirstBad {
+    int at[N], any;
+    GDN_DEV void none(int tid) {
+        if (tid < N) at[tid] = kNever;
+        if (tid == 0) any = kNever;
+    }
+    GDN_DEV void mark(int channel, int pos) {
+        atomicMin(&at[channel], pos);
+        atomicMin(&any, pos);
+    }
+};
+
 // A bounded wait (1 s) in few instructions: these kernels run five roles' loops side by
 // side, and their footprint in the instruction cache counts.  The caller reports a wait
 // that gave up once, after its loop.

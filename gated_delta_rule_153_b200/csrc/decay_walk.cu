@@ -86,6 +86,7 @@ struct alignas(1024) Smem {
     unsigned char S[MODE == 2 ? 2 : 1][DK * 128];
     Gates gate[NST];
     float col[kEpi][CT];         // per warp of P: the column factors of its decays
+    FirstBad<NB> bad;            // MODE 0: values that are not finite
     // of each stage, so that nobody who waits for one can fall two phases behind
     uint64_t full[NST], v_full[NST], v_free[NST], gfull[NST], gfree[NST], n_done[NST], o_done[NST];
     uint64_t img_ready, img_free, fwd_full, fwd_free, q_full, a_done, p_ready, vt_ready, s_ready[2], x_done, o_free, drain;
@@ -142,6 +143,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     auto chunk_of = [&](int c) { return REV ? chunks - 1 - (c0 + c) : c0 + c; };
     const size_t slot0 = (size_t)(tok0 / CT) + seq;
 
+    if (MODE == 0) s.bad.none(tid);
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&s.full[i], 1);
@@ -181,8 +183,10 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         const float2 ge = s.gate[st].G[CT - 1], gr = s.gate[st].G[r];
         return r < L ? (REV ? p.scale * start_decay(gr) : pair_decay(ge, gr)) : 0.f;
     };
-    auto make = [&](auto& t, int st, int r, int q0, float wt, bool in) {
+    auto make = [&](auto& t, int c, int r, int q0, float wt, bool in) {
         constexpr int NP = sizeof(t) / sizeof(t[0]);
+        const int st = c % NST;
+        uint32_t seen = 0;
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
             const uint32_t at = 2 * swz<64>(r, 8 * (q0 + q));
@@ -195,11 +199,22 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float2 f = unpack_bf16(u[e]);
+                if (MODE == 0) seen = seen_bf16(u[e], seen);
                 mul2(f.x, f.y, f.x, f.y, wt, wt);
                 uint32_t x[TERMS];
                 split_bf16<TERMS>(x, f.x, f.y);
 #pragma unroll
                 for (int k = 0; k < TERMS; ++k) t[q][k][e] = x[k];
+            }
+        }
+        if (MODE == 0 && !all_finite(seen)) {  // Y goes without; the state (t) does not
+#pragma unroll 1
+            for (int e = 0; e < 8 * NP; ++e) {
+                uint16_t* v = reinterpret_cast<uint16_t*>(s.st[st].V + 2 * swz<64>(r, 8 * q0 + e));
+                if ((*v & 0x7f80) == 0x7f80) {
+                    *v = 0;
+                    s.bad.mark(8 * q0 + e, c * CT + r);
+                }
             }
         }
     };
@@ -225,7 +240,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             if (lane == 0) mbar_arrive(&s.gfree[st]);
             if (!warp_wait(&s.v_full[st], (c / NST) & 1)) break;
             uint32_t t[NP][TERMS][4];
-            make(t, st, r, NP * part, wt, r < L);
+            make(t, c, r, NP * part, wt, r < L);
             if (MODE != 0) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.v_free[st]);
@@ -233,7 +248,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             if (c > 0 && !warp_wait(&s.n_done[(c - 1) % NST], ((c - 1) / NST) & 1)) break;
             put(t, r, NP * part);
             if (MODE == 0) {
-                make(t, st, r, NP, wt, r < L);
+                make(t, c, r, NP, wt, r < L);
                 put(t, r, NP);
             }
             if (L < CT && !warp_wait(&s.full[st], (c / NST) & 1)) break;
@@ -255,6 +270,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         const int L = min(CT, n - chunk_of(c) * CT);
         if (!warp_wait(&s.o_done[c % NST], (c / NST) & 1)) return false;
         tc5::fence_after();
+        const int bad = s.bad.any;
         float x[16], y[16];
         tc5::ld16(x, trow + TX + vc);
         tc5::ld16(y, trow + TY + vc);
@@ -264,10 +280,13 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         if (lane == 0) mbar_arrive(&s.o_free);
         uint32_t w[8], mine[4], got[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            fma2(x[2 * e], x[2 * e + 1], ein, ein, x[2 * e], x[2 * e + 1], y[2 * e], y[2 * e + 1]);
-            w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+        for (int e = 0; e < 8; ++e) fma2(x[2 * e], x[2 * e + 1], ein, ein, x[2 * e], x[2 * e + 1], y[2 * e], y[2 * e + 1]);
+        if (bad <= c * CT + r) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = s.bad.at[vc + e] <= c * CT + r ? __uint_as_float(kNaN) : x[e];
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
         // lanes 2m, 2m+1 trade 16-byte pieces, so that each store instruction
         // writes whole 32-byte sectors: first row 2m, then row 2m + 1
         const bool odd = lane & 1;
@@ -422,7 +441,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.gfree[st]);
                 if (!(ok = warp_wait(&s.v_full[st], (c / NST) & 1))) break;
-                make(t, st, r, 6 + half, wt, r < L);
+                make(t, c, r, 6 + half, wt, r < L);
                 if (MODE != 0) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.v_free[st]);

@@ -349,6 +349,12 @@ gdn_status gdn_recurrent_step(int N, int H, int dk, int dv, gdn_dtype dtype,
  * nearly all of fp32.  There o, dq, dk, dv take the states and the decayed
  * pair products in bf16, one rounding each (2^-8); all are rounded to `dtype` at
  * the end.
+ * A value of q, k or v that is not finite makes NaN (also where +-inf would be exact)
+ * of what depends on it: its own token and later ones of the sequence, for v in its
+ * own channel.  Earlier tokens, other sequences and other key heads, for v other
+ * value heads, are as they would be without it.  The backward keeps other
+ * sequences apart in the same way; the gradients of the sequence itself are then
+ * unspecified.
  * The backward is that of <dO, o> + <dhT, hT> (dhT NULL = 0) and recomputes the
  * states; dh0 is required exactly when h0 is given.
  * dk, dv in {16, 32, 64, 128} (else GDN_ERR_UNSUPPORTED); all pointers 16-byte
