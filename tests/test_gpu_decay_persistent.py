@@ -1,7 +1,7 @@
-"""gdn_decay_bwd on tensor cores with more chunks than CTAs, so that every CTA goes through
-several: against the definition as masked products of whole sequences in fp64 (the token
-loop of the oracle would hold a state per token), gradients by automatic differentiation.
-The bounds are those of test_gpu_decay.py."""
+"""gdn_decay_* on tensor cores with more chunks than CTAs, so that every CTA of the backward
+goes through several, and batches cut into runs: against the definition as masked products
+of whole sequences in fp64 (the token loop of the oracle would hold a state per token),
+gradients by automatic differentiation.  The bounds are those of test_gpu_decay.py."""
 import math
 
 import pytest
@@ -94,3 +94,54 @@ def test_results_leave_whole_under_memory_traffic(dev, dk, dv):
     for r in got:
         for n in want:
             assert torch.equal(r[n], want[n]), n
+
+
+DIMS = [(64, 64), (64, 128), (128, 64), (128, 128)]
+
+
+def both(x, dev, cu=None):
+    got = base.run(x, dev, cu, scale=0.5)
+    again = base.run(x, dev, cu, scale=0.5)
+    for n in got:
+        assert torch.equal(got[n], again[n]), n
+    check(got, x, 0.5, cu)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [640, 645])
+@pytest.mark.parametrize("Hk", [20, 5])
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_several_chunks_per_cta(dev, dk, dv, Hk, T):
+    """360 chunk-heads, whole chunks alone or with a chunk of 5 tokens at each sequence's end."""
+    both(base.make(3, T, 20, Hk, dk, dv, "bf16", seed=74), dev)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hk", [24, 6])
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_several_chunks_per_cta_packed(dev, dk, dv, Hk):
+    """Sequences of all lengths: whole and short chunks in any order on a CTA, empty slots
+    between them, tokens of no sequence around them."""
+    cu = [7, 7, 8, 136, 400, 401, 657, 657, 700, 1213, 1500]
+    x = base.make(1, 1510, 24, Hk, dk, dv, "bf16", seed=75, nstates=len(cu) - 1)
+    d = {n: t.to(dev) for n, t in x.items()}
+    c = torch.tensor(cu, dtype=torch.int32, device=dev)
+    a = [d[n] for n in ("q", "k", "v", "g")]
+    runs = []
+    for _ in range(2):
+        out = {n: torch.zeros_like(d[n[1:]]) for n in ("dq", "dk", "dv", "dg")}
+        o, hT = gdn.gdn_decay_fwd(*a, d["h0"], cu_seqlens=c, scale=0.5, o=torch.zeros_like(d["v"]))
+        r = gdn.gdn_decay_bwd(*a, d["dO"], d["h0"], d["dhT"], cu_seqlens=c, scale=0.5, out=out)
+        runs.append(dict(o=o, hT=hT, **r))
+    torch.cuda.synchronize()
+    for n in runs[0]:
+        assert torch.equal(runs[0][n], runs[1][n]), n
+    check(runs[0], x, 0.5, cu)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 64), ("bf16", 128, 128), ("f32", 64, 64), ("f32", 16, 32)])
+def test_batches_in_runs(dev, dtype, dk, dv):
+    """More than one sequence and few heads: every sequence of the batch is cut into runs."""
+    both(base.make(2, 3001, 1, 1, dk, dv, dtype, seed=76, shift=-5.0), dev)
+    both(base.make(3, 1100, 2, 1, dk, dv, dtype, seed=77, shift=-4.0), dev)
