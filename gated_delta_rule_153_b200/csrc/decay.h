@@ -118,8 +118,8 @@ void launch_group_sum(const Problem& p, const float* part_q, const float* part_k
 bool tc_supported(const Problem& p);
 size_t tc_fwd_workspace(const Problem& p);
 // The backward (decay_bwd.cu).  launch_tc_states: the state entering each chunk of
-// 128 tokens and the gradient of the one leaving it, [slot][head][2 terms][dv/64][dk][64]
-// bf16 images, and cross [dv/64][slot][head] = e^{G_last} <S, dS>.
+// 128 tokens and the gradient of the one leaving it, in fp32 as images of their upper and
+// lower halves, [slot][head][2][dv/64][dk][64], and cross [dv/64][slot][head] = e^{G_last} <S, dS>.
 size_t tc_states_workspace(const Problem& p);
 bool launch_tc_states(const Problem& p, const void* q, const void* k, const void* v, const float* g, const float* h0,
                       const void* dO, const float* dhT, float* dh0, void* S, void* dS, float* cross, void* runs, void* ws,

@@ -12,9 +12,9 @@
 // part of dk_j),
 //     dg_t = sum_{i >= t} (r_i - c_i) + sum_{i >= t} a_i + sum_{j < t} b_j + e^{G_last} <S, dS>:
 // every pair of tokens before t and from t on, within the chunk, across its start,
-// across its end, and over it.  dg is fp32, so M is taken from fp32 accumulators,
-// and S and dS enter the products behind a and b as two bf16 terms (2^-16); D .* dO V^T,
-// D .* Q K^T and, for dv, dS are rounded to bf16 once, as dq, dk and dv themselves are.
+// across its end, and over it.  dg is fp32, so M is taken from fp32 accumulators, and S
+// and dS enter the products behind a and b as three bf16 terms, exact to fp32 (dv takes two
+// of dS); D .* dO V^T and D .* Q K^T are rounded to bf16 once, as dq, dk and dv themselves are.
 //
 // One CTA per SM takes the chunk-heads in turn.  A chunk runs in two halves, the
 // first with the query token on the tensor-memory lanes, the second with the key
@@ -22,8 +22,8 @@
 //     Q K^T, dO V^T, dO S  -> dq, r, a        K Q^T, V dO^T, V dS, K dS^T  -> dk, dv, c, b
 // The state parts are scaled in place and the other products accumulate onto them.
 // Sixteen warps do the elementwise work (four per 32 tokens, a quarter of the columns
-// each); one issues loads and products; one forms the gates and sums dg.  Loads of the
-// next chunk start as each operand is done with.
+// each) and split the states; one issues loads and products; one forms the gates and sums
+// dg.  Loads of the next chunk start as each operand is done with.
 //
 // What bounds it, at 8 x 2048 tokens of 8 heads, dk = dv = 128 (1,024 chunk-heads, seven
 // per SM): 105 us, 15 us a chunk, 3.3 TB/s of DRAM traffic (356 MB, S and dS are 134 of
@@ -43,9 +43,11 @@ constexpr int kThreads = 32 * (kEpi + 2);
 template <int DK, int DV>
 struct alignas(1024) Smem {
     unsigned char Q[DK / 64][PANEL], K[DK / 64][PANEL], V[DV / 64][PANEL], Y[DV / 64][PANEL];  // Y = dO
-    unsigned char S[2][DV / 64][DK * 128];  // the two terms of S, then of dS
+    // S, then dS: the upper halves, which are the first bf16 term, and the lower halves.  Once
+    // the first term is done with, the third and the second come in their places.
+    unsigned char S[2][DV / 64][DK * 128];
     // Results on their way out: dq, then dk and dv, each once the store before it has read
-    // its source.  At the largest dims they go by way of S: dq through its second term,
+    // its source.  At the largest dims they go by way of S: dq through the second place,
     // between its last use and the arrival of dS's, dk and dv through both, between dS and
     // the next chunk's S, which only the second products of that chunk need.
     static constexpr bool kOwnOut = DK + DV < 256;
@@ -56,15 +58,14 @@ struct alignas(1024) Smem {
     Gates gate[2];
     float r[2][4][CT], c[2][4][CT], a[2][4][CT], b[2][4][CT];  // [chunk parity][column quarter][token]
     float col[kEpi][2][16];
-    uint64_t t_full, kv_full, s_full[2], gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, e3r, e3[2], o_done, e4, gfree[2],
-        drain;
+    uint64_t t_full, kv_full, s_full[2], s_read, s_ready, gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, v_done, e3r, e3[2], o_done, e4, drain;
     uint32_t tmem;
 };
 
 struct Params {
     CUtensorMap qmap, kmap, vmap, ymap, dqmap, dkmap, dvmap;
     Seqs seq;
-    int H, Hk, rep;
+    int H, rep;
     float scale;
     const float* g;
     const unsigned char *S, *dS;
@@ -131,13 +132,9 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long slots = chunk_slots(p.seq, CT), units = slots * p.H;
     if (tid == 0) {
-        for (uint64_t* b : {&s.t_full, &s.kv_full, &s.s_full[0], &s.s_full[1], &s.a_done, &s.x_done, &s.q_done, &s.a2_done, &s.x2_done, &s.o_done, &s.drain})
+        for (uint64_t* b : {&s.t_full, &s.kv_full, &s.s_full[0], &s.s_full[1], &s.a_done, &s.x_done, &s.q_done, &s.a2_done, &s.x2_done, &s.v_done, &s.o_done, &s.s_read, &s.gfull[0], &s.gfull[1], &s.drain})
             mbar_init(b, 1);
-        for (uint64_t* b : {&s.zeroed, &s.e1, &s.e2, &s.e3r, &s.e3[0], &s.e3[1], &s.e4}) mbar_init(b, kEpi);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.gfull[i], 1);
-            mbar_init(&s.gfree[i], 1);
-        }
+        for (uint64_t* b : {&s.zeroed, &s.e1, &s.e2, &s.e3r, &s.e3[0], &s.e3[1], &s.e4, &s.s_ready}) mbar_init(b, kEpi);
         fence_mbar_init();
     }
     if (warp == kEpi) tc5::alloc(&s.tmem, 512);
@@ -153,6 +150,27 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
     if (warp < kEpi) {
         const int blk = warp & 3, qt = warp >> 2, i = 32 * blk + lane;
         const uint32_t trow = tm + ((uint32_t)(32 * blk) << 16);
+        // The second and third terms of a state (0: S, 1: dS), each where this thread reads
+        auto split_state = [&](int which) {
+            if (!warp_wait(&s.s_full[0], which) || !warp_wait(&s.s_full[1], which)) return false;
+            if (!warp_wait(&s.s_read, which)) return false;  // the products are done with the first
+#pragma unroll
+            for (int q = 0; q < DK * DV / (8 * 32 * kEpi); ++q) {
+                uint4 *up = reinterpret_cast<uint4*>(s.S[0]) + tid + 32 * kEpi * q, *low = reinterpret_cast<uint4*>(s.S[1]) + tid + 32 * kEpi * q;
+                const uint4 a = *up, b = *low;
+                uint4 t2, t3;
+                split_rest(t2.x, t3.x, a.x, b.x);
+                split_rest(t2.y, t3.y, a.y, b.y);
+                split_rest(t2.z, t3.z, a.z, b.z);
+                split_rest(t2.w, t3.w, a.w, b.w);
+                *low = t2;
+                *up = t3;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.s_ready);
+            return true;
+        };
         for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
             const int h = (int)(u % p.H);
             if (!chunk_of_slot(p.seq, u / p.H, ch)) continue;
@@ -226,7 +244,9 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                         for (int e = 0; e < 8; ++e) pk[e] = 0;
                     }
                     tc5::st8(trow + TP + 8 * J, pk);
+                    if (z == 0 && !(ok = split_state(0))) break;
                 }
+                if (!ok) break;
                 s.r[ph][qt][i] = rs;
             }
             {   // the state part of dq, scaled in place; a_i = q_i . it
@@ -360,6 +380,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                     tc5::st8(trow + TB + 8 * (qt + 4 * z), pb[z]);
                 }
             }
+            if (!(ok = split_state(1))) break;
             {   // the state parts of dk and dv, scaled in place; b_j = k_j . dk's
                 const float f = i < L ? pair_decay(G.G[CT - 1], gi) : 0.f;
                 if (!(ok = warp_wait(&s.x2_done, ph))) break;
@@ -387,6 +408,8 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                     tc5::st16(trow + TX + c0, w);
                 }
                 s.b[ph][qt][i] = bs;
+                if (!(ok = warp_wait(&s.v_done, ph))) break;
+                tc5::fence_after();
 #pragma unroll 1
                 for (int z = 0; z < QV / 16; ++z) {
                     const uint32_t at = trow + TV + qt * QV + 16 * z;
@@ -511,14 +534,22 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             }
             __syncwarp();
             // (dO S goes where dk of the chunk before was: its e4 came before these loads)
-            if (!(ok = warp_wait(&s.s_full[0], 0)) || !(ok = warp_wait(&s.s_full[1], 0))) break;
+            if (!(ok = warp_wait(&s.s_full[0], 0))) break;
+            tc5::fence_after();
+            if (elect_one()) {
+#pragma unroll 2
+                for (int k = 0; k < DV / 16; ++k) tc5::mma(tm + TX, dY + cols(k, KPANEL), dS + cols(k, SPANEL), ID_K, k > 0);
+                tc5::commit(&s.s_read);
+            }
+            __syncwarp();
+            if (!(ok = warp_wait(&s.s_ready, 0))) break;
             tc5::fence_after();
             if (elect_one()) {
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t)
 #pragma unroll 2
                     for (int k = 0; k < DV / 16; ++k)
-                        tc5::mma(tm + TX, dY + cols(k, KPANEL), dS + t * STERM + cols(k, SPANEL), ID_K, t + k > 0);
+                        tc5::mma(tm + TX, dY + cols(k, KPANEL), dS + t * STERM + cols(k, SPANEL), ID_K, true);
                 tc5::commit(&s.x_done);
             }
             __syncwarp();
@@ -567,17 +598,24 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                 for (int k = 0; k < DV / 16; ++k) tc5::mma(tm + TX, dV + cols(k, KPANEL), dS + cols(k, SPANEL), ID_K, k > 0);
 #pragma unroll 2
                 for (int k = 0; k < DK / 16; ++k) tc5::mma(tm + TV, dK + cols(k, KPANEL), tS + k * KROWS, ID_VT, k > 0);
+                tc5::commit(&s.s_read);
             }
             __syncwarp();
-            if (!(ok = warp_wait(&s.s_full[1], 1))) break;
+            if (!(ok = warp_wait(&s.s_ready, 1))) break;
             tc5::fence_after();
             if (elect_one()) {
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t)
 #pragma unroll 2
-                for (int k = 0; k < DV / 16; ++k) tc5::mma(tm + TX, dV + cols(k, KPANEL), dS + STERM + cols(k, SPANEL), ID_K, true);
+                    for (int k = 0; k < DV / 16; ++k)
+                        tc5::mma(tm + TX, dV + cols(k, KPANEL), dS + t * STERM + cols(k, SPANEL), ID_K, true);
                 tc5::commit(&s.x2_done);
+#pragma unroll 2
+                for (int k = 0; k < DK / 16; ++k) tc5::mma(tm + TV, dK + cols(k, KPANEL), tS + STERM + k * KROWS, ID_VT, true);
+                tc5::commit(&s.v_done);
             }
             __syncwarp();
-            if (!(ok = warp_wait(&s.x2_done, ph))) break;
+            if (!(ok = warp_wait(&s.v_done, ph))) break;
             if (s.kOwnOut && un < units) {
                 load_s(un, p.S, 0);
                 load_s(un, p.S, 1);
@@ -753,7 +791,7 @@ bool launch_tc_bwd(const Problem& p, const void* q, const void* k, const void* v
     if (!encode_head_map(&a.dvmap, dv, p.seq.rows, p.H, p.dv, CT)) return false;
     if (!parts && (!encode_head_map(&a.dqmap, dq, p.seq.rows, p.H, p.dk, CT) || !encode_head_map(&a.dkmap, dk, p.seq.rows, p.H, p.dk, CT)))
         return false;
-    a.seq = p.seq; a.H = p.H; a.Hk = p.Hk; a.rep = p.H / p.Hk; a.scale = p.scale; a.g = g;
+    a.seq = p.seq; a.H = p.H; a.rep = p.H / p.Hk; a.scale = p.scale; a.g = g;
     a.S = (unsigned char*)base + l.S; a.dS = (unsigned char*)base + l.dS; a.cross = (float*)(base + l.cross);
     a.dq = parts ? (void*)(base + l.dq) : dq;
     a.dk = parts ? (void*)(base + l.dk) : dk;

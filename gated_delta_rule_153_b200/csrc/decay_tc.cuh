@@ -104,6 +104,26 @@ GDN_DEV void split_bf16(uint32_t (&t)[TERMS], float x, float y) {
     }
 }
 
+// The upper halves of two fp32 values, packed, and their lower halves; and back.
+GDN_DEV uint2 halves(float x, float y) {
+    return make_uint2(__byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632),
+                      __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x5410));
+}
+GDN_DEV float2 join_halves(uint32_t up, uint32_t low) {
+    return make_float2(__uint_as_float(__byte_perm(low, up, 0x5410)), __uint_as_float(__byte_perm(low, up, 0x7632)));
+}
+// What the upper halves, read as bf16 values, leave of the values: 16 bits, as two bf16
+// terms, exactly.
+GDN_DEV void split_rest(uint32_t& t2, uint32_t& t3, uint32_t up, uint32_t low) {
+    float2 x = join_halves(up, low);
+    const float2 t1 = unpack_bf16(up);
+    add2f(x.x, x.y, x.x, x.y, -t1.x, -t1.y);
+    t2 = pack_bf16(x.x, x.y);
+    const float2 f = unpack_bf16(t2);
+    add2f(x.x, x.y, x.x, x.y, -f.x, -f.y);
+    t3 = pack_bf16(x.x, x.y);
+}
+
 // Zeros of any sign while every bf16 of the x so far was finite, else NaN in one half or both.
 GDN_DEV uint32_t seen_bf16(uint32_t x, uint32_t so_far) {
     asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(so_far) : "r"(x), "r"(0u));

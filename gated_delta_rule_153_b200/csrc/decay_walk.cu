@@ -31,8 +31,8 @@
 // one place.
 //
 // MODE 2 walks K and V (backwards: Q and dO, with the gradient of the state) and
-// writes the state entering each chunk, as two bf16 terms, for the backward's
-// local products (decay_bwd.cu); warps 0-7 split V.
+// writes the state entering each chunk, in fp32, for the backward's local products
+// (decay_bwd.cu); warps 0-7 split V.
 // MODE 1 walks K and V alone and writes the state a run of chunks adds to a zero
 // state, with the run's decay.  With few chains, each is cut into runs: MODE 1 over
 // all runs but the last, then MODE 0 or 2 over all runs at once, each starting from the
@@ -69,10 +69,7 @@ constexpr bool kShare = MODE != 2;
 template <int MODE>
 constexpr int kThreads = 32 * (kEpi + kState + 3 + (MODE == 0 ? 4 : MODE == 2 ? 1 : 0));
 constexpr int NST = 2;
-// bf16 terms of the decayed V: three are exact to fp32; the states that go out in two
-// terms themselves (2^-16) and nowhere else are made of two.
-template <int MODE, bool REV>
-constexpr int kTerms = MODE == 2 && !REV ? 2 : 3;
+constexpr int TERMS = 3;  // bf16 terms of the decayed V: exact to fp32
 
 template <int DK, int MODE>
 struct alignas(1024) Smem {
@@ -82,7 +79,7 @@ struct alignas(1024) Smem {
     } st[NST];
     unsigned char Vt[3][PANEL];  // decayed V, three bf16 terms
     // MODE 0: the entering state in bf16, [key channel][64 value channels]; MODE 2 backwards:
-    // the two terms of the forward state at the chunk's start
+    // the image of the forward state at the chunk's start
     unsigned char S[MODE == 2 ? 2 : 1][DK * 128];
     Gates gate[NST];
     float col[kEpi][CT];         // per warp of P: the column factors of its decays
@@ -103,7 +100,8 @@ struct Params {
     float* hT;
     int runs, len;        // runs per chain, chunks per run
     float *runS, *runG;   // [item][head][value block][DK][64] and [item][head] of MODE 1
-    // MODE 2: [slot][head][2 terms][value block][DK][64] bf16, the state entering each chunk
+    // MODE 2: the fp32 state entering each chunk, as its upper and its lower halves (the upper
+    // ones are bf16 values): [slot][head][2][value block][DK][64] of 16 bits
     __nv_bfloat16* image;
     const __nv_bfloat16* other;  // backwards: the forward states, dotted into cross
     float* cross;                // [value block][slot][head]
@@ -119,7 +117,6 @@ GDN_DEV uint32_t tn(int c) { return MODE == 0 ? TN : 3 * NB * (c & 1); }
 template <int DK, int MODE, bool REV>
 __global__ void __launch_bounds__(kThreads<MODE>, 1)
 decay_tc_walk_kernel(const __grid_constant__ Params p) {
-    constexpr int TERMS = kTerms<MODE, REV>;
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem<DK, MODE>& s = *reinterpret_cast<Smem<DK, MODE>*>(align1k(raw));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -495,10 +492,8 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                             const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                float2 hi = unpack_bf16(x[e]);
-                                const float2 lo = unpack_bf16(y[e]);
-                                add2f(hi.x, hi.y, hi.x, hi.y, lo.x, lo.y);
-                                fma2(d2.x, d2.y, S[8 * q + 2 * e], S[8 * q + 2 * e + 1], hi.x, hi.y, d2.x, d2.y);
+                                const float2 f = join_halves(x[e], y[e]);
+                                fma2(d2.x, d2.y, S[8 * q + 2 * e], S[8 * q + 2 * e + 1], f.x, f.y, d2.x, d2.y);
                             }
                         }
                     }
@@ -512,12 +507,12 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
                 if (own) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t t[4][2];
+                        uint2 t[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) split_bf16<2>(t[e], S[8 * q + 2 * e], S[8 * q + 2 * e + 1]);
+                        for (int e = 0; e < 4; ++e) t[e] = halves(S[8 * q + 2 * e], S[8 * q + 2 * e + 1]);
                         unsigned char* at = (unsigned char*)s.Q + 2 * swz<64>(r, 32 * half + 8 * q);
-                        *reinterpret_cast<uint4*>(at) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
-                        *reinterpret_cast<uint4*>(at + DK * 128) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(t[0].x, t[1].x, t[2].x, t[3].x);
+                        *reinterpret_cast<uint4*>(at + DK * 128) = make_uint4(t[0].y, t[1].y, t[2].y, t[3].y);
                     }
                 }
                 fence_async_smem();

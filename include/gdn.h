@@ -343,12 +343,11 @@ gdn_status gdn_recurrent_step(int N, int H, int dk, int dv, gdn_dtype dtype,
  * Values: g <= 0 (documented, not checked); g = -inf is a reset.  The decay of a
  * pair of tokens is the exponential of a difference in a cumsum of two floats per
  * token (error below 2^-40 of it).  The state that hT and dh0 come from is summed
- * in fp32 from products exact to fp32, with bf16 inputs too.  dg is summed in fp32;
- * with bf16 inputs and dk, dv in {64, 128} (tensor cores) the states enter it in two
- * bf16 terms each, 2^-16 of their entries, and without h0 and dhT it keeps
- * nearly all of fp32.  There o, dq, dk, dv take the states and the decayed
- * pair products in bf16, one rounding each (2^-8); all are rounded to `dtype` at
- * the end.
+ * in fp32 from products exact to fp32, with bf16 inputs too.  dg is summed in fp32,
+ * and the states enter it, dq and dk in products exact to fp32.  With bf16 inputs and
+ * dk, dv in {64, 128} (tensor cores) o, dq, dk, dv take the decayed pair products in
+ * bf16, o the states too, one rounding each (2^-8), and dv the states to 2^-16; all are
+ * rounded to `dtype` at the end.
  * A value of q, k or v that is not finite makes NaN (also where +-inf would be exact)
  * of what depends on it: its own token and later ones of the sequence, for v in its
  * own channel.  Earlier tokens, other sequences and other key heads, for v other
