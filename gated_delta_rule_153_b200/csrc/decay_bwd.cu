@@ -58,7 +58,8 @@ struct alignas(1024) Smem {
     Gates gate[2];
     float r[2][4][CT], c[2][4][CT], a[2][4][CT], b[2][4][CT];  // [chunk parity][column quarter][token]
     float col[kEpi][2][16];
-    uint64_t t_full, kv_full, s_full[2], s_read, s_ready, gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, v_done, e3r, e3[2], o_done, e4, drain;
+    uint64_t t_full, kv_full, s_full[2], s_read, s_ready, gfull[2], zeroed, a_done, x_done, e1, q_done, e2, a2_done, x2_done, v_done, e3r,
+        e3[2], o_done, e4, drain;
     uint32_t tmem;
 };
 
@@ -132,7 +133,8 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long slots = chunk_slots(p.seq, CT), units = slots * p.H;
     if (tid == 0) {
-        for (uint64_t* b : {&s.t_full, &s.kv_full, &s.s_full[0], &s.s_full[1], &s.a_done, &s.x_done, &s.q_done, &s.a2_done, &s.x2_done, &s.v_done, &s.o_done, &s.s_read, &s.gfull[0], &s.gfull[1], &s.drain})
+        for (uint64_t* b : {&s.t_full, &s.kv_full, &s.s_full[0], &s.s_full[1], &s.s_read, &s.gfull[0], &s.gfull[1], &s.a_done, &s.x_done,
+                            &s.q_done, &s.a2_done, &s.x2_done, &s.v_done, &s.o_done, &s.drain})
             mbar_init(b, 1);
         for (uint64_t* b : {&s.zeroed, &s.e1, &s.e2, &s.e3r, &s.e3[0], &s.e3[1], &s.e4, &s.s_ready}) mbar_init(b, kEpi);
         fence_mbar_init();
@@ -244,7 +246,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                         for (int e = 0; e < 8; ++e) pk[e] = 0;
                     }
                     tc5::st8(trow + TP + 8 * J, pk);
-                    if (z == 0 && !(ok = split_state(0))) break;
+                    if (z == 0 && !(ok = split_state(0))) break;  // its products run under the rest
                 }
                 if (!ok) break;
                 s.r[ph][qt][i] = rs;
@@ -542,7 +544,7 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                 tc5::commit(&s.s_read);
             }
             __syncwarp();
-            if (!(ok = warp_wait(&s.s_ready, 0))) break;
+            if (!(ok = warp_wait(&s.s_ready, 0))) break;  // the other terms, in the places of the halves
             tc5::fence_after();
             if (elect_one()) {
 #pragma unroll 1

@@ -145,7 +145,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.v_free[i], kSplit<MODE> + (kShare<MODE> ? kState : 0));
+            mbar_init(&s.v_free[i], kSplit<MODE> + (kShare<MODE> ? kState : 0));  // (MODE 0 has o_done for it)
             mbar_init(&s.n_done[i], 1);
             mbar_init(&s.o_done[i], 1);
             mbar_init(&s.gfull[i], 1);

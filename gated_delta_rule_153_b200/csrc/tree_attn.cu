@@ -212,10 +212,7 @@ GDN_DEV void put16(__nv_bfloat16* to, const float (&u)[16]) {
     *reinterpret_cast<uint4*>(to + 8) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-GDN_DEV unsigned char* align1k(unsigned char* p) {
-    return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
-}
-
+using decay::align1k;
 using decay::elect_one;
 using decay::ex2;
 using decay::wait_for;
