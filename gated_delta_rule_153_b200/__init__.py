@@ -20,6 +20,11 @@ try:  # needed by every call, though not to build the library
     import torch
 except ImportError:
     torch = None
+else:
+    # the current device and a device's current stream handle, by the short way where torch has it
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
+                             lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -710,9 +715,9 @@ class _On:
                 raise ValueError(f"stream of {stream.device} for tensors on {device}")
             self.ctx, self.handle = torch.cuda.stream(stream), stream.cuda_stream  # sets its device too
         else:
-            if device.index != torch._C._cuda_getDevice():
+            if device.index != _current_device():
                 self.ctx = torch.cuda.device(device)
-            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            self.handle = _stream_handle(device.index)
 
     def __enter__(self):
         if self.ctx is not None:
