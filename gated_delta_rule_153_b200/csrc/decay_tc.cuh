@@ -115,13 +115,11 @@ GDN_DEV float2 join_halves(uint32_t up, uint32_t low) {
 // What the upper halves, read as bf16 values, leave of the values: 16 bits, as two bf16
 // terms, exactly.
 GDN_DEV void split_rest(uint32_t& t2, uint32_t& t3, uint32_t up, uint32_t low) {
-    float2 x = join_halves(up, low);
-    const float2 t1 = unpack_bf16(up);
-    add2f(x.x, x.y, x.x, x.y, -t1.x, -t1.y);
-    t2 = pack_bf16(x.x, x.y);
+    const float2 x = join_halves(up, low), t1 = unpack_bf16(up);
+    const float a = x.x - t1.x, b = x.y - t1.y;
+    t2 = pack_bf16(a, b);
     const float2 f = unpack_bf16(t2);
-    add2f(x.x, x.y, x.x, x.y, -f.x, -f.y);
-    t3 = pack_bf16(x.x, x.y);
+    t3 = pack_bf16(a - f.x, b - f.y);
 }
 
 // Zeros of any sign while every bf16 of the x so far was finite, else NaN in one half or both.
