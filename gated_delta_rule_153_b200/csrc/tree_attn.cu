@@ -83,6 +83,10 @@ struct alignas(1024) Smem {
     unsigned char K[NST][D / 64][PANEL], V[NST][D / 64][PANEL];
     float2 ml[128];                  // a segment's end: one group's maxima and sums, then both factors
     int parent[kMaxNodes];
+    // By parity of the segment, values that are not finite where rows differ in what they see:
+    // the nodes that hold one, and the last such cached position (-1: none)
+    unsigned long long bad_nodes[2];
+    int bad_pos[2];
     // 16-row pieces of a step's tile that hold cached rows; twice the stages, as the
     // loader may be that far ahead of the softmax warps
     uint32_t have[2 * NST];
@@ -213,8 +217,10 @@ GDN_DEV void put16(__nv_bfloat16* to, const float (&u)[16]) {
 }
 
 using decay::align1k;
+using decay::all_finite;
 using decay::elect_one;
 using decay::ex2;
+using decay::seen_bf16;
 using decay::wait_for;
 using decay::warp_wait;
 
@@ -317,6 +323,11 @@ tree_attn_kernel(const __grid_constant__ Params p) {
                 if (lane == 0) mbar_arrive(&s.q_full);
             }
             if (tid < p.M) s.parent[tid] = parent_of(p.parent + (size_t)g.n * p.M, tid, p.status);
+            const int par = segs & 1;
+            if (tid == 0) {
+                s.bad_nodes[par] = 0;
+                s.bad_pos[par] = -1;
+            }
             if (!meet()) break;
             // what this row sees: cached positions from `lo`, nodes in `anc`
             unsigned long long anc = 0;
@@ -376,6 +387,20 @@ tree_attn_kernel(const __grid_constant__ Params p) {
 #pragma unroll 1
                         for (int j = 0; j < D / 8; ++j)
                             *reinterpret_cast<uint4*>(s.V[st][j >> 3] + 2 * swz<64>(r, 8 * (j & 7))) = make_uint4(0, 0, 0, 0);
+                    } else if (p.M > 1 && (tree || p.window > 0)) {
+                        // a value that some rows see and others do not: one that is not finite
+                        // goes in as zero, and the rows that see it are made NaN at the end
+                        bool fine = true;
+#pragma unroll 1
+                        for (int j = 0; j < D / 8; ++j) {
+                            uint4* at = reinterpret_cast<uint4*>(s.V[st][j >> 3] + 2 * swz<64>(r, 8 * (j & 7)));
+                            const uint4 v = *at;
+                            if (all_finite(seen_bf16(v.x, seen_bf16(v.y, seen_bf16(v.z, seen_bf16(v.w, 0u)))))) continue;
+                            *at = make_uint4(0, 0, 0, 0);
+                            fine = false;
+                        }
+                        if (!fine && tree) atomicOr(&s.bad_nodes[par], 1ull << r);
+                        if (!fine && !tree) atomicMax(&s.bad_pos[par], key0 + r);
                     }
                     fence_async_smem();
                 }
@@ -465,6 +490,7 @@ tree_attn_kernel(const __grid_constant__ Params p) {
                 f0 = l0 != 0.f ? ex2(m - mx) : 0.f;  // (a NaN goes on)
                 f1 = o.y != 0.f ? ex2(o.x - mx) : 0.f;
                 lt = l0 * f0 + o.y * f1;
+                if ((s.bad_nodes[par] & anc) || s.bad_pos[par] >= lo) f0 = f1 = lt = __uint_as_float(decay::kNaN);
                 if (whole) {
                     f0 *= 1.f / lt;
                     f1 *= 1.f / lt;

@@ -399,11 +399,10 @@ gdn_status gdn_decay_step(int N, int H, int Hk, int dk, int dv, gdn_dtype dtype,
  * head h / (Hq / Hkv):
  *     o_i = sum_p softmax_p(scale q_i . k_p) v_p,
  * the softmax statistics and sums in fp32, the weights rounded to bf16 for their
- * product with v.  What nobody sees (cache rows past cache_len, other branches'
- * nodes) has no effect, whatever its keys and scores are; but the weights' zeros
- * do multiply v, so the v of a node or cached position that some node of the
- * sequence sees must be finite for the sequence's other nodes to be.  A score of NaN, or
- * of +inf, makes the rows that see it NaN.
+ * product with v.  What a node does not see (cache rows past cache_len or before its
+ * window, other branches' nodes) has no effect on it, whatever it holds.  A score of NaN
+ * or of +inf, and a v that is not finite, make the rows that see it NaN (v at least in
+ * its own channel).
  * gdn_tree_append copies the k and v rows of the root path of accepted[n] (-1:
  * nothing) to the cache positions cache_len[n] .. and writes the new length to
  * new_len[n] (new_len may be cache_len).
