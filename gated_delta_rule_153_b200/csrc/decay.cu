@@ -1,5 +1,5 @@
 // decay.cu -- linear attention with a decay per head in fp32 arithmetic on
-// CUDA cores, one token at a time: the path of GDN_F32 and of the head dims the
+// CUDA cores, by tiles of 32 tokens: the path of GDN_F32 and of the head dims the
 // tensor-core kernels do not take; and the single-token step.
 //
 // The recurrence per (sequence, head), with a_t = e^{g_t}:
@@ -32,7 +32,7 @@
 // 64 rows of R.  What bounds it is the issue of fp32 FMAs and, 1.5 to 2 times as long, the
 // shared-memory loads that feed them (a 16-byte load takes four cycles of the SM's 128
 // bytes per cycle, whatever its lanes share): about 6,700 of them per tile of 64 x 64 dims.
-// Forward, 32 x 1024 tokens of 8 heads: 281 us at 64 x 64 dims, 1,010 us at 128 x 128.
+// Forward, 32 x 1024 tokens of 8 heads: 285 us at 64 x 64 dims, 1,017 us at 128 x 128.
 #include <math.h>
 
 #include <algorithm>

@@ -26,10 +26,13 @@
 // dg.  Loads of the next chunk start as each operand is done with.
 //
 // What bounds it, at 8 x 2048 tokens of 8 heads, dk = dv = 128 (1,024 chunk-heads, seven
-// per SM): 105 us, 15 us a chunk, 3.3 TB/s of DRAM traffic (356 MB, S and dS are 134 of
-// them) with the tensor pipe busy for a quarter.  The four rounds of products and elementwise
+// per SM): 127 us, 18 us a chunk, 2.8 TB/s of DRAM traffic (361 MB, S and dS are 134 of
+// them) with the tensor pipe busy for 28 %.  The four rounds of products and elementwise
 // work of a chunk wait for one another, and shared memory (230 KB) and tensor memory
-// (all 512 columns) hold one chunk.  Results leave by TMA from shared memory.
+// (all 512 columns) hold one chunk.  With S and dS in two bf16 terms from memory it took 106
+// us, dg off by 3e-6: of the 21 us the split is 9, its products 4, the two hand-offs 8.
+// Splitting fp32 states from memory took 144 us, three terms from memory 134 us here and
+// 40 us more in the walks.  Results leave by TMA from shared memory.
 #include "decay_tc.cuh"
 
 namespace gdn {

@@ -38,14 +38,14 @@
 // all runs but the last, then MODE 0 or 2 over all runs at once, each starting from the
 // sum of the runs before it.
 //
-// What bounds it, at 8 x 2048 tokens of 8 heads, dk = dv = 128 (128 chains of 16
-// chunks): MODE 0 takes 51 us, 2.6 TB/s of the bytes it cannot do without.  A chunk takes
-// 4,500 cycles: A, P (2,000 cycles: two warps per scheduler, latency), Y, O, each waiting
-// for the one before, with X and N in between; the tensor pipe is busy for a third of them.
-// With O left to the warps of P alone it took 55 us (5,200 cycles), with O left to the
-// state's 53 us.  MODE 2 takes 33 us forwards and 44 us backwards: 2,500 and 3,700
-// cycles, of which the copies of 80 KB (forwards 48 KB and the 32 KB image out, backwards
-// the forward image as well) at the 26 bytes per cycle that an SM gets from HBM are most.
+// What bounds it, at 8 x 2048 tokens of 8 heads, dk = dv = 128 (128 CTAs of 16 chunks):
+// MODE 0 takes 53 us, 2.6 TB/s of the bytes it cannot do without, 3.3 us a chunk: A, P (two
+// warps per scheduler, latency), Y, O, each waiting for the one before, with X and N in
+// between; the tensor pipe is busy for a third of it.  With O left to the warps of P alone
+// it took 55 us, with O left to the state's 53 us.  MODE 2 takes 33 us forwards and 40 us
+// backwards, 135 and 202 MB to and from HBM (K, V and the states out, backwards the forward
+// states as well; the two CTAs of a head share K through L2): 4.1 and 5.0 TB/s, 62 and 77 %
+// of the measured rate.
 #include <math.h>
 
 #include <algorithm>
@@ -776,8 +776,9 @@ void launch_runs(const Params& a, const Problem& p, cudaStream_t st) {
 }  // namespace
 
 // The dims that fill whole 64-channel panels; the products of smaller ones would be
-// padding for the most part.  (16 heads of 8192 tokens, 128 x 128: 81 us here and 767 us
-// on CUDA cores; the 350M-scale training step 232 us and 2.9 ms.)
+// padding for the most part.  (16 heads of 8192 tokens, 128 x 128: 84 us here and 767 us
+// on CUDA cores; the 350M-scale training step 258 us and 2.9 ms.  Of few tokens too: 4 tokens
+// of 8 heads, 128 x 128, 21 us and 26 us, their backward 42 and 75; 64 x 64, 21 and 22.)
 bool tc_supported(const Problem& p) {
     return p.dtype == GDN_BF16 && (p.dk == 64 || p.dk == 128) && (p.dv == 64 || p.dv == 128);
 }

@@ -68,7 +68,7 @@ GDN_DEV int parent_of(const int* parent, int i, unsigned int* status) {
 // the weights, and their sums, are just that much larger.  Keys and values arrive
 // by TMA, page by page, through a three-stage ring.
 // What bounds it is the HBM read of the cached keys and values: 32 sequences of up to
-// 8192 tokens, 32 nodes, 16 query and 4 key heads of 128 channels take 89 us, 4.1 TB/s of
+// 8192 tokens, 32 nodes, 16 query and 4 key heads of 128 channels take 90 us, 4.0 TB/s of
 // the 360 MB, of which the steps are 63 us; the rest is the start, the last partial
 // results and their joins.
 constexpr int KT = 128;              // keys per tile
