@@ -113,6 +113,14 @@ void launch_simt_bwd(const Problem& p, const void* q, const void* k, const void*
 // dq or dk of shared key heads: [token][H][d] fp32 summed over each group into [token][Hk][d].
 void launch_group_sum(const Problem& p, const float* part_q, const float* part_k, void* dq, void* dk, cudaStream_t st);
 
+// Sequences of up to 64 tokens, packed ones on average: the tensor-core kernels then keep
+// what rounding the pair products of such chunks leaves.  The code for it costs a long call
+// (350M-scale forward 53 -> 61 us, local gradients 128 -> 138), a short one little (256
+// sequences of 16 tokens, 8 heads, 128 x 128: 214 -> 227 us, their backward 559 -> 574).
+inline bool short_sequences(const Problem& p) {
+    return (p.seq.cu ? (long long)p.seq.rows : (long long)p.seq.len * p.seq.nseq) <= 64ll * p.seq.nseq;
+}
+
 // Tensor cores: bf16 with dk, dv in {64, 128} (decay_walk.cu).  The launchers return
 // false if a tensor map could not be encoded (nothing launched).
 bool tc_supported(const Problem& p);

@@ -14,7 +14,10 @@
 // every pair of tokens before t and from t on, within the chunk, across its start,
 // across its end, and over it.  dg is fp32, so M is taken from fp32 accumulators, and S
 // and dS enter the products behind a and b as three bf16 terms, exact to fp32 (dv takes two
-// of dS); D .* dO V^T and D .* Q K^T are rounded to bf16 once, as dq, dk and dv themselves are.
+// of dS); D .* dO V^T and D .* Q K^T are rounded to bf16 once, as dq, dk and dv themselves
+// are.  With SHORT, in a chunk of up to 64 tokens, where few roundings average out, the other
+// half of these operands holds what the rounding left, over the same rows of K, Q and dO
+// once more.
 //
 // One CTA per SM takes the chunk-heads in turn.  A chunk runs in two halves, the
 // first with the query token on the tensor-memory lanes, the second with the key
@@ -128,7 +131,7 @@ GDN_DEV void store_rows(__nv_bfloat16* row0, size_t next, const uint32_t (&w)[NW
 // K Q^T and V dO^T (their bf16 operands over them), dk, dv.
 constexpr uint32_t TA = 0, TB = 128, TX = 256, TP = 384, TV = 384;
 
-template <int DK, int DV>
+template <int DK, int DV, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_bwd_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -180,21 +183,27 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
             const int h = (int)(u % p.H);
             if (!chunk_of_slot(p.seq, u / p.H, ch)) continue;
             const int ph = x & 1, L = ch.L;
+            const bool brief = SHORT && L <= CT / 2;
             const Gates& G = s.gate[ph];
             if (!(ok = warp_wait(&s.t_full, ph)) || !(ok = warp_wait(&s.kv_full, ph))) break;
             if (L < CT) {
                 // rows past the chunk's tokens become zero: the products sum over tokens
+                // (of a short chunk, K, Q and dO have a row again where its rest is: same swizzle)
                 if (i >= L) {
+                    const bool again = brief && i >= CT / 2 && i - CT / 2 < L;
                     const uint4 zero = make_uint4(0, 0, 0, 0);
+                    auto fill = [&](unsigned char* row) {
+                        *reinterpret_cast<uint4*>(row) = again ? *reinterpret_cast<const uint4*>(row - CT / 2 * 128) : zero;
+                    };
 #pragma unroll 1
                     for (int q = qt; q < DK / 8; q += 4) {
-                        *reinterpret_cast<uint4*>(s.Q[q >> 3] + 2 * swz<64>(i, 8 * (q & 7))) = zero;
-                        *reinterpret_cast<uint4*>(s.K[q >> 3] + 2 * swz<64>(i, 8 * (q & 7))) = zero;
+                        fill(s.Q[q >> 3] + 2 * swz<64>(i, 8 * (q & 7)));
+                        fill(s.K[q >> 3] + 2 * swz<64>(i, 8 * (q & 7)));
                     }
 #pragma unroll 1
                     for (int q = qt; q < DV / 8; q += 4) {
                         *reinterpret_cast<uint4*>(s.V[q >> 3] + 2 * swz<64>(i, 8 * (q & 7))) = zero;
-                        *reinterpret_cast<uint4*>(s.Y[q >> 3] + 2 * swz<64>(i, 8 * (q & 7))) = zero;
+                        fill(s.Y[q >> 3] + 2 * swz<64>(i, 8 * (q & 7)));
                     }
                 }
                 fence_async_smem();
@@ -220,9 +229,9 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                 tc5::fence_after();
                 float rs = 0.f;
 #pragma unroll 1
-                for (int z = 0; z < 2; ++z) {
+                for (int z = 0; z < (brief ? 1 : 2); ++z) {
                     const int J = qt + 4 * z, j0 = 16 * J;
-                    uint32_t pk[8];
+                    uint32_t pk[8], rest[8] = {};
                     if (J < 2 * blk + 2) {
                         float A[16], B[16];
                         tc5::ld16(A, trow + TA + j0);
@@ -244,11 +253,16 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(B[2 * e], B[2 * e + 1]);
+                        if (brief) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) rest[e] = rest_bf16(pk[e], B[2 * e], B[2 * e + 1]);
+                        }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) pk[e] = 0;
                     }
                     tc5::st8(trow + TP + 8 * J, pk);
+                    if (brief) tc5::st8(trow + TP + 8 * J + CT / 4, rest);
                     if (z == 0 && !(ok = split_state(0))) break;  // its products run under the rest
                 }
                 if (!ok) break;
@@ -340,7 +354,9 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const int J = qt + 4 * z, t0 = 16 * J;
-                    if (J >= 2 * blk) {
+                    if (brief && z) {
+                        // (made with the first)
+                    } else if (J >= 2 * blk) {
                         float A[16], B[16];
                         tc5::ld16(A, trow + TA + t0);
                         tc5::ld16(B, trow + TB + t0);
@@ -367,9 +383,19 @@ decay_tc_bwd_kernel(const __grid_constant__ Params p) {
                             pa[z][e] = pack_bf16(A[2 * e], A[2 * e + 1]);
                             pb[z][e] = pack_bf16(B[2 * e], B[2 * e + 1]);
                         }
+                        if (z == 0 && brief) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                pa[1][e] = rest_bf16(pa[0][e], A[2 * e], A[2 * e + 1]);
+                                pb[1][e] = rest_bf16(pb[0][e], B[2 * e], B[2 * e + 1]);
+                            }
+                        }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) pa[z][e] = pb[z][e] = 0;
+                        for (int e = 0; e < 8; ++e) {
+                            pa[z][e] = pb[z][e] = 0;
+                            if (z == 0 && brief) pa[1][e] = pb[1][e] = 0;
+                        }
                     }
                 }
                 s.c[ph][qt][i] = cs;
@@ -774,9 +800,10 @@ Layout layout(const Problem& p) {
 template <int DK, int DV>
 void launch(const Params& a, const Problem& p, cudaStream_t st) {
     const int smem = sizeof(Smem<DK, DV>) + 1024;
-    cudaFuncSetAttribute(decay_tc_bwd_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto* kernel = short_sequences(p) ? decay_tc_bwd_kernel<DK, DV, true> : decay_tc_bwd_kernel<DK, DV, false>;
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     const long long units = chunk_slots(p.seq, CT) * p.H;
-    GDN_LAUNCH("decay_tc_bwd", st, (decay_tc_bwd_kernel<DK, DV><<<(unsigned)(units < 148 ? units : 148), kThreads, smem, st>>>(a)));
+    GDN_LAUNCH("decay_tc_bwd", st, (kernel<<<(unsigned)(units < 148 ? units : 148), kThreads, smem, st>>>(a)));
 }
 
 }  // namespace

@@ -90,6 +90,12 @@ GDN_DEV void form_gates(Gates& s, const float (&x)[4]) {
     for (int j = 0; j < 4; ++j) s.G[4 * lane + j] = add2(c[j], before);
 }
 
+// What packing left of x and y, packed.
+GDN_DEV uint32_t rest_bf16(uint32_t packed, float x, float y) {
+    const float2 f = unpack_bf16(packed);
+    return pack_bf16(x - f.x, y - f.y);
+}
+
 // x and y as sums of TERMS bf16 values each (2 terms: to 2^-16, 3: to 2^-24),
 // packed as (x, y) per term.
 template <int TERMS>

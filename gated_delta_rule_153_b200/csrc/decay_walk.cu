@@ -18,7 +18,11 @@
 //
 // Rounding.  Products take bf16 operands and accumulate in fp32.  q, k, v are
 // bf16 already.  P and, for X, the state are rounded to bf16 once: o itself is
-// bf16, and the two errors are of the size of its own rounding.  The decayed V of
+// bf16, and the two errors are of the size of its own rounding.  Where a row of P has few
+// entries, though, its rounding does not average out (o of few tokens was up to 1.8 times
+// its type's rounding off): with SHORT, in a chunk of up to 64 tokens the other half of P
+// holds what the rounding left, over the same V rows once more, for which the products take
+// no longer.  The decayed V of
 // the state is split into three bf16 terms (exact to fp32), because errors there
 // would stay in the state, which is kept and returned in fp32.
 //
@@ -69,6 +73,7 @@ constexpr bool kShare = MODE != 2;
 template <int MODE>
 constexpr int kThreads = 32 * (kEpi + kState + 3 + (MODE == 0 ? 4 : MODE == 2 ? 1 : 0));
 constexpr int NST = 2;
+constexpr int kShort = CT / 2;  // tokens of a chunk that has room for P in two terms
 constexpr int TERMS = 3;  // bf16 terms of the decayed V: exact to fp32
 
 template <int DK, int MODE>
@@ -114,7 +119,7 @@ constexpr uint32_t TA = 0, TP = 128, TX = 192, TY = 256, TN = 320, kCols = 512;
 template <int MODE>
 GDN_DEV uint32_t tn(int c) { return MODE == 0 ? TN : 3 * NB * (c & 1); }
 
-template <int DK, int MODE, bool REV>
+template <int DK, int MODE, bool REV, bool SHORT>
 __global__ void __launch_bounds__(kThreads<MODE>, 1)
 decay_tc_walk_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -183,6 +188,19 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
     auto make = [&](auto& t, int c, int r, int q0, float wt, bool in) {
         constexpr int NP = sizeof(t) / sizeof(t[0]);
         const int st = c % NST;
+        const int left = n - chunk_of(c) * CT;
+        const bool again = SHORT && left <= kShort && r >= kShort && r - kShort < left;
+        // of a short chunk, the piece kShort rows before the one at `at` (the swizzle is the same)
+        auto twice = [&](uint32_t at) {
+            uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at - kShort * 128);
+            uint32_t* const x[4] = {&v.x, &v.y, &v.z, &v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if ((*x[e] & 0x7f80u) == 0x7f80u) *x[e] &= 0xffff0000u;
+                if ((*x[e] & 0x7f800000u) == 0x7f800000u) *x[e] &= 0xffffu;
+            }
+            return v;
+        };
         uint32_t seen = 0;
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
@@ -190,7 +208,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             uint4 v = *reinterpret_cast<const uint4*>(s.st[st].V + at);
             if (!in) {  // rows past the chunk's tokens become zero, in V (for Y) and K too
                 v = make_uint4(0, 0, 0, 0);
-                if (MODE == 0) *reinterpret_cast<uint4*>(s.st[st].V + at) = v;
+                if (MODE == 0) *reinterpret_cast<uint4*>(s.st[st].V + at) = again ? twice(at) : v;
             }
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -340,6 +358,7 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
             for (int c = 0; done == c && c < nc; ++c) {
                 const int st = c % NST;
                 const Gates& G = s.gate[st];
+                const bool brief = SHORT && n - chunk_of(c) * CT <= kShort;
                 if (!warp_wait(&s.a_done, c & 1)) break;
                 tc5::fence_after();
 #pragma unroll 1
@@ -374,11 +393,17 @@ decay_tc_walk_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q) pk[q] = pack_bf16(a[2 * q], a[2 * q + 1]);
                     tc5::st8(tp + 8 * J, pk);
+                    if (brief && J < 4) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) pk[q] = rest_bf16(pk[q], a[2 * q], a[2 * q + 1]);
+                        tc5::st8(tp + 8 * J + 32, pk);
+                    }
                 }
-                {
+                {   // (of a short chunk, rows past its tokens may hold anything)
                     const uint32_t zero[8] = {};
 #pragma unroll 1
-                    for (int J = 2 * blk + 2 + half; J < 8; J += 2) tc5::st8(tp + 8 * J, zero);
+                    for (int J = 2 * blk + 2 + half; J < 8; J += 2)
+                        if (!brief || (J & 3) >= 2 * blk + 2) tc5::st8(tp + 8 * J, zero);
                 }
                 tc5::wait_st();
                 tc5::fence_before();
@@ -734,14 +759,14 @@ Cut cut_of(const Problem& p) {
     return best;
 }
 
-template <int MODE, bool REV>
+template <int MODE, bool REV, bool SHORT = false>
 void launch(const Params& a, int dk, dim3 grid, cudaStream_t st) {
     auto go = [&](auto d) {
         constexpr int DK = decltype(d)::value;
         const int smem = sizeof(Smem<DK, MODE>) + 1024;
-        cudaFuncSetAttribute(decay_tc_walk_kernel<DK, MODE, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(decay_tc_walk_kernel<DK, MODE, REV, SHORT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         GDN_LAUNCH(MODE == 0 ? "decay_tc_walk" : MODE == 1 ? "decay_tc_map" : "decay_tc_states", st,
-                   (decay_tc_walk_kernel<DK, MODE, REV><<<grid, kThreads<MODE>, smem, st>>>(a)));
+                   (decay_tc_walk_kernel<DK, MODE, REV, SHORT><<<grid, kThreads<MODE>, smem, st>>>(a)));
     };
     if (dk == 64) go(std::integral_constant<int, 64>{});
     else go(std::integral_constant<int, 128>{});
@@ -770,7 +795,8 @@ template <int MODE, bool REV>
 void launch_runs(const Params& a, const Problem& p, cudaStream_t st) {
     const auto grid = [&](int runs) { return dim3((unsigned)(items(p.seq, runs, a.len * CT) * p.H), p.dv / NB); };
     if (a.runs > 1) launch<1, REV>(a, p.dk, p.seq.cu ? grid(a.runs) : grid(a.runs - 1), st);
-    launch<MODE, REV>(a, p.dk, grid(a.runs), st);
+    if (MODE == 0 && short_sequences(p)) launch<MODE, REV, MODE == 0>(a, p.dk, grid(a.runs), st);
+    else launch<MODE, REV>(a, p.dk, grid(a.runs), st);
 }
 
 }  // namespace

@@ -346,8 +346,9 @@ gdn_status gdn_recurrent_step(int N, int H, int dk, int dv, gdn_dtype dtype,
  * in fp32 from products exact to fp32, with bf16 inputs too.  dg is summed in fp32,
  * and the states enter it, dq and dk in products exact to fp32.  With bf16 inputs and
  * dk, dv in {64, 128} (tensor cores) o, dq, dk, dv take the decayed pair products in
- * bf16, o the states too, one rounding each (2^-8), and dv the states to 2^-16; all are
- * rounded to `dtype` at the end.
+ * bf16, o the states too, one rounding each (2^-8), and dv the states to 2^-16; in
+ * chunks of up to 64 tokens of calls whose sequences have up to 64 on average the pair
+ * products keep 2^-16.  All are rounded to `dtype` at the end.
  * A value of q, k or v that is not finite makes NaN (also where +-inf would be exact)
  * of what depends on it: its own token and later ones of the sequence, for v in its
  * own channel.  Earlier tokens, other sequences and other key heads, for v other
